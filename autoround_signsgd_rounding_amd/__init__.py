@@ -7,9 +7,11 @@ Entry points mirror include/autoround_hip.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libautoround_hip.so")
@@ -30,7 +32,12 @@ EXPORTS = (
     "ar_tune_linear_gram", "ar_init_clip", "ar_resolve_layer_config", "ar_resolve_fused_config",
     "ar_dequant_gemm_workspace_size", "ar_dequant_gemm", "ar_block_workspace_size",
     "ar_block_forward", "ar_tune_block", "ar_attention", "ar_tune_step_noalloc",
+    "ar_fp8_quant_act", "ar_fp8_quant_weight", "ar_rmsnorm_fp8", "ar_fp8_gemm_workspace_size",
+    "ar_fp8_gemm", "ar_fp8_gemm_grouped_workspace_size", "ar_fp8_gemm_grouped",
 )
+
+# input channels per scale of the e4m3 operands
+FP8_BLOCK = 128
 
 # fixed scratch of ar_tune_step_noalloc per GPU (AR_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -140,6 +147,14 @@ def _load():
         "ar_attention": [ctypes.POINTER(ArBlockDims), vp, vp, vp, vp, vp],
         "ar_tune_block": [cfgp, ctypes.POINTER(ArBlockDims), ctypes.POINTER(ArBlockWeights), vp,
                           vp, i32, ctypes.POINTER(ArBlockOutputs), vp, sz, vp],
+        "ar_fp8_quant_act": [i32, vp, i32, i64, i64, vp, vp, vp],
+        "ar_fp8_quant_weight": [i32, vp, i64, i64, i64, vp, vp, vp],
+        "ar_rmsnorm_fp8": [i32, vp, vp, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp],
+        "ar_fp8_gemm_workspace_size": [i64, i64, i64, ctypes.POINTER(sz)],
+        "ar_fp8_gemm": [vp, vp, i64, i64, vp, vp, i64, vp, i32, vp, sz, vp],
+        "ar_fp8_gemm_grouped_workspace_size": [i64, i64, i64, i64, ctypes.POINTER(sz)],
+        "ar_fp8_gemm_grouped": [vp, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i32, vp, sz,
+                                vp],
         "ar_pack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
         "ar_unpack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
     }
@@ -533,6 +548,196 @@ def unpack(qweight, qzeros, bits: int, N: int, K: int, G: int, stream=None):
     _check(lib.ar_unpack(bits, _ptr(qweight), _ptr(qzeros), N, K, G, _ptr(codes), _ptr(zp),
                          _stream(stream)), "ar_unpack")
     return codes, zp
+
+
+# ------------------------------------------------------------------ e4m3 operands
+def _on(stream, *tensors):
+    """Context in which a call on these tensors allocates and launches: their
+    device, and ``stream`` (its current stream if None). ValueError when the
+    tensors or the stream are on different devices."""
+    torch = _torch()
+    ts = [t for t in tensors if t is not None]
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t.device != dev:
+            raise ValueError(f"tensors must live on one GPU, got {dev} and {t.device}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        if stream != torch.cuda.current_stream(dev):
+            for t in ts:   # the allocator must not hand the memory on before the call ends
+                t.record_stream(stream)
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _fp8_scales(K: int) -> int:
+    return -(-K // FP8_BLOCK)
+
+
+def fp8_quant_act(X, *, gate: bool = False, stream=None):
+    """e4m3 codes [M, K] and scales [ceil(K/128), M] of activations X [M, K]
+    (float32 / bf16), one scale per 128 channels of a row (ar_fp8_quant_act).
+    ``gate``: X is [M, 2K], the gate and the up half side by side, and the codes
+    are those of SiLU(gate)·up."""
+    torch = _torch()
+    M, K = _weight(X, "X")
+    if gate:
+        if K % 2:
+            raise ValueError("gate needs an even number of channels")
+        K //= 2
+    with _on(stream, X):
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+        s = torch.empty((_fp8_scales(K), M), dtype=torch.float32, device=X.device)
+        _check(lib.ar_fp8_quant_act(_dt(X), _ptr(X), int(gate), M, K, _ptr(q), _ptr(s),
+                                    _stream()), "ar_fp8_quant_act")
+    return q, s
+
+
+def fp8_quant_weight(W, *, stream=None):
+    """e4m3 codes and 128 x 128 block scales of a weight [N, K] (scales
+    [ceil(N/128), ceil(K/128)]) or of E experts' weights [E, N, K] (a leading E),
+    float32 / bf16 (ar_fp8_quant_weight)."""
+    torch = _torch()
+    if W is None or W.dim() not in (2, 3):
+        raise ValueError("W must be a [N, K] or [E, N, K] tensor")
+    _need(W, "W", W.shape, (torch.float32, torch.bfloat16))
+    lead, (N, K) = W.shape[:-2], W.shape[-2:]
+    with _on(stream, W):
+        q = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device)
+        s = torch.empty((*lead, _fp8_scales(N), _fp8_scales(K)), dtype=torch.float32,
+                        device=W.device)
+        _check(lib.ar_fp8_quant_weight(_dt(W), _ptr(W), lead[0] if lead else 1, N, K, _ptr(q),
+                                       _ptr(s), _stream()), "ar_fp8_quant_weight")
+    return q, s
+
+
+class NormOutput(NamedTuple):
+    q: object        # e4m3 codes [M, D]
+    scale: object    # [ceil(D/128), M] float32
+    h: object        # x + residual [M, D], or None
+    y: object        # the norm's output [M, D], or None
+
+
+def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = False, h_out=None,
+                stream=None) -> NormOutput:
+    """RMSNorm of x + residual with an e4m3 output (ar_rmsnorm_fp8): x, residual
+    [M, D] and weight [D] all float32 or all bf16. ``h`` is the sum, written to
+    ``h_out`` if given (x or residual themselves may be given: the residual
+    stream is then updated in place); ``want_y`` also returns the norm's output
+    in x's dtype."""
+    torch = _torch()
+    M, D = _weight(x, "x")
+    _need(weight, "weight", (D,), x.dtype)
+    if residual is not None:
+        _need(residual, "residual", (M, D), x.dtype)
+    if h_out is not None:
+        if residual is None:
+            raise ValueError("h_out needs a residual")
+        _need(h_out, "h_out", (M, D), x.dtype)
+    with _on(stream, x, weight, residual, h_out):
+        q = torch.empty((M, D), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((_fp8_scales(D), M), dtype=torch.float32, device=x.device)
+        h = h_out
+        if residual is not None and h is None:
+            h = torch.empty_like(x)
+        y = torch.empty_like(x) if want_y else None
+        _check(lib.ar_rmsnorm_fp8(_dt(x), _ptr(x), _ptr(residual), _ptr(weight), M, D, eps,
+                                  _ptr(h), _ptr(y), _ptr(q), _ptr(s), _stream()),
+               "ar_rmsnorm_fp8")
+    return NormOutput(q, s, h, y)
+
+
+def fp8_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    need = ctypes.c_size_t()
+    _check(lib.ar_fp8_gemm_workspace_size(M, N, K, ctypes.byref(need)),
+           "ar_fp8_gemm_workspace_size")
+    return need.value
+
+
+def fp8_gemm_grouped_workspace_size(E: int, R: int, N: int, K: int) -> int:
+    need = ctypes.c_size_t()
+    _check(lib.ar_fp8_gemm_grouped_workspace_size(E, R, N, K, ctypes.byref(need)),
+           "ar_fp8_gemm_grouped_workspace_size")
+    return need.value
+
+
+def _fp8_operands(Xq, xs, Wq, ws, dims: int):
+    """Shapes of the two operands and their scales, checked."""
+    torch = _torch()
+    f8 = torch.float8_e4m3fn
+    if Xq is None or Xq.dim() != 2:
+        raise ValueError("Xq must be a 2-D [T, K] tensor")
+    if Wq is None or Wq.dim() != dims:
+        raise ValueError("Wq must be a [%sN, K] tensor" % ("E, " if dims == 3 else ""))
+    (T, K), N = Xq.shape, Wq.shape[-2]
+    _need(Xq, "Xq", (T, K), f8)
+    _need(xs, "xs", (_fp8_scales(K), T), torch.float32)
+    _need(Wq, "Wq", (*Wq.shape[:-2], N, K), f8)
+    _need(ws, "ws", (*Wq.shape[:-2], _fp8_scales(N), _fp8_scales(K)), torch.float32)
+    return T, K, N
+
+
+def _fp8_out(out, workspace, R, N, out_dtype, need, device):
+    torch = _torch()
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=device)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return out, workspace, 0 if workspace is None else workspace.numel()
+
+
+def _fp8_given(out, workspace, R, N):
+    torch = _torch()
+    if out is not None:
+        _need(out, "out", (R, N), (torch.float32, torch.bfloat16))
+    if workspace is not None:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8)
+
+
+def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, workspace=None, stream=None):
+    """Y [M, N] (bf16 unless ``out_dtype`` or ``out`` say float32) = X·Wᵀ of e4m3
+    operands with their block scales (ar_fp8_gemm): Xq [M, K], xs [ceil(K/128), M]
+    from fp8_quant_act or rmsnorm_fp8; Wq [N, K], ws from fp8_quant_weight."""
+    M, K, N = _fp8_operands(Xq, xs, Wq, ws, 2)
+    _fp8_given(out, workspace, M, N)
+    with _on(stream, Xq, xs, Wq, ws, out, workspace):
+        Y, wsb, nb = _fp8_out(out, workspace, M, N, out_dtype,
+                              fp8_gemm_workspace_size(M, N, K) if M and N else 0, Xq.device)
+        _check(lib.ar_fp8_gemm(_ptr(Xq), _ptr(xs), M, K, _ptr(Wq), _ptr(ws), N, _ptr(Y), _dt(Y),
+                               _ptr(wsb), nb, _stream()), "ar_fp8_gemm")
+    return Y
+
+
+def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None, out=None,
+                     workspace=None, stream=None):
+    """Y [R, N]: rows offsets[e]..offsets[e+1] are the product with expert e's
+    weight (ar_fp8_gemm_grouped): Wq [E, N, K] and ws from fp8_quant_weight,
+    offsets [E + 1] int32 on the GPU. ``row_index`` [R] int32 names the row of
+    Xq behind each row of Y (None: R = Xq's rows, in order). Rows of Y outside
+    the offsets keep what ``out`` held (without ``out`` they hold nothing
+    meaningful)."""
+    torch = _torch()
+    T, K, N = _fp8_operands(Xq, xs, Wq, ws, 3)
+    E = Wq.shape[0]
+    _need(offsets, "offsets", (E + 1,), torch.int32)
+    R = T
+    if row_index is not None:
+        if row_index.dim() != 1:
+            raise ValueError("row_index must be a 1-D [R] tensor")
+        R = row_index.shape[0]
+        _need(row_index, "row_index", (R,), torch.int32)
+    _fp8_given(out, workspace, R, N)
+    with _on(stream, Xq, xs, Wq, ws, offsets, row_index, out, workspace):
+        Y, wsb, nb = _fp8_out(out, workspace, R, N, out_dtype,
+                              fp8_gemm_grouped_workspace_size(E, R, N, K) if R and N else 0,
+                              Xq.device)
+        _check(lib.ar_fp8_gemm_grouped(_ptr(Xq), _ptr(xs), T, K, _ptr(Wq), _ptr(ws), E, N,
+                                       _ptr(offsets), _ptr(row_index), R, _ptr(Y), _dt(Y),
+                                       _ptr(wsb), nb, _stream()), "ar_fp8_gemm_grouped")
+    return Y
 
 
 # ------------------------------------------------------------------ per-layer config

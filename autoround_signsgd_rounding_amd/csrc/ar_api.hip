@@ -997,6 +997,110 @@ ar_status ar_dequant_gemm(int32_t bits, int32_t group_size, const uint16_t* X, i
   return ar_launch_gemm_out(XB, WB, Y, ydt, M, N, K, st);
 }
 
+// ------------------------------------------------------------------ e4m3 operands
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) / 256;   // one 256-thread workgroup per row
+constexpr int64_t kMaxExperts = 8192;
+inline bool a4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rows of K codes: K a multiple of 16 below kMaxLd.
+ar_status check_fp8_rows(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || M >= kMaxRows) return AR_ERR_SHAPE;
+  return K % 16 == 0 && K < kMaxLd ? AR_OK : AR_ERR_SHAPE;
+}
+
+ar_status check_fp8_gemm(int64_t E, int64_t R, int64_t N, int64_t K) {
+  if (E < 1 || E > kMaxExperts || K == 0) return AR_ERR_SHAPE;
+  AR_TRY(check_fp8_rows(R, K));
+  return N >= 0 && N < kMaxRows ? AR_OK : AR_ERR_SHAPE;
+}
+
+}  // namespace
+
+ar_status ar_fp8_quant_act(int32_t xdt, const void* X, int32_t gate, int64_t M, int64_t K,
+                           uint8_t* q, float* scale, void* stream) {
+  if (!dtype_ok(xdt)) return AR_ERR_UNSUPPORTED;
+  if (gate != 0 && gate != 1) return AR_ERR_INVALID_ARG;
+  AR_TRY(check_fp8_rows(M, K));
+  if (M == 0 || K == 0) return AR_OK;
+  if (!X || !q || !scale || !a16(X) || !a16(q) || !a4(scale)) return AR_ERR_INVALID_ARG;
+  return ar_launch_fp8_quant_act(xdt, X, gate, M, K, q, scale, static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_fp8_quant_weight(int32_t wdt, const void* W, int64_t E, int64_t N, int64_t K,
+                              uint8_t* q, float* scale, void* stream) {
+  if (!dtype_ok(wdt)) return AR_ERR_UNSUPPORTED;
+  if (E < 0) return AR_ERR_SHAPE;
+  AR_TRY(check_fp8_rows(N, K));
+  if (E == 0 || N == 0 || K == 0) return AR_OK;
+  const int64_t blocks = ((N + 127) / 128) * ((K + 127) / 128);
+  if (E > kMaxRows || E * blocks >= kMaxRows * 2) return AR_ERR_SHAPE;   // one workgroup per block
+  if (!W || !q || !scale || !a16(W) || !a16(q) || !a4(scale)) return AR_ERR_INVALID_ARG;
+  return ar_launch_fp8_quant_weight(wdt, W, E, N, K, q, scale, static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const void* w, int64_t M,
+                         int64_t D, float eps, void* h, void* y, uint8_t* q, float* scale,
+                         void* stream) {
+  if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
+  if (!finite(eps) || eps < 0.0f) return AR_ERR_INVALID_ARG;
+  AR_TRY(check_fp8_rows(M, D));
+  if (M == 0 || D == 0) return AR_OK;
+  if (!x || !w || !q || !scale || (h && !residual)) return AR_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, w, (const void*)h, (const void*)y, (const void*)q})
+    if (!a16(p)) return AR_ERR_INVALID_ARG;
+  if (!a4(scale)) return AR_ERR_INVALID_ARG;
+  return ar_launch_rmsnorm_fp8(dt, x, residual, w, M, D, eps, h, y, q, scale,
+                               static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_fp8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return ar_fp8_gemm_grouped_workspace_size(1, M, N, K, bytes);
+}
+
+ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
+                      const float* ws, int64_t N, void* Y, int32_t ydt, void* ws_buf,
+                      size_t ws_bytes, void* stream) {
+  AR_TRY(check_fp8_gemm(1, M, N, K));
+  if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return AR_OK;
+  if (!Xq || !xs || !Wq || !ws || !Y) return AR_ERR_INVALID_ARG;
+  if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a16(Y)) return AR_ERR_INVALID_ARG;
+  (void)ws_buf;
+  (void)ws_bytes;
+  return ar_launch_fp8_gemm(ArFp8Gemm{Xq, xs, Wq, ws, nullptr, nullptr, Y, ydt, M, M, N, K, 1},
+                            static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_fp8_gemm_grouped_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K,
+                                             size_t* bytes) {
+  if (!bytes) return AR_ERR_INVALID_ARG;
+  AR_TRY(check_fp8_gemm(E, R, N, K));
+  *bytes = 0;
+  return AR_OK;
+}
+
+ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int64_t K,
+                              const uint8_t* Wq, const float* ws, int64_t E, int64_t N,
+                              const int32_t* offsets, const int32_t* row_index, int64_t R, void* Y,
+                              int32_t ydt, void* ws_buf, size_t ws_bytes, void* stream) {
+  AR_TRY(check_fp8_gemm(E, R, N, K));
+  AR_TRY(check_fp8_rows(T, K));
+  if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
+  if (R == 0 || N == 0) return AR_OK;
+  if (row_index ? T * K >= (int64_t(1) << 32) : T != R) return AR_ERR_SHAPE;
+  if (T == 0) return AR_ERR_SHAPE;   // an index needs a row to point at
+  if (!Xq || !xs || !Wq || !ws || !offsets || !Y) return AR_ERR_INVALID_ARG;
+  if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a4(offsets) || !a4(row_index) || !a16(Y))
+    return AR_ERR_INVALID_ARG;
+  (void)ws_buf;
+  (void)ws_bytes;
+  return ar_launch_fp8_gemm(
+      ArFp8Gemm{Xq, xs, Wq, ws, offsets, row_index, Y, ydt, T, R, N, K, E},
+      static_cast<hipStream_t>(stream));
+}
+
 ar_status ar_pack(int32_t bits, const uint8_t* codes, const uint8_t* zp, int64_t N, int64_t K,
                   int64_t G, int32_t* qweight, int32_t* qzeros, void* stream) {
   if (!(bits == 2 || bits == 3 || bits == 4 || bits == 8)) return AR_ERR_UNSUPPORTED;

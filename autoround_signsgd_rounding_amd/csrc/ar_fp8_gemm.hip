@@ -1,0 +1,535 @@
+// Block-scaled e4m3 product, dense and by expert (gfx950):
+//   Y[r, n] = sum over blocks j of 128 k:
+//             xs[j, row(r)] · ws[e, n/128, j] · sum_{k in j} X[row(r), k]·W[e, n, k]
+// with X [T, K], W [E, N, K] e4m3 row-major, xs [KB, T] and ws [E, NB, KB]
+// float32 (ar_fp8.hip writes both). The rows offsets[e] <= r < offsets[e + 1]
+// of Y are expert e's; row(r) = r or row_index[r]. The dense product is the
+// case E = 1 with all rows.
+//
+// The inner sum of one block comes from the matrix unit, from a zero
+// accumulator, and joins a float32 accumulator with one fma by the product of the
+// two scales.
+// W is the A operand and X the B operand, so a lane holds four neighbouring
+// n of one row r: the row's scale is one value per lane, W's scale is one
+// value for a whole wave, and Y is stored four values at a time. A and B use
+// one assignment of k to lanes (32 consecutive bytes per lane: K is summed
+// over, so any will do).
+#include "ar_device.h"
+#include "ar_launch.h"
+
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int BLK = 128;
+
+inline ar_status last_status() { return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP; }
+
+struct Args {
+  const uint8_t* X;
+  const float* xs;
+  const uint8_t* W;
+  const float* ws;
+  const int32_t* off;   // [E + 1], NULL: one expert with all R rows
+  const int32_t* idx;   // [R], NULL: row r of X
+  void* Y;
+  int ydt;
+  int64_t T, R, N, K;
+  int E, NB, KB;
+};
+
+// Tile t of the rows cut into tiles of TM within each expert: expert e, first
+// row r0 and row count (0: there is no such tile). Offsets are clamped to
+// [0, R], so no table of offsets leads outside the arrays. The whole wave
+// calls it; 64 experts are scanned at a time.
+template <int TM>
+__device__ __forceinline__ void find_tile(const Args& a, int t, int& e, int64_t& r0, int& rows) {
+  e = 0;
+  rows = 0;
+  r0 = 0;
+  if (!a.off) {
+    r0 = (int64_t)t * TM;
+    rows = (int)(a.R - r0 < TM ? a.R - r0 : TM);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    const int ee = base + lane;
+    int lo = 0, hi = 0;
+    if (ee < a.E) {
+      const int R = (int)a.R;
+      lo = min(max(a.off[ee], 0), R);
+      hi = min(max(a.off[ee + 1], lo), R);
+    }
+    const int tiles = (hi - lo + TM - 1) / TM;
+    int sum = tiles;   // inclusive scan over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(before + sum > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int first = before + __shfl(sum, l, 64) - __shfl(tiles, l, 64);
+      const int elo = __shfl(lo, l, 64), ehi = __shfl(hi, l, 64);
+      e = __builtin_amdgcn_readfirstlane(base + l);
+      const int at = __builtin_amdgcn_readfirstlane(elo + (t - first) * TM);
+      r0 = at;
+      rows = min(__builtin_amdgcn_readfirstlane(ehi) - at, TM);
+      return;
+    }
+    before += __shfl(sum, 63, 64);
+  }
+}
+
+__device__ __forceinline__ void store_y(const Args& a, int64_t r, int64_t n, const float (&v)[4]) {
+  if (a.ydt == AR_BF16) {
+    uint16_t* y = static_cast<uint16_t*>(a.Y) + r * a.N + n;
+    if (n + 3 < a.N && a.N % 4 == 0) {
+      *reinterpret_cast<u32x2_t*>(y) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) y[i] = (uint16_t)bf16_bits(v[i]);
+    }
+  } else {
+    float* y = static_cast<float*>(a.Y) + r * a.N + n;
+    if (n + 3 < a.N && a.N % 4 == 0) {
+      *reinterpret_cast<f32x4_t*>(y) = f32x4_t{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) y[i] = v[i];
+    }
+  }
+}
+
+// One block's products. A fragment is 32 codes of one row; the unscaled
+// v_mfma_f32_16x16x128_f8f6f4 (scale operands 0) multiplies two of them at twice
+// the bf16 rate, but adds its 128 products to about 16 bits: measured 1.3e-5 to
+// 3.7e-5 of the sum's size, a hundredth of the half step of a bf16 output
+// (2^-9 on average). For a float32 output that would be the largest error by far,
+// so there the codes are widened to bf16 (exact) and multiplied by
+// v_mfma_f32_16x16x32_bf16 (1e-8, measured), at half the rate.
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+struct WideFrag {
+  bf16x8_t v[4];
+};
+template <bool WIDE>
+struct FragOf {
+  typedef i32x8_t type;
+  static __device__ __forceinline__ type of(const i32x8_t& x) { return x; }
+  static __device__ __forceinline__ f32x4_t mul(const type& w, const type& x) {
+    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
+  }
+};
+template <>
+struct FragOf<true> {
+  typedef WideFrag type;
+  static __device__ __forceinline__ type of(const i32x8_t& x) {
+    WideFrag f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t d = (uint32_t)x[2 * c + h];
+        const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false);
+        const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true);
+        f.v[c][4 * h] = lo[0];
+        f.v[c][4 * h + 1] = lo[1];
+        f.v[c][4 * h + 2] = hi[0];
+        f.v[c][4 * h + 3] = hi[1];
+      }
+    return f;
+  }
+  static __device__ __forceinline__ f32x4_t mul(const type& w, const type& x) {
+    f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[c], x.v[c], d, 0, 0, 0);
+    return d;
+  }
+};
+
+// 32 bytes at p (16-byte aligned); `left` bytes of the row remain from p on:
+// 16-byte halves past the row are zero (K % 16 == 0).
+__device__ __forceinline__ i32x8_t frag(const uint8_t* p) {
+  const i32x4_t a = reinterpret_cast<const i32x4_t*>(p)[0];
+  const i32x4_t b = reinterpret_cast<const i32x4_t*>(p)[1];
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ i32x8_t frag_tail(const uint8_t* p, int left) {
+  i32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+  if (left > 0) a = reinterpret_cast<const i32x4_t*>(p)[0];
+  if (left > 16) b = reinterpret_cast<const i32x4_t*>(p)[1];
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Row of X behind row r of Y; -1 when row_index names none (its row of Y is zero).
+__device__ __forceinline__ int64_t x_row(const Args& a, int64_t r) {
+  if (!a.idx) return r;
+  const int i = a.idx[r];
+  return i >= 0 && i < a.T ? i : -1;
+}
+
+// ------------------------------------------------------------------ few rows
+// Operands straight from memory to registers. A workgroup of 8 waves makes a
+// tile of 16 n by 16·MT rows; the waves take the blocks of K in turn (wave w:
+// blocks w, w + 8, ...) and their sums are added through LDS in wave order.
+constexpr int DW = 8;
+
+template <int MT, bool WIDE>
+__global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
+  typedef FragOf<WIDE> Op;
+  constexpr int TM = 16 * MT;
+  __shared__ float red[DW][MT][64][4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int e, rows;
+  int64_t r0;
+  find_tile<TM>(a, blockIdx.y, e, r0, rows);
+  if (rows <= 0) return;
+  const int l16 = lane & 15, kc = 32 * (lane >> 4);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n = n0 + l16 < a.N ? n0 + l16 : a.N - 1;
+  const uint8_t* wp = a.W + ((int64_t)e * a.N + n) * a.K + kc;
+  const float* wsp = a.ws + ((int64_t)e * a.NB + n0 / BLK) * a.KB;
+  const uint8_t* xp[MT];
+  const float* xsp[MT];
+  bool live[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = 16 * t + l16;
+    const int64_t x = x_row(a, r0 + (m < rows ? m : rows - 1));
+    live[t] = x >= 0;
+    xp[t] = a.X + (x < 0 ? 0 : x) * a.K + kc;
+    xsp[t] = a.xs + (x < 0 ? 0 : x);
+  }
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int full = (int)(a.K / BLK);
+  auto add = [&](int j, const i32x8_t& w, const i32x8_t (&x)[MT]) {
+    const float sw = wsp[j];
+    const typename Op::type wf = Op::of(w);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float s = sw * xsp[t][(int64_t)j * a.T];
+      const f32x4_t p = Op::mul(wf, Op::of(x[t]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], s, acc[t][i]);
+    }
+  };
+  for (int j = wave; j < full; j += DW) {
+    const i32x8_t w = frag(wp + (int64_t)j * BLK);
+    i32x8_t x[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) x[t] = frag(xp[t] + (int64_t)j * BLK);
+    add(j, w, x);
+  }
+  if (full < a.KB && full % DW == wave) {
+    const int left = (int)(a.K - (int64_t)full * BLK) - kc;
+    const i32x8_t w = frag_tail(wp + (int64_t)full * BLK, left);
+    i32x8_t x[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) x[t] = frag_tail(xp[t] + (int64_t)full * BLK, left);
+    add(full, w, x);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+    *reinterpret_cast<f32x4_t*>(red[wave][t][lane]) = acc[t];
+  __syncthreads();
+  if (wave < MT) {
+    const int t = wave;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < DW; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += red[w][t][lane][i];
+    const int m = 16 * t + l16;
+    bool ok = false;
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+      if (u == t) ok = live[u];
+    if (!ok) v[0] = v[1] = v[2] = v[3] = 0.0f;
+    if (m < rows) store_y(a, r0 + m, n0 + 4 * (lane >> 4), v);
+  }
+}
+
+// ------------------------------------------------------------------ many rows
+// Tiles of TM = 16·MB·WM rows by TN = 16·NA·WN columns, one wave per 16·MB x 16·NA
+// part. A step is one block of 128 k: W's and X's rows of the tile (128 bytes
+// each) and X's scales go straight from memory to LDS, two stages of them. In
+// LDS, 16-byte chunk c of row r sits at chunk c ^ ((r >> 1) & 7), so that the 16
+// rows a fragment read touches with one chunk number lie in 16 different
+// 16-byte slots of a 256-byte LDS cycle.
+//
+// A wave keeps its MB X fragments of the step and streams its NA W fragments
+// past them, two ahead. When the last of them is in registers, the wave waits
+// for the next stage's loads (a whole step old by then) and the workgroup meets;
+// the loads of the step after the next go into the stage just left, and the next
+// stage's fragments are read while the last W fragment's products run.
+template <int WM, int WN, int MB, int NA>
+struct Tile {
+  static constexpr int TM = 16 * MB * WM, TN = 16 * NA * WN, NW = WM * WN;
+  static constexpr int W_BYTES = TN * BLK, X_BYTES = TM * BLK;
+  static constexpr int STAGE = W_BYTES + X_BYTES + TM * 4;
+  static constexpr int IW = TN / 8 / NW, IX = TM / 8 / NW;   // 1 KiB loads per wave and operand
+};
+constexpr uint32_t kNone = 0xFFFFFFF0u;   // past every buffer: the load writes zeros
+
+// Workgroup -> (m tile, n tile). The dispatcher places workgroup w on XCD w mod 8:
+// each XCD gets one contiguous range of the tile sequence, walked in groups of
+// GI tile rows, so the tiles that run on one XCD at a time share operands in its
+// L2.
+__device__ __forceinline__ void tile_of(int w, int n, int tilesM, int tilesN, int& tm, int& tn) {
+  constexpr int GI = 4;
+  const int xcd = w & 7, q = n >> 3, r = n & 7;
+  const int L = xcd * q + min(xcd, r) + (w >> 3);
+  const int g = L / (GI * tilesN), first = g * GI;
+  const int size = min(tilesM - first, GI), in = L - g * GI * tilesN;
+  tm = first + in % size;
+  tn = in / size;
+}
+
+// Tiles of TM rows in all ranges (the dense product: of all rows).
+template <int TM>
+__device__ __forceinline__ int count_tiles(const Args& a) {
+  if (!a.off) return (int)((a.R + TM - 1) / TM);
+  int n = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    const int e = base + (threadIdx.x & 63);
+    if (e < a.E) {
+      const int R = (int)a.R, lo = min(max(a.off[e], 0), R);
+      n += (min(max(a.off[e + 1], lo), R) - lo + TM - 1) / TM;
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+template <int WM, int WN, int MB, int NA, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN) {
+  typedef Tile<WM, WN, MB, NA> C;
+  typedef FragOf<WIDE> Op;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int tilesM = count_tiles<C::TM>(a);
+  if ((int)blockIdx.x >= tilesM * tilesN) return;   // more workgroups than tiles: ragged ranges
+  int tm, tn, e, rows;
+  int64_t r0;
+  tile_of(blockIdx.x, tilesM * tilesN, tilesM, tilesN, tm, tn);
+  find_tile<C::TM>(a, tm, e, r0, rows);
+  if (rows <= 0) return;
+  const int64_t n0 = (int64_t)tn * C::TN;
+  const uint32_t K = (uint32_t)a.K;
+  const int KB = a.KB;
+
+  // Loads: piece i of an operand is rows 8·(wave·I + i) .. + 7 of its tile, eight
+  // lanes of 16 bytes a row; chunk[] is the lane's k offset within the block.
+  const int cols = (int)(a.N - n0 < C::TN ? a.N - n0 : C::TN);
+  const __amdgpu_buffer_rsrc_t bw =
+      make_rsrc(a.W + ((int64_t)e * a.N + n0) * a.K, (uint32_t)cols * K);
+  const __amdgpu_buffer_rsrc_t bx =
+      a.idx ? make_rsrc(a.X, (uint32_t)((uint64_t)a.T * K))
+            : make_rsrc(a.X + r0 * a.K, (uint32_t)rows * K);
+  auto chunk = [&](int r) { return (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) * 16); };
+  uint32_t vw[C::IW], vx[C::IX];
+#pragma unroll
+  for (int i = 0; i < C::IW; ++i) {
+    const int r = 8 * (wave * C::IW + i) + (lane >> 3);
+    vw[i] = r < cols ? (uint32_t)r * K + chunk(r) : kNone;
+  }
+#pragma unroll
+  for (int i = 0; i < C::IX; ++i) {
+    const int r = 8 * (wave * C::IX + i) + (lane >> 3);
+    int64_t x = -1;
+    if (r < rows) x = a.idx ? x_row(a, r0 + r) : r;
+    vx[i] = x >= 0 ? (uint32_t)x * K + chunk(r) : kNone;
+  }
+  // scales: 64 rows per wave, four bytes a lane
+  const int sr = 64 * (wave % (C::TM / 64)) + lane;
+  uint32_t vs = kNone;
+  if (sr < rows) {
+    const int64_t x = a.idx ? x_row(a, r0 + sr) : sr;
+    if (x >= 0) vs = (uint32_t)x * 4u;
+  }
+  const float* xs = a.xs + (a.idx ? 0 : r0);
+  const uint32_t xs_bytes = (uint32_t)(a.idx ? a.T : rows) * 4u;
+#define AR_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+  // Past the last block (and in its missing chunks) the loads write zeros, so the
+  // loop needs no branch around them.
+  auto issue = [&](int kt) {
+    uint8_t* st = lds + (kt & 1) * C::STAGE;
+    const uint32_t so = (uint32_t)kt * BLK;
+    const bool tail = so + BLK > K;
+#pragma unroll
+    for (int i = 0; i < C::IW; ++i) {
+      const int r = 8 * (wave * C::IW + i) + (lane >> 3);
+      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vw[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, AR_LDS(st + (wave * C::IW + i) * 1024), 16, v,
+                                               so, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < C::IX; ++i) {
+      const int r = 8 * (wave * C::IX + i) + (lane >> 3);
+      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vx[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          bx, AR_LDS(st + C::W_BYTES + (wave * C::IX + i) * 1024), 16, v, so, 0, 0);
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        make_rsrc(xs + (int64_t)kt * a.T, xs_bytes),
+        AR_LDS(st + C::W_BYTES + C::X_BYTES + (wave % (C::TM / 64)) * 256), 4,
+        kt < KB ? vs : kNone, 0, 0, 0);
+  };
+#undef AR_LDS
+
+  // Fragments: lane l reads row l % 16, chunks 2·(l / 16) and the next.
+  const int l16 = lane & 15, q = lane >> 4;
+  const uint32_t slot = (uint32_t)(((2 * q) ^ (l16 >> 1)) * 16);
+  const uint32_t aw = (uint32_t)(wn * NA * 16 + l16) * BLK + slot;
+  const uint32_t ax = (uint32_t)C::W_BYTES + (uint32_t)(wm * MB * 16 + l16) * BLK + slot;
+  const uint32_t as = (uint32_t)(C::W_BYTES + C::X_BYTES) + (uint32_t)(wm * MB * 16 + l16) * 4;
+  auto rd = [&](int kt, uint32_t at) {
+    const uint8_t* st = lds + (kt & 1) * C::STAGE;
+    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(st + at);
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(st + (at ^ 16u));
+    return Op::of(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+  // W's scales of this wave's columns (one block of 128), 64 blocks of K at a time
+  const int64_t nb = (n0 + wn * NA * 16) / BLK;
+  const float* wsp = a.ws + ((int64_t)e * a.NB + (nb < a.NB ? nb : a.NB - 1)) * KB;
+  float wsv = 0.0f;
+
+  f32x4_t acc[NA][MB];
+#pragma unroll
+  for (int t = 0; t < NA; ++t)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[t][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto arrive = [&]() {   // this wave's loads are in LDS and its reads done; then everyone's
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+  };
+  issue(0);
+  arrive();
+  issue(1);
+  typename Op::type fx[MB], fw[2];
+  float sx[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    fx[b] = rd(0, ax + b * 16 * BLK);
+    sx[b] = *reinterpret_cast<const float*>(lds + as + b * 64);
+  }
+  fw[0] = rd(0, aw);
+  fw[1] = rd(0, aw + 16 * BLK);
+
+  auto step = [&](int kt) {
+    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), kt & 63));
+    float s[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) s[b] = sw * sx[b];
+    // products three items behind the matrix unit's issue join the accumulators
+    f32x4_t p[4];
+    auto join = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[u / MB][u % MB][i] = fmaf(p[u % 4][i], s[u % MB], acc[u / MB][u % MB][i]);
+    };
+#pragma unroll
+    for (int u = 0; u < NA * MB; ++u) {
+      const int t = u / MB, b = u % MB;
+      if (u == (NA - 1) * MB) {
+        arrive();
+        issue(kt + 2);
+      }
+      p[u % 4] = Op::mul(fw[t & 1], fx[b]);
+      if (t == NA - 1) {   // the next step's fragments replace these
+        fx[b] = rd(kt + 1, ax + b * 16 * BLK);
+        sx[b] = *reinterpret_cast<const float*>(lds + ((kt + 1) & 1) * C::STAGE + as + b * 64);
+        if (b == 0) fw[t & 1 ^ 1] = rd(kt + 1, aw);
+        if (b == MB - 1) fw[t & 1] = rd(kt + 1, aw + 16 * BLK);
+      } else if (b == MB - 1 && t + 2 < NA) {
+        fw[t & 1] = rd(kt, aw + (t + 2) * 16 * BLK);
+      }
+      if (u >= 3) join(u - 3);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int u = NA * MB - 3; u < NA * MB; ++u) join(u);
+  };
+  for (int k0 = 0; k0 < KB; k0 += 64) {
+    float v = k0 + lane < KB ? wsp[k0 + lane] : 0.0f;
+    asm volatile("" : "+v"(v));   // waits for it here, not in every step
+    wsv = v;
+    const int k1 = min(k0 + 64, KB);
+    for (int kt = k0; kt < k1; ++kt) step(kt);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load may land in LDS after the end
+
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int m = wm * MB * 16 + 16 * b + l16;
+    if (m < rows) {
+#pragma unroll
+      for (int t = 0; t < NA; ++t) {
+        const float v[4] = {acc[t][b][0], acc[t][b][1], acc[t][b][2], acc[t][b][3]};
+        store_y(a, r0 + m, n0 + wn * NA * 16 + 16 * t + 4 * q, v);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Tiles of TM rows that R rows in E ranges can need at most.
+static int64_t max_tiles(int64_t R, int64_t E, int64_t TM) {
+  const int64_t t = R / TM + E;   // every range adds at most one ragged tile
+  return t < R ? t : R;
+}
+
+template <int WM, int WN, int MB, int NA, bool WIDE>
+static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
+  typedef Tile<WM, WN, MB, NA> C;
+  static_assert(2 * C::STAGE <= 160 * 1024, "LDS of one workgroup");
+  const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
+  if (tilesM * tilesN >= (int64_t(1) << 22)) return AR_ERR_SHAPE;
+  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, WIDE>);
+  if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * C::STAGE) != hipSuccess)
+    return AR_ERR_HIP;
+  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, WIDE>), dim3((unsigned)(tilesM * tilesN)),
+                     dim3(64 * WM * WN), 2 * C::STAGE, st, a, (int)tilesN);
+  return last_status();
+}
+
+template <int MT>
+static ar_status rows_launch(const Args& a, int64_t tilesM, hipStream_t st) {
+  const dim3 g((unsigned)((a.N + 15) / 16), (unsigned)tilesM);
+  if (a.ydt == AR_BF16)
+    hipLaunchKernelGGL((k_fp8_rows<MT, false>), g, dim3(64 * DW), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_fp8_rows<MT, true>), g, dim3(64 * DW), 0, st, a);
+  return last_status();
+}
+
+ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
+  Args a{g.X, g.xs, g.W, g.ws, g.offsets, g.row_index, g.Y, g.ydt, g.T, g.R, g.N, g.K, (int)g.E,
+         (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
+  const int64_t mean = (g.R + g.E - 1) / g.E;
+  auto tiles = [&](int64_t TM) {
+    return g.offsets ? max_tiles(g.R, g.E, TM) : (g.R + TM - 1) / TM;
+  };
+  if (mean <= 16) return rows_launch<1>(a, tiles(16), st);
+  if (mean <= 64) return rows_launch<4>(a, tiles(64), st);
+  if (g.ydt == AR_F32) return tile_launch<2, 2, 4, 4, true>(a, tiles(128), st);
+  if (tiles(256) * ((g.N + 255) / 256) >= 256) return tile_launch<4, 2, 4, 8, false>(a, tiles(256), st);
+  return tile_launch<2, 2, 4, 4, false>(a, tiles(128), st);
+}

@@ -199,3 +199,32 @@ ar_status ar_launch_pack(int bits, const uint8_t* codes, const uint8_t* zp, int6
                          int64_t G, int32_t* qweight, int32_t* qzeros, hipStream_t st);
 ar_status ar_launch_unpack(int bits, const int32_t* qweight, const int32_t* qzeros, int64_t N,
                            int64_t K, int64_t G, uint8_t* codes, uint8_t* zp, hipStream_t st);
+
+// e4m3 operands (ar_fp8.hip). K and D are multiples of 16. Activations: X
+// [M, K] (gate: [M, 2K], SiLU of the first half times the second) -> q [M, K],
+// scale [KB, M]; weights: W [E, N, K] -> q, scale [E, NB, KB]; KB = ceil(K/128).
+ar_status ar_launch_fp8_quant_act(int xdt, const void* X, int gate, int64_t M, int64_t K,
+                                  uint8_t* q, float* scale, hipStream_t st);
+ar_status ar_launch_fp8_quant_weight(int wdt, const void* W, int64_t E, int64_t N, int64_t K,
+                                     uint8_t* q, float* scale, hipStream_t st);
+// RMSNorm of x + res (res nullable) -> q [M, D], scale [KB, M]; h (the sum) and
+// y (the norm's output) nullable, of x's dtype.
+ar_status ar_launch_rmsnorm_fp8(int dt, const void* x, const void* res, const void* w, int64_t M,
+                                int64_t D, float eps, void* h, void* y, uint8_t* q, float* scale,
+                                hipStream_t st);
+
+// Block-scaled e4m3 product (ar_fp8_gemm.hip): Y [R, N] from X [T, K] and
+// W [E, N, K]; offsets [E + 1] NULL for one expert with all R rows, row_index
+// [R] NULL for row r of X.
+struct ArFp8Gemm {
+  const uint8_t* X;
+  const float* xs;
+  const uint8_t* W;
+  const float* ws;
+  const int32_t* offsets;
+  const int32_t* row_index;
+  void* Y;
+  int ydt;
+  int64_t T, R, N, K, E;
+};
+ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st);

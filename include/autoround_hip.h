@@ -243,6 +243,74 @@ ar_status ar_dequant_gemm(int32_t bits, int32_t group_size, const uint16_t* X, i
                           const float* scale, int64_t N, void* Y, int32_t ydt, void* ws,
                           size_t ws_bytes, void* stream);
 
+/* ---- e4m3 operands and their product ---------------------------------------
+   The 8-bit-float path of a decoder layer: both sides of a Linear in e4m3 (the
+   OCP format: no infinities, largest value 448) with float32 scales per block of
+   128 input channels. ar_fp8_quant_weight stands beside ar_rtn_quant,
+   ar_rmsnorm_fp8 beside the block's RMSNorm, ar_fp8_gemm and
+   ar_fp8_gemm_grouped beside ar_dequant_gemm. Codes are passed as uint8 bit
+   patterns. KB = ceil(K/128) and NB = ceil(N/128); K (and D) must be a multiple
+   of 16, and a last block may be shorter than 128. Scale and index arrays need
+   4-byte alignment only.
+
+   Scale of a block: s = 1 if its largest magnitude amax is 0, else
+   max(amax/448, 2^-126); code = e4m3(x·(1/s)), round to nearest even, float32
+   steps. A NaN gives a NaN code and does not enter amax. An infinity makes s
+   infinite and its own code NaN, and with s every product of the block NaN. */
+
+/* Activations: q [M, K], scale [KB, M] (one row of scales per block of 128
+   channels). gate = 0: the codes of X [M, K]. gate = 1: X is [M, 2K] and the
+   codes are those of SiLU(X[:, :K])·X[:, K:], computed in float32 and not rounded
+   before. xdt: AR_F32 or AR_BF16. M*K = 0 is a no-op. */
+ar_status ar_fp8_quant_act(int32_t xdt, const void* X, int32_t gate, int64_t M, int64_t K,
+                           uint8_t* q, float* scale, void* stream);
+
+/* Weights of E layers (E = 1: one Linear; more: the experts of a fused layer):
+   W [E, N, K] -> q [E, N, K], scale [E, NB, KB], one scale per 128 x 128 block.
+   E*N*K = 0 is a no-op. */
+ar_status ar_fp8_quant_weight(int32_t wdt, const void* W, int64_t E, int64_t N, int64_t K,
+                              uint8_t* q, float* scale, void* stream);
+
+/* RMSNorm with the residual's addition and an e4m3 output: v = x + residual
+   rounded to dt (residual NULL: v = x), y = (v / sqrt(mean(v²) + eps))·w (sum of
+   squares in float64, y in float32), q [D per row] and scale [KB, M] of the
+   unrounded y as ar_fp8_quant_act forms them. x, residual [M, D] and w [D] of
+   dtype dt (AR_F32 or AR_BF16). h [M, D] dt: v (nullable, needs residual; may be
+   x or residual itself, for a residual stream kept in place). y [M, D] dt: the
+   norm's output rounded (nullable). eps >= 0 and finite. M*D = 0 is a no-op. */
+ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const void* w, int64_t M,
+                         int64_t D, float eps, void* h, void* y, uint8_t* q, float* scale,
+                         void* stream);
+
+/* Y [M, N] = Σ_j xs[j, m]·ws[n/128, j]·Σ_{k in block j} Xq[m, k]·Wq[n, k]: Xq
+   [M, K] with xs [KB, M] (ar_fp8_quant_act or ar_rmsnorm_fp8), Wq [N, K] with ws
+   [NB, KB] (ar_fp8_quant_weight, E = 1). float32 accumulation, in a fixed order;
+   ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE. ws_buf:
+   ar_fp8_gemm_workspace_size bytes (may be 0: NULL then). */
+ar_status ar_fp8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
+                      const float* ws, int64_t N, void* Y, int32_t ydt, void* ws_buf,
+                      size_t ws_bytes, void* stream);
+
+/* The product by expert: rows offsets[e] <= r < offsets[e+1] of Y [R, N] are
+   X_row(r)·Wq[e]ᵀ as above, with Wq [E, N, K], ws [E, NB, KB], Xq [T, K], xs [KB, T].
+   offsets [E+1] int32 on the device, non-decreasing, in [0, R]; an expert may have
+   no rows; rows outside [offsets[0], offsets[E]) keep what they held. row_index
+   [R] int32 on the device: row(r) = row_index[r], so a token's codes serve each of
+   its experts (an entry may occur any number of times; one outside [0, T) gives
+   a row of zeros); NULL: row(r) = r, and T must equal R. The contents of offsets
+   are not checked on the host: offsets outside [0, R] are clamped to it, and
+   with decreasing ones the rows of Y are unspecified, but nothing outside the
+   arrays is read or written. 1 <= E <= 8192; with row_index T*K < 2^32. R = 0
+   or N = 0 is a no-op. No host synchronisation: the call can be captured in a
+   HIP graph and replayed with other offsets. */
+ar_status ar_fp8_gemm_grouped_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K,
+                                             size_t* bytes);
+ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int64_t K,
+                              const uint8_t* Wq, const float* ws, int64_t E, int64_t N,
+                              const int32_t* offsets, const int32_t* row_index, int64_t R, void* Y,
+                              int32_t ydt, void* ws_buf, size_t ws_bytes, void* stream);
+
 /* ---- Sequential block-wise tuning with quantized inputs --------------------
    [LLMC] tuning loop (each Linear of a subgraph tuned in turn on its captured
    inputs and targets), parameter table and "enable_quanted_input 모드" (the
