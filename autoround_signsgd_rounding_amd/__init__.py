@@ -551,26 +551,46 @@ def unpack(qweight, qzeros, bits: int, N: int, K: int, G: int, stream=None):
 
 
 # ------------------------------------------------------------------ e4m3 operands
+# These calls run in microseconds, so the checks below ask each question of a
+# tensor once and build no objects on the way that succeeds.
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _want(t, name, shape, dtype):
+    """_need for one dtype: its message, where this quick look finds a fault."""
+    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_cuda or \
+            not t.is_contiguous():
+        _need(t, name, shape, dtype)
+
+
 def _on(stream, *tensors):
     """Context in which a call on these tensors allocates and launches: their
     device, and ``stream`` (its current stream if None). ValueError when the
     tensors or the stream are on different devices."""
     torch = _torch()
-    ts = [t for t in tensors if t is not None]
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t.device != dev:
-            raise ValueError(f"tensors must live on one GPU, got {dev} and {t.device}")
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must live on one GPU, got cuda:{dev} and {t.device}")
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        if stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
         if stream != torch.cuda.current_stream(dev):
-            for t in ts:   # the allocator must not hand the memory on before the call ends
-                t.record_stream(stream)
+            for t in tensors:   # the allocator must not hand the memory on before the call ends
+                if t is not None:
+                    t.record_stream(stream)
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return _HERE_AND_NOW if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_of(t) -> int:
+    """Handle of the current stream of t's device (torch.cuda.current_stream builds
+    an object around the same number, 2.7 us a time)."""
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _fp8_scales(K: int) -> int:
@@ -591,8 +611,8 @@ def fp8_quant_act(X, *, gate: bool = False, stream=None):
     with _on(stream, X):
         q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
         s = torch.empty((_fp8_scales(K), M), dtype=torch.float32, device=X.device)
-        _check(lib.ar_fp8_quant_act(_dt(X), _ptr(X), int(gate), M, K, _ptr(q), _ptr(s),
-                                    _stream()), "ar_fp8_quant_act")
+        _check(lib.ar_fp8_quant_act(_dt(X), _at(X), int(gate), M, K, _at(q), _at(s),
+                                    _stream_of(X)), "ar_fp8_quant_act")
     return q, s
 
 
@@ -609,8 +629,8 @@ def fp8_quant_weight(W, *, stream=None):
         q = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device)
         s = torch.empty((*lead, _fp8_scales(N), _fp8_scales(K)), dtype=torch.float32,
                         device=W.device)
-        _check(lib.ar_fp8_quant_weight(_dt(W), _ptr(W), lead[0] if lead else 1, N, K, _ptr(q),
-                                       _ptr(s), _stream()), "ar_fp8_quant_weight")
+        _check(lib.ar_fp8_quant_weight(_dt(W), _at(W), lead[0] if lead else 1, N, K, _at(q),
+                                       _at(s), _stream_of(W)), "ar_fp8_quant_weight")
     return q, s
 
 
@@ -630,13 +650,13 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
     in x's dtype."""
     torch = _torch()
     M, D = _weight(x, "x")
-    _need(weight, "weight", (D,), x.dtype)
+    _want(weight, "weight", (D,), x.dtype)
     if residual is not None:
-        _need(residual, "residual", (M, D), x.dtype)
+        _want(residual, "residual", (M, D), x.dtype)
     if h_out is not None:
         if residual is None:
             raise ValueError("h_out needs a residual")
-        _need(h_out, "h_out", (M, D), x.dtype)
+        _want(h_out, "h_out", (M, D), x.dtype)
     with _on(stream, x, weight, residual, h_out):
         q = torch.empty((M, D), dtype=torch.float8_e4m3fn, device=x.device)
         s = torch.empty((_fp8_scales(D), M), dtype=torch.float32, device=x.device)
@@ -644,8 +664,8 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
         if residual is not None and h is None:
             h = torch.empty_like(x)
         y = torch.empty_like(x) if want_y else None
-        _check(lib.ar_rmsnorm_fp8(_dt(x), _ptr(x), _ptr(residual), _ptr(weight), M, D, eps,
-                                  _ptr(h), _ptr(y), _ptr(q), _ptr(s), _stream()),
+        _check(lib.ar_rmsnorm_fp8(_dt(x), _at(x), _at(residual), _at(weight), M, D, eps,
+                                  _at(h), _at(y), _at(q), _at(s), _stream_of(x)),
                "ar_rmsnorm_fp8")
     return NormOutput(q, s, h, y)
 
@@ -667,16 +687,18 @@ def fp8_gemm_grouped_workspace_size(E: int, R: int, N: int, K: int) -> int:
 def _fp8_operands(Xq, xs, Wq, ws, dims: int):
     """Shapes of the two operands and their scales, checked."""
     torch = _torch()
-    f8 = torch.float8_e4m3fn
+    f8, f32 = torch.float8_e4m3fn, torch.float32
     if Xq is None or Xq.dim() != 2:
         raise ValueError("Xq must be a 2-D [T, K] tensor")
     if Wq is None or Wq.dim() != dims:
         raise ValueError("Wq must be a [%sN, K] tensor" % ("E, " if dims == 3 else ""))
-    (T, K), N = Xq.shape, Wq.shape[-2]
-    _need(Xq, "Xq", (T, K), f8)
-    _need(xs, "xs", (_fp8_scales(K), T), torch.float32)
-    _need(Wq, "Wq", (*Wq.shape[:-2], N, K), f8)
-    _need(ws, "ws", (*Wq.shape[:-2], _fp8_scales(N), _fp8_scales(K)), torch.float32)
+    T, K = Xq.shape
+    lead, N = Wq.shape[:-2], Wq.shape[-2]
+    KB = _fp8_scales(K)
+    _want(Xq, "Xq", (T, K), f8)
+    _want(xs, "xs", (KB, T), f32)
+    _want(Wq, "Wq", (*lead, N, K), f8)
+    _want(ws, "ws", (*lead, _fp8_scales(N), KB), f32)
     return T, K, N
 
 
@@ -706,8 +728,8 @@ def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, workspace=None, stream
     with _on(stream, Xq, xs, Wq, ws, out, workspace):
         Y, wsb, nb = _fp8_out(out, workspace, M, N, out_dtype,
                               fp8_gemm_workspace_size(M, N, K) if M and N else 0, Xq.device)
-        _check(lib.ar_fp8_gemm(_ptr(Xq), _ptr(xs), M, K, _ptr(Wq), _ptr(ws), N, _ptr(Y), _dt(Y),
-                               _ptr(wsb), nb, _stream()), "ar_fp8_gemm")
+        _check(lib.ar_fp8_gemm(_at(Xq), _at(xs), M, K, _at(Wq), _at(ws), N, _at(Y), _dt(Y),
+                               _at(wsb), nb, _stream_of(Xq)), "ar_fp8_gemm")
     return Y
 
 
@@ -722,21 +744,21 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
     torch = _torch()
     T, K, N = _fp8_operands(Xq, xs, Wq, ws, 3)
     E = Wq.shape[0]
-    _need(offsets, "offsets", (E + 1,), torch.int32)
+    _want(offsets, "offsets", (E + 1,), torch.int32)
     R = T
     if row_index is not None:
         if row_index.dim() != 1:
             raise ValueError("row_index must be a 1-D [R] tensor")
         R = row_index.shape[0]
-        _need(row_index, "row_index", (R,), torch.int32)
+        _want(row_index, "row_index", (R,), torch.int32)
     _fp8_given(out, workspace, R, N)
     with _on(stream, Xq, xs, Wq, ws, offsets, row_index, out, workspace):
         Y, wsb, nb = _fp8_out(out, workspace, R, N, out_dtype,
                               fp8_gemm_grouped_workspace_size(E, R, N, K) if R and N else 0,
                               Xq.device)
-        _check(lib.ar_fp8_gemm_grouped(_ptr(Xq), _ptr(xs), T, K, _ptr(Wq), _ptr(ws), E, N,
-                                       _ptr(offsets), _ptr(row_index), R, _ptr(Y), _dt(Y),
-                                       _ptr(wsb), nb, _stream()), "ar_fp8_gemm_grouped")
+        _check(lib.ar_fp8_gemm_grouped(_at(Xq), _at(xs), T, K, _at(Wq), _at(ws), E, N,
+                                       _at(offsets), _at(row_index), R, _at(Y), _dt(Y),
+                                       _at(wsb), nb, _stream_of(Xq)), "ar_fp8_gemm_grouped")
     return Y
 
 

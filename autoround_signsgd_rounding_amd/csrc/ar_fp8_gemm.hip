@@ -121,6 +121,7 @@ struct WideFrag {
 template <bool WIDE>
 struct FragOf {
   typedef i32x8_t type;
+  typedef uint16_t out;   // bf16
   static __device__ __forceinline__ type of(const i32x8_t& x) { return x; }
   static __device__ __forceinline__ f32x4_t mul(const type& w, const type& x) {
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -130,6 +131,7 @@ struct FragOf {
 template <>
 struct FragOf<true> {
   typedef WideFrag type;
+  typedef float out;
   static __device__ __forceinline__ type of(const i32x8_t& x) {
     WideFrag f;
 #pragma unroll
@@ -263,23 +265,35 @@ __global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
 // ------------------------------------------------------------------ many rows
 // Tiles of TM = 16·MB·WM rows by TN = 16·NA·WN columns, one wave per 16·MB x 16·NA
 // part. A step is one block of 128 k: W's and X's rows of the tile (128 bytes
-// each) and X's scales go straight from memory to LDS, two stages of them. In
+// each) and X's scales go straight from memory to LDS, NS stages of them. In
 // LDS, 16-byte chunk c of row r sits at chunk c ^ ((r >> 1) & 7), so that the 16
 // rows a fragment read touches with one chunk number lie in 16 different
 // 16-byte slots of a 256-byte LDS cycle.
 //
 // A wave keeps its MB X fragments of the step and streams its NA W fragments
-// past them, two ahead. When the last of them is in registers, the wave waits
-// for the next stage's loads (a whole step old by then) and the workgroup meets;
-// the loads of the step after the next go into the stage just left, and the next
-// stage's fragments are read while the last W fragment's products run.
-template <int WM, int WN, int MB, int NA>
+// past them, two ahead. When the last two of them are in registers, the wave waits
+// for the next stage's loads and the workgroup meets; while the products of those
+// two run, the stage just left is filled for NS steps ahead and the next step's
+// fragments are read, each X fragment as the old one is done with.
+template <int WM, int WN, int MB, int NA, int NS>
 struct Tile {
   static constexpr int TM = 16 * MB * WM, TN = 16 * NA * WN, NW = WM * WN;
   static constexpr int W_BYTES = TN * BLK, X_BYTES = TM * BLK;
-  static constexpr int STAGE = W_BYTES + X_BYTES + TM * 4;
+  static constexpr int SROWS = TM < 64 ? 64 : TM;            // rows of scales loaded, 64 at a time
+  static constexpr int STAGE = W_BYTES + X_BYTES + SROWS * 4;
+  static constexpr int LDS = NS * STAGE;
   static constexpr int IW = TN / 8 / NW, IX = TM / 8 / NW;   // 1 KiB loads per wave and operand
+  static constexpr int LOADS = IW + IX + 1;                  // of one wave and step
+  static_assert(IW * NW * 8 == TN && IX * NW * 8 == TM, "whole loads");
+  static_assert(LDS <= 160 * 1024 && (NS - 1) * LOADS < 64, "LDS of a workgroup, vmcnt's range");
 };
+
+// Waits until at most n of the wave's vector-memory operations and none of its LDS
+// operations are outstanding.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4));
+}
 constexpr uint32_t kNone = 0xFFFFFFF0u;   // past every buffer: the load writes zeros
 
 // Workgroup -> (m tile, n tile). The dispatcher places workgroup w on XCD w mod 8:
@@ -313,9 +327,9 @@ __device__ __forceinline__ int count_tiles(const Args& a) {
   return __builtin_amdgcn_readfirstlane(n);
 }
 
-template <int WM, int WN, int MB, int NA, bool WIDE>
+template <int WM, int WN, int MB, int NA, int NS, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN) {
-  typedef Tile<WM, WN, MB, NA> C;
+  typedef Tile<WM, WN, MB, NA, NS> C;
   typedef FragOf<WIDE> Op;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
@@ -355,7 +369,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
     vx[i] = x >= 0 ? (uint32_t)x * K + chunk(r) : kNone;
   }
   // scales: 64 rows per wave, four bytes a lane
-  const int sr = 64 * (wave % (C::TM / 64)) + lane;
+  const int sw0 = 64 * (wave % (C::SROWS / 64)), sr = sw0 + lane;
   uint32_t vs = kNone;
   if (sr < rows) {
     const int64_t x = a.idx ? x_row(a, r0 + sr) : sr;
@@ -366,48 +380,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
 #define AR_LDS(p) ((__attribute__((address_space(3))) void*)(p))
   // Past the last block (and in its missing chunks) the loads write zeros, so the
   // loop needs no branch around them.
-  auto issue = [&](int kt) {
-    uint8_t* st = lds + (kt & 1) * C::STAGE;
+  auto issue = [&](int kt, int stage, int piece) {
+    uint8_t* st = lds + stage;
     const uint32_t so = (uint32_t)kt * BLK;
     const bool tail = so + BLK > K;
-#pragma unroll
-    for (int i = 0; i < C::IW; ++i) {
-      const int r = 8 * (wave * C::IW + i) + (lane >> 3);
-      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vw[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, AR_LDS(st + (wave * C::IW + i) * 1024), 16, v,
-                                               so, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < C::IX; ++i) {
-      const int r = 8 * (wave * C::IX + i) + (lane >> 3);
-      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vx[i];
+    if (piece < C::IW) {
+      const int i8 = wave * C::IW + piece, r = 8 * i8 + (lane >> 3);
+      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vw[piece];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, AR_LDS(st + i8 * 1024), 16, v, so, 0, 0);
+    } else if (piece < C::IW + C::IX) {
+      const int i8 = wave * C::IX + piece - C::IW, r = 8 * i8 + (lane >> 3);
+      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vx[piece - C::IW];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bx, AR_LDS(st + C::W_BYTES + i8 * 1024), 16, v, so,
+                                               0, 0);
+    } else {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          bx, AR_LDS(st + C::W_BYTES + (wave * C::IX + i) * 1024), 16, v, so, 0, 0);
+          make_rsrc(xs + (int64_t)kt * a.T, xs_bytes),
+          AR_LDS(st + C::W_BYTES + C::X_BYTES + sw0 * 4), 4, kt < KB ? vs : kNone, 0, 0, 0);
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        make_rsrc(xs + (int64_t)kt * a.T, xs_bytes),
-        AR_LDS(st + C::W_BYTES + C::X_BYTES + (wave % (C::TM / 64)) * 256), 4,
-        kt < KB ? vs : kNone, 0, 0, 0);
   };
 #undef AR_LDS
 
-  // Fragments: lane l reads row l % 16, chunks 2·(l / 16) and the next.
+  // Fragments: lane l reads row l % 16, chunks l / 16 and l / 16 + 4. An LDS cycle
+  // serves 16 lanes of two neighbouring quarters of the wave, rows 0-3 and 12-15 of
+  // one and 4-11 of the other (or the reverse): with chunk numbers that differ
+  // in the last bit only, their slots are all different.
   const int l16 = lane & 15, q = lane >> 4;
-  const uint32_t slot = (uint32_t)(((2 * q) ^ (l16 >> 1)) * 16);
+  const uint32_t slot = (uint32_t)((q ^ (l16 >> 1)) * 16);
   const uint32_t aw = (uint32_t)(wn * NA * 16 + l16) * BLK + slot;
   const uint32_t ax = (uint32_t)C::W_BYTES + (uint32_t)(wm * MB * 16 + l16) * BLK + slot;
   const uint32_t as = (uint32_t)(C::W_BYTES + C::X_BYTES) + (uint32_t)(wm * MB * 16 + l16) * 4;
-  auto rd = [&](int kt, uint32_t at) {
-    const uint8_t* st = lds + (kt & 1) * C::STAGE;
+  auto rd = [&](int stage, uint32_t at) {
+    const uint8_t* st = lds + stage;
     const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(st + at);
-    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(st + (at ^ 16u));
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(st + (at ^ 64u));
     return Op::of(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
   // W's scales of this wave's columns (one block of 128), 64 blocks of K at a time
   const int64_t nb = (n0 + wn * NA * 16) / BLK;
   const float* wsp = a.ws + ((int64_t)e * a.NB + (nb < a.NB ? nb : a.NB - 1)) * KB;
-  float wsv = 0.0f;
+  auto window = [&](int k0) { return k0 + lane < KB ? wsp[k0 + lane] : 0.0f; };
+  float wsv = window(0);   // requested before the stages, so that it arrives first
 
   f32x4_t acc[NA][MB];
 #pragma unroll
@@ -415,14 +429,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[t][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto arrive = [&]() {   // this wave's loads are in LDS and its reads done; then everyone's
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
-    __syncthreads();
+  int cur = 0, nxt = C::STAGE;   // stages of steps kt and kt + 1
+  auto meet = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
-  issue(0);
-  arrive();
-  issue(1);
-  typename Op::type fx[MB], fw[2];
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int j = 0; j < C::LOADS; ++j) issue(i, i * C::STAGE, j);
+  wait_loads<(NS - 1) * C::LOADS>();
+  meet();
+  // W fragment t of a step is in fw[t % 4] (with NA = 2, where a step's last two
+  // fragments are all it has, the next step's two come in through fw[2] and fw[3])
+  typename Op::type fx[MB], fw[4];
   float sx[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
@@ -437,55 +459,103 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
     float s[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) s[b] = sw * sx[b];
-    // products three items behind the matrix unit's issue join the accumulators
+    // Items: W fragment by W fragment up to the last two, those X fragment by X
+    // fragment. Products join the accumulators three items behind the matrix
+    // unit's issue.
+    constexpr int ITEMS = NA * MB, LAST = (NA - 2) * MB;
+    auto tile = [](int u) { return u < LAST ? u / MB : NA - 2 + (u - LAST) % 2; };
+    auto part = [](int u) { return u < LAST ? u % MB : (u - LAST) / 2; };
     f32x4_t p[4];
     auto join = [&](int u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        acc[u / MB][u % MB][i] = fmaf(p[u % 4][i], s[u % MB], acc[u / MB][u % MB][i]);
+        acc[tile(u)][part(u)][i] = fmaf(p[u % 4][i], s[part(u)], acc[tile(u)][part(u)][i]);
     };
 #pragma unroll
-    for (int u = 0; u < NA * MB; ++u) {
-      const int t = u / MB, b = u % MB;
-      if (u == (NA - 1) * MB) {
-        arrive();
-        issue(kt + 2);
+    for (int u = 0; u < ITEMS; ++u) {
+      const int t = tile(u), b = part(u);
+      if (u == LAST) {
+        // the next step's stage has landed, this one's reads are done; then everyone's
+        wait_loads<(NS - 2) * C::LOADS>();
+        meet();
       }
-      p[u % 4] = Op::mul(fw[t & 1], fx[b]);
-      if (t == NA - 1) {   // the next step's fragments replace these
-        fx[b] = rd(kt + 1, ax + b * 16 * BLK);
-        sx[b] = *reinterpret_cast<const float*>(lds + ((kt + 1) & 1) * C::STAGE + as + b * 64);
-        if (b == 0) fw[t & 1 ^ 1] = rd(kt + 1, aw);
-        if (b == MB - 1) fw[t & 1] = rd(kt + 1, aw + 16 * BLK);
-      } else if (b == MB - 1 && t + 2 < NA) {
-        fw[t & 1] = rd(kt, aw + (t + 2) * 16 * BLK);
+      p[u % 4] = Op::mul(fw[t % 4], fx[b]);
+      if (u < LAST) {
+        if (b == 0) fw[(t + 2) % 4] = rd(cur, aw + (t + 2) * 16 * BLK);
+      } else {
+        constexpr int EACH = (C::LOADS + 2 * MB - 1) / (2 * MB);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+          if ((u - LAST) * EACH + i < C::LOADS) issue(kt + NS, cur, (u - LAST) * EACH + i);
+        if (t == NA - 1) {   // the next step's fragments replace these
+          fx[b] = rd(nxt, ax + b * 16 * BLK);
+          sx[b] = *reinterpret_cast<const float*>(lds + nxt + as + b * 64);
+          if (b == 0) fw[NA % 4] = rd(nxt, aw);
+          if (b == MB - 1) fw[(NA + 1) % 4] = rd(nxt, aw + 16 * BLK);
+        }
       }
       if (u >= 3) join(u - 3);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int u = NA * MB - 3; u < NA * MB; ++u) join(u);
+    for (int u = ITEMS > 3 ? ITEMS - 3 : 0; u < ITEMS; ++u) join(u);
+    if constexpr (NA == 2) {
+      fw[0] = fw[2];
+      fw[1] = fw[3];
+    }
+    cur = nxt;
+    nxt = nxt + C::STAGE == C::LDS ? 0 : nxt + C::STAGE;
   };
   for (int k0 = 0; k0 < KB; k0 += 64) {
-    float v = k0 + lane < KB ? wsp[k0 + lane] : 0.0f;
-    asm volatile("" : "+v"(v));   // waits for it here, not in every step
-    wsv = v;
+    if (k0 > 0) wsv = window(k0);
+    asm volatile("" : "+v"(wsv));   // waits for it here, not in every step
     const int k1 = min(k0 + 64, KB);
     for (int kt = k0; kt < k1; ++kt) step(kt);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load may land in LDS after the end
 
+  // The wave's part of Y goes through LDS (the stages are free once everyone is
+  // here) so that rows leave as whole 256-byte runs, past the caches: nothing
+  // reads them soon, and the tiles of all CUs end at about the same time.
+  // Measured at 16384 x 4096 x 4096 against storing from the accumulators: 253
+  // us instead of 267.
+  __syncthreads();
+  typedef typename Op::out O;
+  constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
+  static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
+  uint8_t* own = lds + wave * (MB * 16 * RB);
+  auto at = [&](int r, int byte) {   // 16-byte chunks spread over the banks by row
+    return own + r * RB + (byte ^ ((r & (RB / 16 - 1)) * 16));
+  };
 #pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int m = wm * MB * 16 + 16 * b + l16;
-    if (m < rows) {
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int t = 0; t < NA; ++t) {
-        const float v[4] = {acc[t][b][0], acc[t][b][1], acc[t][b][2], acc[t][b][3]};
-        store_y(a, r0 + m, n0 + wn * NA * 16 + 16 * t + 4 * q, v);
-      }
+    for (int t = 0; t < NA; ++t) {
+      const f32x4_t v = acc[t][b];
+      uint8_t* d = at(16 * b + l16, (16 * t + 4 * q) * (int)sizeof(O));
+      if constexpr (sizeof(O) == 2)
+        *reinterpret_cast<u32x2_t*>(d) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      else
+        *reinterpret_cast<f32x4_t*>(d) = v;
     }
-  }
+  O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
+  const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
+  auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
+    typedef decltype(unit) V;
+    constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
+#pragma unroll 8
+    for (int i = lane; i < MB * 16 * UPR; i += 64) {
+      const int r = i / UPR, u = i % UPR;
+      if (r < mleft && u * PER < nleft)
+        __builtin_nontemporal_store(*reinterpret_cast<const V*>(at(r, u * (int)sizeof(V))),
+                                    reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u);
+    }
+  };
+  const int64_t pitch = a.N * (int64_t)sizeof(O);
+  if (pitch % 16 == 0) write(u32x4_t{});
+  else if (pitch % 8 == 0) write(u32x2_t{});
+  else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
+  else write(uint16_t{});
 }
 
 }  // namespace
@@ -496,17 +566,16 @@ static int64_t max_tiles(int64_t R, int64_t E, int64_t TM) {
   return t < R ? t : R;
 }
 
-template <int WM, int WN, int MB, int NA, bool WIDE>
+template <int WM, int WN, int MB, int NA, int NS, bool WIDE>
 static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
-  typedef Tile<WM, WN, MB, NA> C;
-  static_assert(2 * C::STAGE <= 160 * 1024, "LDS of one workgroup");
+  typedef Tile<WM, WN, MB, NA, NS> C;
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
   if (tilesM * tilesN >= (int64_t(1) << 22)) return AR_ERR_SHAPE;
-  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, WIDE>);
-  if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * C::STAGE) != hipSuccess)
+  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, WIDE>);
+  if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess)
     return AR_ERR_HIP;
-  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, WIDE>), dim3((unsigned)(tilesM * tilesN)),
-                     dim3(64 * WM * WN), 2 * C::STAGE, st, a, (int)tilesN);
+  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, WIDE>), dim3((unsigned)(tilesM * tilesN)),
+                     dim3(64 * WM * WN), C::LDS, st, a, (int)tilesN);
   return last_status();
 }
 
@@ -529,7 +598,7 @@ ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
   };
   if (mean <= 16) return rows_launch<1>(a, tiles(16), st);
   if (mean <= 64) return rows_launch<4>(a, tiles(64), st);
-  if (g.ydt == AR_F32) return tile_launch<2, 2, 4, 4, true>(a, tiles(128), st);
-  if (tiles(256) * ((g.N + 255) / 256) >= 256) return tile_launch<4, 2, 4, 8, false>(a, tiles(256), st);
-  return tile_launch<2, 2, 4, 4, false>(a, tiles(128), st);
+  if (g.ydt == AR_F32) return tile_launch<2, 2, 4, 4, 2, true>(a, tiles(128), st);
+  if (tiles(256) * ((g.N + 255) / 256) >= 256) return tile_launch<4, 2, 4, 8, 2, false>(a, tiles(256), st);
+  return tile_launch<2, 2, 4, 4, 2, false>(a, tiles(128), st);
 }
