@@ -32,8 +32,8 @@ EXPORTS = (
     "ar_tune_linear_gram", "ar_init_clip", "ar_resolve_layer_config", "ar_resolve_fused_config",
     "ar_dequant_gemm_workspace_size", "ar_dequant_gemm", "ar_block_workspace_size",
     "ar_block_forward", "ar_tune_block", "ar_attention", "ar_tune_step_noalloc",
-    "ar_fp8_quant_act", "ar_fp8_quant_weight", "ar_rmsnorm_fp8", "ar_fp8_gemm_workspace_size",
-    "ar_fp8_gemm", "ar_fp8_gemm_grouped_workspace_size", "ar_fp8_gemm_grouped",
+    "ar_fp8_quant_act", "ar_fp8_quant_weight", "ar_rmsnorm_fp8", "ar_fp8_gemm",
+    "ar_fp8_gemm_grouped",
 )
 
 # input channels per scale of the e4m3 operands
@@ -150,11 +150,8 @@ def _load():
         "ar_fp8_quant_act": [i32, vp, i32, i64, i64, vp, vp, vp],
         "ar_fp8_quant_weight": [i32, vp, i64, i64, i64, vp, vp, vp],
         "ar_rmsnorm_fp8": [i32, vp, vp, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp],
-        "ar_fp8_gemm_workspace_size": [i64, i64, i64, ctypes.POINTER(sz)],
-        "ar_fp8_gemm": [vp, vp, i64, i64, vp, vp, i64, vp, i32, vp, sz, vp],
-        "ar_fp8_gemm_grouped_workspace_size": [i64, i64, i64, i64, ctypes.POINTER(sz)],
-        "ar_fp8_gemm_grouped": [vp, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i32, vp, sz,
-                                vp],
+        "ar_fp8_gemm": [vp, vp, i64, i64, vp, vp, i64, vp, i32, vp],
+        "ar_fp8_gemm_grouped": [vp, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i32, vp],
         "ar_pack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
         "ar_unpack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
     }
@@ -670,20 +667,6 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
     return NormOutput(q, s, h, y)
 
 
-def fp8_gemm_workspace_size(M: int, N: int, K: int) -> int:
-    need = ctypes.c_size_t()
-    _check(lib.ar_fp8_gemm_workspace_size(M, N, K, ctypes.byref(need)),
-           "ar_fp8_gemm_workspace_size")
-    return need.value
-
-
-def fp8_gemm_grouped_workspace_size(E: int, R: int, N: int, K: int) -> int:
-    need = ctypes.c_size_t()
-    _check(lib.ar_fp8_gemm_grouped_workspace_size(E, R, N, K, ctypes.byref(need)),
-           "ar_fp8_gemm_grouped_workspace_size")
-    return need.value
-
-
 def _fp8_operands(Xq, xs, Wq, ws, dims: int):
     """Shapes of the two operands and their scales, checked."""
     torch = _torch()
@@ -702,39 +685,25 @@ def _fp8_operands(Xq, xs, Wq, ws, dims: int):
     return T, K, N
 
 
-def _fp8_out(out, workspace, R, N, out_dtype, need, device):
-    torch = _torch()
-    if out is None:
-        out = torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=device)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return out, workspace, 0 if workspace is None else workspace.numel()
-
-
-def _fp8_given(out, workspace, R, N):
-    torch = _torch()
-    if out is not None:
-        _need(out, "out", (R, N), (torch.float32, torch.bfloat16))
-    if workspace is not None:
-        _need(workspace, "workspace", (workspace.numel(),), torch.uint8)
-
-
-def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, workspace=None, stream=None):
+def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
     """Y [M, N] (bf16 unless ``out_dtype`` or ``out`` say float32) = X·Wᵀ of e4m3
     operands with their block scales (ar_fp8_gemm): Xq [M, K], xs [ceil(K/128), M]
     from fp8_quant_act or rmsnorm_fp8; Wq [N, K], ws from fp8_quant_weight."""
+    torch = _torch()
     M, K, N = _fp8_operands(Xq, xs, Wq, ws, 2)
-    _fp8_given(out, workspace, M, N)
-    with _on(stream, Xq, xs, Wq, ws, out, workspace):
-        Y, wsb, nb = _fp8_out(out, workspace, M, N, out_dtype,
-                              fp8_gemm_workspace_size(M, N, K) if M and N else 0, Xq.device)
+    if out is not None:
+        _need(out, "out", (M, N), (torch.float32, torch.bfloat16))
+    with _on(stream, Xq, xs, Wq, ws, out):
+        Y = out
+        if Y is None:
+            Y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=Xq.device)
         _check(lib.ar_fp8_gemm(_at(Xq), _at(xs), M, K, _at(Wq), _at(ws), N, _at(Y), _dt(Y),
-                               _at(wsb), nb, _stream_of(Xq)), "ar_fp8_gemm")
+                               _stream_of(Xq)), "ar_fp8_gemm")
     return Y
 
 
 def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None, out=None,
-                     workspace=None, stream=None):
+                     stream=None):
     """Y [R, N]: rows offsets[e]..offsets[e+1] are the product with expert e's
     weight (ar_fp8_gemm_grouped): Wq [E, N, K] and ws from fp8_quant_weight,
     offsets [E + 1] int32 on the GPU. ``row_index`` [R] int32 names the row of
@@ -751,14 +720,15 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
             raise ValueError("row_index must be a 1-D [R] tensor")
         R = row_index.shape[0]
         _want(row_index, "row_index", (R,), torch.int32)
-    _fp8_given(out, workspace, R, N)
-    with _on(stream, Xq, xs, Wq, ws, offsets, row_index, out, workspace):
-        Y, wsb, nb = _fp8_out(out, workspace, R, N, out_dtype,
-                              fp8_gemm_grouped_workspace_size(E, R, N, K) if R and N else 0,
-                              Xq.device)
+    if out is not None:
+        _need(out, "out", (R, N), (torch.float32, torch.bfloat16))
+    with _on(stream, Xq, xs, Wq, ws, offsets, row_index, out):
+        Y = out
+        if Y is None:
+            Y = torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=Xq.device)
         _check(lib.ar_fp8_gemm_grouped(_at(Xq), _at(xs), T, K, _at(Wq), _at(ws), E, N,
                                        _at(offsets), _at(row_index), R, _at(Y), _dt(Y),
-                                       _at(wsb), nb, _stream_of(Xq)), "ar_fp8_gemm_grouped")
+                                       _stream_of(Xq)), "ar_fp8_gemm_grouped")
     return Y
 
 

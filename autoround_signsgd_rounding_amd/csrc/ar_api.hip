@@ -1055,36 +1055,21 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
                                static_cast<hipStream_t>(stream));
 }
 
-ar_status ar_fp8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
-  return ar_fp8_gemm_grouped_workspace_size(1, M, N, K, bytes);
-}
-
 ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
-                      const float* ws, int64_t N, void* Y, int32_t ydt, void* ws_buf,
-                      size_t ws_bytes, void* stream) {
+                      const float* ws, int64_t N, void* Y, int32_t ydt, void* stream) {
   AR_TRY(check_fp8_gemm(1, M, N, K));
   if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return AR_OK;
   if (!Xq || !xs || !Wq || !ws || !Y) return AR_ERR_INVALID_ARG;
   if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a16(Y)) return AR_ERR_INVALID_ARG;
-  (void)ws_buf;
-  (void)ws_bytes;
   return ar_launch_fp8_gemm(ArFp8Gemm{Xq, xs, Wq, ws, nullptr, nullptr, Y, ydt, M, M, N, K, 1},
                             static_cast<hipStream_t>(stream));
-}
-
-ar_status ar_fp8_gemm_grouped_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K,
-                                             size_t* bytes) {
-  if (!bytes) return AR_ERR_INVALID_ARG;
-  AR_TRY(check_fp8_gemm(E, R, N, K));
-  *bytes = 0;
-  return AR_OK;
 }
 
 ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int64_t K,
                               const uint8_t* Wq, const float* ws, int64_t E, int64_t N,
                               const int32_t* offsets, const int32_t* row_index, int64_t R, void* Y,
-                              int32_t ydt, void* ws_buf, size_t ws_bytes, void* stream) {
+                              int32_t ydt, void* stream) {
   AR_TRY(check_fp8_gemm(E, R, N, K));
   AR_TRY(check_fp8_rows(T, K));
   if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
@@ -1094,8 +1079,6 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
   if (!Xq || !xs || !Wq || !ws || !offsets || !Y) return AR_ERR_INVALID_ARG;
   if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a4(offsets) || !a4(row_index) || !a16(Y))
     return AR_ERR_INVALID_ARG;
-  (void)ws_buf;
-  (void)ws_bytes;
   return ar_launch_fp8_gemm(
       ArFp8Gemm{Xq, xs, Wq, ws, offsets, row_index, Y, ydt, T, R, N, K, E},
       static_cast<hipStream_t>(stream));

@@ -14,6 +14,10 @@
 // value for a whole wave, and Y is stored four values at a time. A and B use
 // one assignment of k to lanes (32 consecutive bytes per lane: K is summed
 // over, so any will do).
+#include <math.h>
+
+#include <type_traits>
+
 #include "ar_device.h"
 #include "ar_launch.h"
 
@@ -121,7 +125,6 @@ struct WideFrag {
 template <bool WIDE>
 struct FragOf {
   typedef i32x8_t type;
-  typedef uint16_t out;   // bf16
   static __device__ __forceinline__ type of(const i32x8_t& x) { return x; }
   static __device__ __forceinline__ f32x4_t mul(const type& w, const type& x) {
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -131,7 +134,6 @@ struct FragOf {
 template <>
 struct FragOf<true> {
   typedef WideFrag type;
-  typedef float out;
   static __device__ __forceinline__ type of(const i32x8_t& x) {
     WideFrag f;
 #pragma unroll
@@ -157,17 +159,17 @@ struct FragOf<true> {
   }
 };
 
-// 32 bytes at p (16-byte aligned); `left` bytes of the row remain from p on:
-// 16-byte halves past the row are zero (K % 16 == 0).
+// Two 16-byte chunks of a row, 64 bytes apart (p 16-byte aligned); in a row's last,
+// short block the chunks past the `left` bytes from p on are zero (K % 16 == 0).
 __device__ __forceinline__ i32x8_t frag(const uint8_t* p) {
   const i32x4_t a = reinterpret_cast<const i32x4_t*>(p)[0];
-  const i32x4_t b = reinterpret_cast<const i32x4_t*>(p)[1];
+  const i32x4_t b = reinterpret_cast<const i32x4_t*>(p)[4];
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 __device__ __forceinline__ i32x8_t frag_tail(const uint8_t* p, int left) {
   i32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
   if (left > 0) a = reinterpret_cast<const i32x4_t*>(p)[0];
-  if (left > 16) b = reinterpret_cast<const i32x4_t*>(p)[1];
+  if (left > 64) b = reinterpret_cast<const i32x4_t*>(p)[4];
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -180,85 +182,72 @@ __device__ __forceinline__ int64_t x_row(const Args& a, int64_t r) {
 
 // ------------------------------------------------------------------ few rows
 // Operands straight from memory to registers. A workgroup of 8 waves makes a
-// tile of 16 n by 16·MT rows; the waves take the blocks of K in turn (wave w:
-// blocks w, w + 8, ...) and their sums are added through LDS in wave order.
+// tile of 16 columns by 16 rows (rows past the tile's repeat its last one, and
+// are not stored); the waves take the blocks of K in turn (wave w: blocks w,
+// w + 8, ...; four of them requested at a time) and their sums are added
+// through LDS in wave order.
 constexpr int DW = 8;
 
-template <int MT, bool WIDE>
+template <bool WIDE>
 __global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
   typedef FragOf<WIDE> Op;
-  constexpr int TM = 16 * MT;
-  __shared__ float red[DW][MT][64][4];
+  __shared__ float red[DW][64][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int e, rows;
   int64_t r0;
-  find_tile<TM>(a, blockIdx.y, e, r0, rows);
+  find_tile<16>(a, blockIdx.y, e, r0, rows);
   if (rows <= 0) return;
-  const int l16 = lane & 15, kc = 32 * (lane >> 4);
+  const int l16 = lane & 15, kc = 16 * (lane >> 4);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int64_t n = n0 + l16 < a.N ? n0 + l16 : a.N - 1;
   const uint8_t* wp = a.W + ((int64_t)e * a.N + n) * a.K + kc;
   const float* wsp = a.ws + ((int64_t)e * a.NB + n0 / BLK) * a.KB;
-  const uint8_t* xp[MT];
-  const float* xsp[MT];
-  bool live[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = 16 * t + l16;
-    const int64_t x = x_row(a, r0 + (m < rows ? m : rows - 1));
-    live[t] = x >= 0;
-    xp[t] = a.X + (x < 0 ? 0 : x) * a.K + kc;
-    xsp[t] = a.xs + (x < 0 ? 0 : x);
-  }
-  f32x4_t acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t xr = x_row(a, r0 + (l16 < rows ? l16 : rows - 1));
+  const uint8_t* xp = a.X + (xr < 0 ? 0 : xr) * a.K + kc;
+  const float* xsp = a.xs + (xr < 0 ? 0 : xr);
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
   const int full = (int)(a.K / BLK);
-  auto add = [&](int j, const i32x8_t& w, const i32x8_t (&x)[MT]) {
-    const float sw = wsp[j];
-    const typename Op::type wf = Op::of(w);
+  auto add = [&](const i32x8_t& w, const i32x8_t& x, float s) {
+    const f32x4_t p = Op::mul(Op::of(w), Op::of(x));
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float s = sw * xsp[t][(int64_t)j * a.T];
-      const f32x4_t p = Op::mul(wf, Op::of(x[t]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], s, acc[t][i]);
-    }
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
   };
-  for (int j = wave; j < full; j += DW) {
-    const i32x8_t w = frag(wp + (int64_t)j * BLK);
-    i32x8_t x[MT];
+  auto batch = [&](int j, auto count) {
+    constexpr int U = decltype(count)::value;
+    i32x8_t w[U], x[U];
+    float sw[U], sx[U];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) x[t] = frag(xp[t] + (int64_t)j * BLK);
-    add(j, w, x);
-  }
-  if (full < a.KB && full % DW == wave) {
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = j + u * DW;
+      w[u] = frag(wp + k * BLK);
+      x[u] = frag(xp + k * BLK);
+      sw[u] = wsp[k];
+      sx[u] = xsp[k * a.T];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(w[u], x[u], sw[u] * sx[u]);
+    return j + U * DW;
+  };
+  int j = wave;
+  while (j + 3 * DW < full) j = batch(j, std::integral_constant<int, 4>());
+  if (j + DW < full) j = batch(j, std::integral_constant<int, 2>());
+  if (j < full) j = batch(j, std::integral_constant<int, 1>());
+  if (j < a.KB) {   // j = full: the short block
     const int left = (int)(a.K - (int64_t)full * BLK) - kc;
-    const i32x8_t w = frag_tail(wp + (int64_t)full * BLK, left);
-    i32x8_t x[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) x[t] = frag_tail(xp[t] + (int64_t)full * BLK, left);
-    add(full, w, x);
+    add(frag_tail(wp + (int64_t)full * BLK, left), frag_tail(xp + (int64_t)full * BLK, left),
+        wsp[full] * xsp[(int64_t)full * a.T]);
   }
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-    *reinterpret_cast<f32x4_t*>(red[wave][t][lane]) = acc[t];
+  *reinterpret_cast<f32x4_t*>(red[wave][lane]) = acc;
   __syncthreads();
-  if (wave < MT) {
-    const int t = wave;
+  if (wave == 0) {
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < DW; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += red[w][t][lane][i];
-    const int m = 16 * t + l16;
-    bool ok = false;
-#pragma unroll
-    for (int u = 0; u < MT; ++u)
-      if (u == t) ok = live[u];
-    if (!ok) v[0] = v[1] = v[2] = v[3] = 0.0f;
-    if (m < rows) store_y(a, r0 + m, n0 + 4 * (lane >> 4), v);
+      for (int i = 0; i < 4; ++i) v[i] += red[w][lane][i];
+    if (xr < 0) v[0] = v[1] = v[2] = v[3] = 0.0f;
+    if (l16 < rows) store_y(a, r0 + l16, n0 + 4 * (lane >> 4), v);
   }
 }
 
@@ -275,13 +264,19 @@ __global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
 // for the next stage's loads and the workgroup meets; while the products of those
 // two run, the stage just left is filled for NS steps ahead and the next step's
 // fragments are read, each X fragment as the old one is done with.
-template <int WM, int WN, int MB, int NA, int NS>
+//
+// With KG > 1 a workgroup has KG such sets of waves and stages, each on its own
+// contiguous part of the blocks of K (steps past the end add zeros); the sums of
+// sets 1 .. KG - 1 join those of set 0 through LDS, in order. It shortens the
+// chain of steps where there are too few tiles to keep several workgroups on
+// each CU.
+template <int WM, int WN, int MB, int NA, int NS, int KG>
 struct Tile {
   static constexpr int TM = 16 * MB * WM, TN = 16 * NA * WN, NW = WM * WN;
   static constexpr int W_BYTES = TN * BLK, X_BYTES = TM * BLK;
   static constexpr int SROWS = TM < 64 ? 64 : TM;            // rows of scales loaded, 64 at a time
   static constexpr int STAGE = W_BYTES + X_BYTES + SROWS * 4;
-  static constexpr int LDS = NS * STAGE;
+  static constexpr int RING = NS * STAGE, LDS = KG * RING, THREADS = 64 * NW * KG;
   static constexpr int IW = TN / 8 / NW, IX = TM / 8 / NW;   // 1 KiB loads per wave and operand
   static constexpr int LOADS = IW + IX + 1;                  // of one wave and step
   static_assert(IW * NW * 8 == TN && IX * NW * 8 == TM, "whole loads");
@@ -327,13 +322,15 @@ __device__ __forceinline__ int count_tiles(const Args& a) {
   return __builtin_amdgcn_readfirstlane(n);
 }
 
-template <int WM, int WN, int MB, int NA, int NS, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN) {
-  typedef Tile<WM, WN, MB, NA, NS> C;
+template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int tilesN) {
+  typedef Tile<WM, WN, MB, NA, NS, KG> C;
   typedef FragOf<WIDE> Op;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds_all[];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int gwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int set = gwave / C::NW, wave = gwave % C::NW;
+  uint8_t* lds = lds_all + set * C::RING;
   const int wm = wave % WM, wn = wave / WM;
   const int tilesM = count_tiles<C::TM>(a);
   if ((int)blockIdx.x >= tilesM * tilesN) return;   // more workgroups than tiles: ragged ranges
@@ -344,7 +341,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
   if (rows <= 0) return;
   const int64_t n0 = (int64_t)tn * C::TN;
   const uint32_t K = (uint32_t)a.K;
-  const int KB = a.KB;
+  const int steps = (a.KB + KG - 1) / KG;                  // of every set
+  const int kb0 = set * steps, kb1 = min(kb0 + steps, a.KB);
+  const uint32_t kend = min((uint32_t)kb1 * BLK, K);
 
   // Loads: piece i of an operand is rows 8·(wave·I + i) .. + 7 of its tile, eight
   // lanes of 16 bytes a row; chunk[] is the lane's k offset within the block.
@@ -383,20 +382,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
   auto issue = [&](int kt, int stage, int piece) {
     uint8_t* st = lds + stage;
     const uint32_t so = (uint32_t)kt * BLK;
-    const bool tail = so + BLK > K;
+    const bool tail = so + BLK > kend;
     if (piece < C::IW) {
       const int i8 = wave * C::IW + piece, r = 8 * i8 + (lane >> 3);
-      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vw[piece];
+      const uint32_t v = tail && so + chunk(r) >= kend ? kNone : vw[piece];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, AR_LDS(st + i8 * 1024), 16, v, so, 0, 0);
     } else if (piece < C::IW + C::IX) {
       const int i8 = wave * C::IX + piece - C::IW, r = 8 * i8 + (lane >> 3);
-      const uint32_t v = tail && so + chunk(r) >= K ? kNone : vx[piece - C::IW];
+      const uint32_t v = tail && so + chunk(r) >= kend ? kNone : vx[piece - C::IW];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bx, AR_LDS(st + C::W_BYTES + i8 * 1024), 16, v, so,
                                                0, 0);
     } else {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           make_rsrc(xs + (int64_t)kt * a.T, xs_bytes),
-          AR_LDS(st + C::W_BYTES + C::X_BYTES + sw0 * 4), 4, kt < KB ? vs : kNone, 0, 0, 0);
+          AR_LDS(st + C::W_BYTES + C::X_BYTES + sw0 * 4), 4, kt < kb1 ? vs : kNone, 0, 0, 0);
     }
   };
 #undef AR_LDS
@@ -419,9 +418,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
 
   // W's scales of this wave's columns (one block of 128), 64 blocks of K at a time
   const int64_t nb = (n0 + wn * NA * 16) / BLK;
-  const float* wsp = a.ws + ((int64_t)e * a.NB + (nb < a.NB ? nb : a.NB - 1)) * KB;
-  auto window = [&](int k0) { return k0 + lane < KB ? wsp[k0 + lane] : 0.0f; };
-  float wsv = window(0);   // requested before the stages, so that it arrives first
+  const float* wsp = a.ws + ((int64_t)e * a.NB + (nb < a.NB ? nb : a.NB - 1)) * a.KB;
+  auto window = [&](int k0) { return k0 + lane < kb1 ? wsp[k0 + lane] : 0.0f; };
+  float wsv = window(kb0);   // requested before the stages, so that it arrives first
 
   f32x4_t acc[NA][MB];
 #pragma unroll
@@ -439,7 +438,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
-    for (int j = 0; j < C::LOADS; ++j) issue(i, i * C::STAGE, j);
+    for (int j = 0; j < C::LOADS; ++j) issue(kb0 + i, i * C::STAGE, j);
   wait_loads<(NS - 1) * C::LOADS>();
   meet();
   // W fragment t of a step is in fw[t % 4] (with NA = 2, where a step's last two
@@ -455,7 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
   fw[1] = rd(0, aw + 16 * BLK);
 
   auto step = [&](int kt) {
-    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), kt & 63));
+    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), (kt - kb0) & 63));
     float s[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) s[b] = sw * sx[b];
@@ -504,23 +503,42 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tile(Args a, int tilesN
       fw[1] = fw[3];
     }
     cur = nxt;
-    nxt = nxt + C::STAGE == C::LDS ? 0 : nxt + C::STAGE;
+    nxt = nxt + C::STAGE == C::RING ? 0 : nxt + C::STAGE;
   };
-  for (int k0 = 0; k0 < KB; k0 += 64) {
-    if (k0 > 0) wsv = window(k0);
+  for (int k0 = kb0; k0 < kb0 + steps; k0 += 64) {
+    if (k0 > kb0) wsv = window(k0);
     asm volatile("" : "+v"(wsv));   // waits for it here, not in every step
-    const int k1 = min(k0 + 64, KB);
+    const int k1 = min(k0 + 64, kb0 + steps);
     for (int kt = k0; kt < k1; ++kt) step(kt);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load may land in LDS after the end
 
   // The wave's part of Y goes through LDS (the stages are free once everyone is
-  // here) so that rows leave as whole 256-byte runs, past the caches: nothing
-  // reads them soon, and the tiles of all CUs end at about the same time.
-  // Measured at 16384 x 4096 x 4096 against storing from the accumulators: 253
-  // us instead of 267.
+  // here) so that rows leave as whole runs of 128 or 256 bytes, past the caches:
+  // the tiles of all CUs end at about the same time. Measured at 16384 x 4096 x
+  // 4096 against storing from the accumulators: 253 us instead of 267.
   __syncthreads();
-  typedef typename Op::out O;
+  if constexpr (KG > 1) {
+    static_assert((KG - 1) * C::TM * C::TN * 4 <= C::LDS, "the other sets' sums in LDS");
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds_all) + wave * (NA * MB * 64) + lane;
+    if (set > 0)
+#pragma unroll
+      for (int u = 0; u < NA * MB; ++u)
+        sums[((set - 1) * C::NW * NA * MB + u) * 64] = acc[u / MB][u % MB];
+    __syncthreads();
+    if (set > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int u = 0; u < NA * MB; ++u) {
+        const f32x4_t v = sums[(g * C::NW * NA * MB + u) * 64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u / MB][u % MB][i] += v[i];
+      }
+    static_assert((KG - 1) * C::TM * C::TN * 4 + C::TM * C::TN * 4 <= C::LDS, "beside Y's tile");
+    lds = lds_all + (KG - 1) * C::TM * C::TN * 4;
+  }
+  typedef std::conditional_t<WIDE, float, uint16_t> O;
   constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
   static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
   uint8_t* own = lds + wave * (MB * 16 * RB);
@@ -566,39 +584,120 @@ static int64_t max_tiles(int64_t R, int64_t E, int64_t TM) {
   return t < R ? t : R;
 }
 
-template <int WM, int WN, int MB, int NA, int NS, bool WIDE>
+// Which kernel: the one with the least estimated time. A tile's step (128 of K)
+// takes `step` us of a CU when two workgroups share it, and `step2` us of a
+// workgroup with two K sets that has a CU to itself (two steps of K at once);
+// the two sets are taken when no CU gets a second workgroup. Streaming from
+// memory (5.3 TB/s measured) and from the caches into LDS (14 TB/s) bound the
+// time from below. Measured (us), M x N x K:           the rule's pick   next size up / down
+//   64 x 11008 x 4096, bf16     64x64, two sets    12.2  14.9 / 17.0
+//   512 x 4096 x 4096           64x128, two sets   15.2  20.6 / 17.5
+//   1024 x 4096 x 4096          128x128, two sets  22.9  48.1 / 24.7
+//   4096 x 4096 x 4096          256x256            59.8   -   / 69.8
+//   16 x 4096 x 4096            rows                6.6   8.8
+//   16 x 11008 x 4096           32x64, two sets    10.4  11.7 / 13.9 (rows)
+//   333 x 4096 x 4096, float32  64x128, two sets   22.9  33.1 / 28.1
+// The float32 form runs at half the matrix rate and on more registers: it has
+// its own times, and no 256 x 256 tile.
+namespace {
+enum Kind { kRows, k32x64, k64x64, k64x128, k128x128, k256x256, kKinds };
+struct Times {
+  int tm, tn;
+  float step, step2;
+};
+constexpr Times kTimes[2][kKinds] = {
+    {{16, 16, 0, 0}, {32, 64, .155f, .30f}, {64, 64, .23f, .43f}, {64, 128, .362f, .62f},
+     {128, 128, .55f, .92f}, {256, 256, 1.80f, 0}},
+    {{16, 16, 0, 0}, {32, 64, .24f, .50f}, {64, 64, .37f, .75f}, {64, 128, .58f, 1.15f},
+     {128, 128, .94f, 1.80f}, {0, 0, 0, 0}}};
+
+// Tiles of tm rows to expect: what E ranges of equal size need, and half a tile more
+// for each where sizes differ.
+double expected_tiles(const ArFp8Gemm& g, int tm) {
+  if (!g.offsets) return (double)((g.R + tm - 1) / tm);
+  const double used = (double)(g.E < g.R ? g.E : g.R);
+  const double t = (double)g.R / tm + 0.5 * used;
+  return t > used ? t : used;
+}
+
+struct Plan {
+  Kind kind;
+  bool two;   // two K sets
+};
+Plan plan_of(const ArFp8Gemm& g) {
+  const double K = (double)g.K, N = (double)g.N, KB = (double)((g.K + BLK - 1) / BLK);
+  const double used = (double)(g.E < g.R ? g.E : g.R);
+  const double memory = (used * N + (double)g.R) * K / 5.3e6;
+  Plan best{kRows, false};
+  double least = -1.0;
+  // rows: every tile of 16 rows streams W at 5.8 TB/s, less X's share of the loads
+  const double mean = (double)g.R / used;
+  if (mean <= 64) {
+    const double share = 1.0 + 0.4 * (mean < 16 ? mean : 16) / 16;
+    const double stream = expected_tiles(g, 16) * N * K * share / 5.8e6, chain = KB / 8 * 0.45;
+    least = 3.0 + (stream > chain ? stream : chain);
+  }
+  for (int k = k32x64; k < kKinds; ++k) {
+    const Times& c = kTimes[g.ydt == AR_F32][k];
+    if (!c.tm) continue;
+    const double t = expected_tiles(g, c.tm) * (double)((g.N + c.tn - 1) / c.tn);
+    const bool two = c.step2 > 0 && t <= 256;
+    double us = two ? 4.0 + 0.5 * (KB + 1) * c.step2 : 3.0 + KB * c.step * ceil(t / 256);
+    const double cache = 3.0 + t * KB * (c.tm + c.tn) * BLK / 14e6;
+    if (us < 3.0 + memory) us = 3.0 + memory;
+    if (us < cache) us = cache;
+    if (least < 0 || us < least) {
+      least = us;
+      best = Plan{(Kind)k, two};
+    }
+  }
+  return best;
+}
+}  // namespace
+
+template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
 static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
-  typedef Tile<WM, WN, MB, NA, NS> C;
+  typedef Tile<WM, WN, MB, NA, NS, KG> C;
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
   if (tilesM * tilesN >= (int64_t(1) << 22)) return AR_ERR_SHAPE;
-  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, WIDE>);
+  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>);
   if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess)
     return AR_ERR_HIP;
-  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, WIDE>), dim3((unsigned)(tilesM * tilesN)),
-                     dim3(64 * WM * WN), C::LDS, st, a, (int)tilesN);
+  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>), dim3((unsigned)(tilesM * tilesN)),
+                     dim3(C::THREADS), C::LDS, st, a, (int)tilesN);
   return last_status();
 }
 
-template <int MT>
 static ar_status rows_launch(const Args& a, int64_t tilesM, hipStream_t st) {
   const dim3 g((unsigned)((a.N + 15) / 16), (unsigned)tilesM);
   if (a.ydt == AR_BF16)
-    hipLaunchKernelGGL((k_fp8_rows<MT, false>), g, dim3(64 * DW), 0, st, a);
+    hipLaunchKernelGGL((k_fp8_rows<false>), g, dim3(64 * DW), 0, st, a);
   else
-    hipLaunchKernelGGL((k_fp8_rows<MT, true>), g, dim3(64 * DW), 0, st, a);
+    hipLaunchKernelGGL((k_fp8_rows<true>), g, dim3(64 * DW), 0, st, a);
   return last_status();
 }
 
+template <int WM, int WN, int MB, int NA, int NS1, int NS2>
+static ar_status tile_pick(const Args& a, int64_t tilesM, bool two, hipStream_t st) {
+  if (a.ydt == AR_F32)
+    return two ? tile_launch<WM, WN, MB, NA, NS2, 2, true>(a, tilesM, st)
+               : tile_launch<WM, WN, MB, NA, NS1, 1, true>(a, tilesM, st);
+  return two ? tile_launch<WM, WN, MB, NA, NS2, 2, false>(a, tilesM, st)
+             : tile_launch<WM, WN, MB, NA, NS1, 1, false>(a, tilesM, st);
+}
+
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
-  Args a{g.X, g.xs, g.W, g.ws, g.offsets, g.row_index, g.Y, g.ydt, g.T, g.R, g.N, g.K, (int)g.E,
-         (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
-  const int64_t mean = (g.R + g.E - 1) / g.E;
-  auto tiles = [&](int64_t TM) {
-    return g.offsets ? max_tiles(g.R, g.E, TM) : (g.R + TM - 1) / TM;
-  };
-  if (mean <= 16) return rows_launch<1>(a, tiles(16), st);
-  if (mean <= 64) return rows_launch<4>(a, tiles(64), st);
-  if (g.ydt == AR_F32) return tile_launch<2, 2, 4, 4, 2, true>(a, tiles(128), st);
-  if (tiles(256) * ((g.N + 255) / 256) >= 256) return tile_launch<4, 2, 4, 8, 2, false>(a, tiles(256), st);
-  return tile_launch<2, 2, 4, 4, 2, false>(a, tiles(128), st);
+  const Args a{g.X, g.xs, g.W, g.ws, g.offsets, g.row_index, g.Y, g.ydt, g.T, g.R, g.N, g.K,
+               (int)g.E, (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
+  const Plan p = plan_of(g);
+  const int tm = kTimes[g.ydt == AR_F32][p.kind].tm;
+  const int64_t tiles = g.offsets ? max_tiles(g.R, g.E, tm) : (g.R + tm - 1) / tm;
+  switch (p.kind) {
+    case kRows: return rows_launch(a, tiles, st);
+    case k32x64: return tile_pick<2, 2, 1, 2, 4, 4>(a, tiles, p.two, st);
+    case k64x64: return tile_pick<2, 2, 2, 2, 4, 4>(a, tiles, p.two, st);
+    case k64x128: return tile_pick<2, 2, 2, 4, 3, 3>(a, tiles, p.two, st);
+    case k128x128: return tile_pick<2, 2, 4, 4, 2, 2>(a, tiles, p.two, st);
+    default: return tile_launch<4, 2, 4, 8, 2, 1, false>(a, tiles, st);
+  }
 }

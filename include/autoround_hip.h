@@ -285,12 +285,10 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
 /* Y [M, N] = Σ_j xs[j, m]·ws[n/128, j]·Σ_{k in block j} Xq[m, k]·Wq[n, k]: Xq
    [M, K] with xs [KB, M] (ar_fp8_quant_act or ar_rmsnorm_fp8), Wq [N, K] with ws
    [NB, KB] (ar_fp8_quant_weight, E = 1). float32 accumulation, in a fixed order;
-   ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE. ws_buf:
-   ar_fp8_gemm_workspace_size bytes (may be 0: NULL then). */
-ar_status ar_fp8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+   ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE. No
+   workspace. */
 ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
-                      const float* ws, int64_t N, void* Y, int32_t ydt, void* ws_buf,
-                      size_t ws_bytes, void* stream);
+                      const float* ws, int64_t N, void* Y, int32_t ydt, void* stream);
 
 /* The product by expert: rows offsets[e] <= r < offsets[e+1] of Y [R, N] are
    X_row(r)·Wq[e]ᵀ as above, with Wq [E, N, K], ws [E, NB, KB], Xq [T, K], xs [KB, T].
@@ -302,14 +300,12 @@ ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, 
    are not checked on the host: offsets outside [0, R] are clamped to it, and
    with decreasing ones the rows of Y are unspecified, but nothing outside the
    arrays is read or written. 1 <= E <= 8192; with row_index T*K < 2^32. R = 0
-   or N = 0 is a no-op. No host synchronisation: the call can be captured in a
-   HIP graph and replayed with other offsets. */
-ar_status ar_fp8_gemm_grouped_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K,
-                                             size_t* bytes);
+   or N = 0 is a no-op. No workspace and no host synchronisation: the call can be
+   captured in a HIP graph and replayed with other offsets. */
 ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int64_t K,
                               const uint8_t* Wq, const float* ws, int64_t E, int64_t N,
                               const int32_t* offsets, const int32_t* row_index, int64_t R, void* Y,
-                              int32_t ydt, void* ws_buf, size_t ws_bytes, void* stream);
+                              int32_t ydt, void* stream);
 
 /* ---- Sequential block-wise tuning with quantized inputs --------------------
    [LLMC] tuning loop (each Linear of a subgraph tuned in turn on its captured

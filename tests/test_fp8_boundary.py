@@ -11,7 +11,7 @@ pytestmark = pytest.mark.skipif(
     torch.cuda.is_available(),
     reason="validation-only tests pass fake device pointers; they run on a host without a GPU")
 
-OK, INV, UNSUP, SHAPE, WS = 0, 1, 2, 3, 4
+OK, INV, UNSUP, SHAPE = 0, 1, 2, 3
 P = ctypes.c_void_p(0x100000)          # fake, 16-byte aligned, never dereferenced
 P4 = ctypes.c_void_p(0x100004)         # 4-byte aligned
 P2 = ctypes.c_void_p(0x100002)
@@ -61,13 +61,12 @@ def test_rmsnorm_validation():
     assert norm(M=0) == norm(D=0) == OK
 
 
-def gemm(X=P, xs=P, M=4, K=128, W=P, ws=P, N=64, Y=P, ydt=1, wsb=P, nb=1 << 30):
-    return ar.lib.ar_fp8_gemm(X, xs, M, K, W, ws, N, Y, ydt, wsb, nb, NULL)
+def gemm(X=P, xs=P, M=4, K=128, W=P, ws=P, N=64, Y=P, ydt=1):
+    return ar.lib.ar_fp8_gemm(X, xs, M, K, W, ws, N, Y, ydt, NULL)
 
 
-def grouped(X=P, xs=P, T=4, K=128, W=P, ws=P, E=2, N=64, off=P, idx=NULL, R=4, Y=P, ydt=1, wsb=P,
-            nb=1 << 30):
-    return ar.lib.ar_fp8_gemm_grouped(X, xs, T, K, W, ws, E, N, off, idx, R, Y, ydt, wsb, nb, NULL)
+def grouped(X=P, xs=P, T=4, K=128, W=P, ws=P, E=2, N=64, off=P, idx=NULL, R=4, Y=P, ydt=1):
+    return ar.lib.ar_fp8_gemm_grouped(X, xs, T, K, W, ws, E, N, off, idx, R, Y, ydt, NULL)
 
 
 @pytest.mark.parametrize("f", [gemm, grouped])
@@ -96,18 +95,3 @@ def test_grouped_validation():
         assert grouped(**kw) == INV
     assert grouped(T=0, R=0) == grouped(T=9, idx=P, R=0) == OK
 
-
-def test_workspace_sizes():
-    out = ctypes.c_size_t()
-    f, g = ar.lib.ar_fp8_gemm_workspace_size, ar.lib.ar_fp8_gemm_grouped_workspace_size
-    assert f(4, 64, 128, NULL) == g(2, 4, 64, 128, NULL) == INV
-    assert f(4, 64, 120, ctypes.byref(out)) == g(0, 4, 64, 128, ctypes.byref(out)) == SHAPE
-    assert f(0, 64, 128, ctypes.byref(out)) == OK and out.value == 0
-    for M in (1, 16, 333, 16384):
-        assert f(M, 4096, 4096, ctypes.byref(out)) == OK
-        n = out.value
-        assert n == ar.fp8_gemm_workspace_size(M, 4096, 4096) and n % 256 == 0
-        if n:                                # too small a workspace, or none
-            assert gemm(M=M, N=4096, K=4096, nb=n - 1) == WS
-            assert gemm(M=M, N=4096, K=4096, wsb=NULL, nb=n) == INV
-            assert gemm(M=M, N=4096, K=4096, wsb=P4, nb=n) == INV

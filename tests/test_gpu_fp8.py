@@ -343,13 +343,11 @@ def test_grouped_under_graph_capture():
         ops, _, _, offd, idxd, R = grouped_case(counts, 320, 384, True, 11)
         Y = torch.zeros((R, 320), device=dev())
         ar.fp8_gemm_grouped(*ops, offd, row_index=idxd, out=Y)
-        need = ar.fp8_gemm_grouped_workspace_size(len(counts), R, 320, 384)
-        ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device=dev())
         torch.cuda.synchronize()
         g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
         with torch.cuda.stream(s):
             with torch.cuda.graph(g, stream=s):
-                ar.fp8_gemm_grouped(*ops, offd, row_index=idxd, out=Y, workspace=ws)
+                ar.fp8_gemm_grouped(*ops, offd, row_index=idxd, out=Y)
         torch.cuda.synchronize()
         for i in range(4):
             c = counts if i % 2 else more
@@ -505,8 +503,7 @@ def test_refusals():
     for args in bad:
         with pytest.raises(ValueError):
             ar.fp8_gemm(*args)
-    for kw in (dict(out=z(M, N + 1)), dict(out=z(M, N, d=torch.float16)),
-               dict(workspace=z(16))):
+    for kw in (dict(out=z(M, N + 1)), dict(out=z(M, N, d=torch.float16))):
         with pytest.raises(ValueError):
             ar.fp8_gemm(xq, xs, wq, ws, **kw)
     with pytest.raises(TypeError):
