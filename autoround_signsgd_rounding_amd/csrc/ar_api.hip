@@ -1024,6 +1024,7 @@ ar_status ar_fp8_quant_act(int32_t xdt, const void* X, int32_t gate, int64_t M, 
   if (gate != 0 && gate != 1) return AR_ERR_INVALID_ARG;
   AR_TRY(check_fp8_rows(M, K));
   if (M == 0 || K == 0) return AR_OK;
+  if (M * K >= int64_t(1) << 36) return AR_ERR_SHAPE;   // workgroups of one launch
   if (!X || !q || !scale || !a16(X) || !a16(q) || !a4(scale)) return AR_ERR_INVALID_ARG;
   return ar_launch_fp8_quant_act(xdt, X, gate, M, K, q, scale, static_cast<hipStream_t>(stream));
 }

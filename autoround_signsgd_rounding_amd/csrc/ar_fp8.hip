@@ -3,7 +3,7 @@
 // ar_fp8_gemm.hip.
 //
 // One scale per block of values, s = amax/448 (448 is the largest e4m3 value),
-// 1 for a block of zeros and never below 2^-126; a code is e4m3(x · (1/s)),
+// 1 for a block of zeros and never below 2^-126; a code is e4m3(x · (1/s)), 1/s good to 1 ulp,
 // round to nearest even. |x·(1/s)| exceeds 448 by float32 roundings only, far
 // less than the half step of 16 that would round away from 448, so nothing
 // has to be clamped. A NaN becomes a NaN code and leaves the scale alone; an
@@ -11,6 +11,8 @@
 // Activations: a block is 128 channels of one row, scales [KB][M] (KB =
 // ceil(K/128)), so a product's tile reads the scales of its rows side by side.
 // Weights: a block is 128 x 128, scales [NB][KB].
+#include <type_traits>
+
 #include "ar_device.h"
 #include "ar_launch.h"
 
@@ -18,64 +20,60 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int BLK = 128;      // channels per scale
-constexpr int CH = 16;        // values per lane: one 16-byte store of codes
+constexpr int CH = 8;         // values per lane: a wave reads 1 KiB of bf16 in one piece
 constexpr int LPB = BLK / CH; // lanes per block row
 
 inline ar_status last_status() { return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP; }
 
-__device__ __forceinline__ void load16(const uint16_t* p, float (&o)[CH]) {
-  const u32x4_t a = reinterpret_cast<const u32x4_t*>(p)[0];
-  const u32x4_t b = reinterpret_cast<const u32x4_t*>(p)[1];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = __uint_as_float(a[i] << 16);
-    o[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-    o[8 + 2 * i] = __uint_as_float(b[i] << 16);
-    o[8 + 2 * i + 1] = __uint_as_float(b[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load16(const float* p, float (&o)[CH]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f32x4_t v = reinterpret_cast<const f32x4_t*>(p)[i];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[4 * i + e] = v[e];
-  }
-}
-__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[CH]) {
-  u32x4_t a, b;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-    b[i] = bf16_pair(v[8 + 2 * i], v[8 + 2 * i + 1]);
-  }
-  reinterpret_cast<u32x4_t*>(p)[0] = a;
-  reinterpret_cast<u32x4_t*>(p)[1] = b;
-}
-__device__ __forceinline__ void store16(float* p, const float (&v)[CH]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<f32x4_t*>(p)[i] = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-}
-
-__device__ __forceinline__ float amax16(const float (&v)[CH]) {
+// Largest magnitude of a block: 8 values of a lane, then the 16 lanes of a DPP
+// row, rotated by 8, 4, 2 and 1. fmaxf drops a NaN.
+__device__ __forceinline__ float amax_row(const float (&v)[CH]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) m = fmaxf(m, fabsf(v[i]));   // fmaxf drops a NaN
+  for (int i = 0; i < CH; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
+  auto turn = [&](auto by) {
+    const int o = __builtin_amdgcn_mov_dpp(__float_as_int(m), 0x120 + decltype(by)::value, 0xF, 0xF,
+                                           true);
+    m = fmaxf(m, __int_as_float(o));
+  };
+  turn(std::integral_constant<int, 8>());
+  turn(std::integral_constant<int, 4>());
+  turn(std::integral_constant<int, 2>());
+  turn(std::integral_constant<int, 1>());
   return m;
 }
+// amax/448, rounded once: the quotient by the reciprocal, corrected by the
+// remainder (an infinite amax has none).
 __device__ __forceinline__ float scale_of(float amax) {
-  return amax == 0.0f ? 1.0f : fmaxf(amax / 448.0f, 0x1p-126f);
+  constexpr float R = 1.0f / 448.0f;
+  const float q0 = amax * R;
+  const float q = fmaf(fmaf(-q0, 448.0f, amax), R, q0);
+  const float s = amax < __builtin_inff() ? fmaxf(q, 0x1p-126f) : amax;
+  return amax == 0.0f ? 1.0f : s;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[CH], float inv) {
-  u32x4_t o;
+// Outputs are stored past the caches, whole 512-byte or 1-KiB pieces a wave:
+// measured on a 16384 x 8192 norm 186 us instead of 197, on a 29568 x 8192 weight
+// 124 instead of 134; a 1 x 4096 norm takes as long either way.
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[CH], float s) {
+  const float inv = __builtin_amdgcn_rcpf(s);   // 1 ulp; s is a normal number or infinite
+  u32x2_t o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, w, true);
     o[i] = (uint32_t)w;
   }
-  *reinterpret_cast<u32x4_t*>(p) = o;
+  __builtin_nontemporal_store(o, reinterpret_cast<u32x2_t*>(p));
+}
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[CH]) {
+  __builtin_nontemporal_store(u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                      bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
+                              reinterpret_cast<u32x4_t*>(p));
+}
+__device__ __forceinline__ void store_row(float* p, const float (&v)[CH]) {
+  f32x4_t* d = reinterpret_cast<f32x4_t*>(p);
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, d);
+  __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, d + 1);
 }
 
 // SiLU(g)·u in float32: the exponential's argument is rounded once (a relative
@@ -86,87 +84,98 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // ------------------------------------------------------------------ activations
-// Eight lanes per (row, block): a workgroup covers 32 rows of `bpw` blocks in
-// turn, so the scales of one block leave as one 128-byte line.
-template <class T, bool GATE>
+// Units of one block of one row, 16 lanes each. A workgroup takes RT rows by BT
+// blocks of them, row by row, a wave four units (1 KiB of bf16) at a time and
+// ITERS times; the scales leave through LDS, the RT rows of a block side by
+// side. ITERS = 1 spreads small inputs over more CUs: 16 x 11008, gated, takes 2.9 us
+// instead of 6.5 at 32 rows a workgroup.
+template <class T, bool GATE, int ITERS>
 __global__ __launch_bounds__(NT) void k_fp8_quant_act(const T* X, int64_t M, int64_t K, uint8_t* q,
-                                                      float* scale, int bpw) {
-  const int64_t m = (int64_t)blockIdx.x * 32 + threadIdx.x / LPB;
-  const int c = threadIdx.x % LPB;
+                                                      float* scale, int RT, int BT,
+                                                      int chunks) {
+  __shared__ float sc[ITERS * NT / LPB];
   const int64_t KB = (K + BLK - 1) / BLK;
-  const int64_t j0 = (int64_t)blockIdx.y * bpw;
-  const int64_t j1 = j0 + bpw < KB ? j0 + bpw : KB;
-  if (m >= M) return;   // all eight lanes of a row
-  const T* xr = X + m * K * (GATE ? 2 : 1);
-  for (int64_t j = j0; j < j1; ++j) {
-    const int64_t k = j * BLK + c * CH;
-    float v[CH];
+  const int mt = blockIdx.x / chunks;   // consecutive workgroups share rows
+  const int64_t j0 = (int64_t)(blockIdx.x - mt * chunks) * BT, m0 = (int64_t)mt * RT;
+  const int c = threadIdx.x % LPB * CH;
+  float v[ITERS][CH], u[ITERS][CH];
+  int64_t at[ITERS];   // offset of the lane's values in q, -1: none
 #pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = 0.0f;
-    if (k < K) {   // K % 16 == 0: a lane's 16 values are wholly in or out
-      load16(xr + k, v);
-      if constexpr (GATE) {
-        float u[CH];
-        load16(xr + K + k, u);
+  for (int i = 0; i < ITERS; ++i) {
+    const int unit = i * (NT / LPB) + threadIdx.x / LPB, r = unit / BT;
+    const int64_t m = m0 + r, k = (j0 + unit - r * BT) * BLK + c;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) v[i] = silu_mul(v[i], u[i]);
-      }
+    for (int e = 0; e < CH; ++e) v[i][e] = u[i][e] = 0.0f;
+    at[i] = -1;
+    if (r < RT && m < M && k < K) {   // K % 16 == 0: the 8 values are in or out
+      at[i] = m * K + k;
+      load8(X + m * K * (GATE ? 2 : 1) + k, v[i]);
+      if constexpr (GATE) load8(X + (2 * m + 1) * K + k, u[i]);
     }
-    const float s = scale_of(group_max<LPB>(amax16(v)));
-    if (k < K) store_codes(q + m * K + k, v, 1.0f / s);
-    if (c == 0) scale[j * M + m] = s;
   }
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    if constexpr (GATE) {
+#pragma unroll
+      for (int e = 0; e < CH; ++e) v[i][e] = silu_mul(v[i][e], u[i][e]);
+    }
+    const float s = scale_of(amax_row(v[i]));
+    if (at[i] >= 0) store_codes(q + at[i], v[i], s);
+    if (threadIdx.x % LPB == 0) sc[i * (NT / LPB) + threadIdx.x / LPB] = s;
+  }
+  __syncthreads();
+  const int b = threadIdx.x / RT, r = threadIdx.x - b * RT;
+  if (b < BT && j0 + b < KB && m0 + r < M) scale[(j0 + b) * M + m0 + r] = sc[r * BT + b];
 }
 
 // ------------------------------------------------------------------ weights
 // One workgroup per 128 x 128 block, held in registers between the maximum and
-// the codes: eight lanes per row, 32 rows at a time.
+// the codes: sixteen lanes per row, 16 rows at a time.
 template <class T>
 __global__ __launch_bounds__(NT) void k_fp8_quant_weight(const T* W, int64_t N, int64_t K,
                                                          uint8_t* q, float* scale, int NB, int KB) {
+  constexpr int PASS = NT / LPB, P = BLK / PASS;   // rows at a time, times
   __shared__ float red[NT / 64];
   const int64_t b = blockIdx.x;
   const int64_t e = b / ((int64_t)NB * KB);
   const int r = (int)(b - e * NB * KB), nb = r / KB, j = r - nb * KB;
   const int64_t k = (int64_t)j * BLK + (threadIdx.x % LPB) * CH;
-  float v[4][CH];
-  float m = 0.0f;
+  const int64_t n0 = (int64_t)nb * BLK + threadIdx.x / LPB;
+  float v[P][CH];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int64_t n = (int64_t)nb * BLK + p * 32 + threadIdx.x / LPB;
+  for (int p = 0; p < P; ++p) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) v[p][i] = 0.0f;
-    if (n < N && k < K) load16(W + (e * N + n) * K + k, v[p]);
+    if (n0 + p * PASS < N && k < K) load8(W + (e * N + n0 + p * PASS) * K + k, v[p]);
   }
+  float m = 0.0f;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) m = fmaxf(m, amax16(v[p]));
-  m = group_max<64>(m);
+  for (int p = 0; p < P; ++p) m = fmaxf(m, amax_row(v[p]));
+  m = fmaxf(m, __shfl_xor(m, 16, 64));
+  m = fmaxf(m, __shfl_xor(m, 32, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
   const float s = scale_of(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-  const float inv = 1.0f / s;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int64_t n = (int64_t)nb * BLK + p * 32 + threadIdx.x / LPB;
-    if (n < N && k < K) store_codes(q + (e * N + n) * K + k, v[p], inv);
-  }
+  for (int p = 0; p < P; ++p)
+    if (n0 + p * PASS < N && k < K) store_codes(q + (e * N + n0 + p * PASS) * K + k, v[p], s);
   if (threadIdx.x == 0) scale[b] = s;
 }
 
 // ------------------------------------------------------------------ RMSNorm
-// One workgroup per row: v = x + residual rounded to T (the stored sum is what
-// is normalised, as the block's separate addition has it), the sum of squares
-// in float64 (the block's norm does the same, and no square of a finite input
-// overflows), y = (v·r)·w in float32, codes from the unrounded y. The row stays
-// in registers (C chunks of 16 values per thread); C = 0 reads it twice.
-// Every thread reads an element before it writes any output at that place, so
-// h may be x or the residual itself.
+// v = x + residual rounded to T (the stored sum is what is normalised, as the
+// block's separate addition has it), the sum of squares in float64 (the block's
+// norm does the same, and no square of a finite input overflows), y = (v·r)·w in
+// float32, codes from the unrounded y. A row is a wave's (four rows to a
+// workgroup; rows of up to 2048) or a workgroup's, and stays in registers, C
+// chunks of 8 values per lane; C = 0 reads it twice. Every lane reads an element
+// before it writes any output at that place, so h may be x or the residual itself.
 template <class T>
 __device__ __forceinline__ void norm_input(const T* x, const T* res, int64_t o, float (&v)[CH]) {
-  load16(x + o, v);
+  load8(x + o, v);
   if (res) {
     float u[CH];
-    load16(res + o, u);
+    load8(res + o, u);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       v[i] += u[i];
@@ -174,6 +183,25 @@ __device__ __forceinline__ void norm_input(const T* x, const T* res, int64_t o, 
     }
   }
 }
+
+// Eight values of T as they lie in memory.
+template <class T>
+struct RowOf {
+  u32x4_t raw[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = reinterpret_cast<const u32x4_t*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float (&o)[CH]) const {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if constexpr (sizeof(T) == 4)
+        o[i] = __uint_as_float(raw[i / 4][i % 4]);
+      else
+        o[i] = __uint_as_float(i % 2 ? raw[0][i / 2] & 0xFFFF0000u : raw[0][i / 2] << 16);
+    }
+  }
+};
 
 struct NormArgs {
   const void *x, *res, *w;
@@ -184,20 +212,23 @@ struct NormArgs {
   float eps;
 };
 
-template <class T, int THREADS, int C>
-__global__ __launch_bounds__(THREADS) void k_rmsnorm_fp8(NormArgs a) {
-  __shared__ double red[THREADS / 64];
+template <class T, int LANES, int C>   // LANES per row: 64 or NT
+__global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
+  __shared__ double red[NT / 64];
+  constexpr int ROWS = NT / LANES;
   // consecutive rows on one XCD, whose L2 then joins their scales (4 bytes a
   // row) into whole lines
   const int64_t per = gridDim.x >> 3, rem = gridDim.x & 7;
   const int64_t xcd = blockIdx.x & 7;
-  const int64_t m = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+  const int64_t g = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+  const int64_t m = g * ROWS + threadIdx.x / LANES;
+  if (m >= a.M) return;   // whole waves (ROWS > 1 has no barrier below)
   const T *x = static_cast<const T*>(a.x) + m * a.D;
   const T *res = a.res ? static_cast<const T*>(a.res) + m * a.D : nullptr;
   const T* w = static_cast<const T*>(a.w);
-  const int t = threadIdx.x;
-  constexpr int NC = C > 0 ? C : 1;
-  float v[NC][CH];
+  const int t = threadIdx.x % LANES;
+  float v[C > 0 ? C : 1][CH];
+  RowOf<T> wr[C > 0 ? C : 1];   // w, requested with x so that it is there after the sum
   double ss = 0.0;
   auto add = [&](const float (&u)[CH]) {
 #pragma unroll
@@ -206,104 +237,118 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_fp8(NormArgs a) {
   if constexpr (C > 0) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t k = ((int64_t)c * THREADS + t) * CH;
+      const int64_t k = ((int64_t)c * LANES + t) * CH;
       if (k < a.D) {
+        wr[c].load(w + k);
         norm_input(x, res, k, v[c]);
         add(v[c]);
       }
     }
   } else {
-    for (int64_t k = (int64_t)t * CH; k < a.D; k += THREADS * CH) {
+    for (int64_t k = (int64_t)t * CH; k < a.D; k += LANES * CH) {
       norm_input(x, res, k, v[0]);
       add(v[0]);
     }
   }
   ss = group_sum_f64<64>(ss);
-  if constexpr (THREADS > 64) {
+  if constexpr (LANES > 64) {
     if ((t & 63) == 0) red[t >> 6] = ss;
     __syncthreads();
-    ss = red[0];
-#pragma unroll
-    for (int i = 1; i < THREADS / 64; ++i) ss += red[i];
+    ss = ((red[0] + red[1]) + red[2]) + red[3];
   }
   const float r = (float)(1.0 / sqrt(ss / (double)a.D + (double)a.eps));
-  const int64_t KB = (a.D + BLK - 1) / BLK;
-  auto finish = [&](int64_t k, float (&u)[CH]) {
+  auto finish = [&](int64_t k, const float (&u)[CH], const RowOf<T>& wv) {
     const bool in = k < a.D;
     float y[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) y[i] = 0.0f;
     if (in) {
-      if (a.h) store16(static_cast<T*>(a.h) + m * a.D + k, u);
-      float g[CH];
-      load16(w + k, g);
+      if (a.h) store_row(static_cast<T*>(a.h) + m * a.D + k, u);
+      wv.get(y);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) y[i] = (u[i] * r) * g[i];
-      if (a.y) store16(static_cast<T*>(a.y) + m * a.D + k, y);
+      for (int i = 0; i < CH; ++i) y[i] = (u[i] * r) * y[i];
+      if (a.y) store_row(static_cast<T*>(a.y) + m * a.D + k, y);
     }
-    const float s = scale_of(group_max<LPB>(amax16(y)));
-    if (in) store_codes(a.q + m * a.D + k, y, 1.0f / s);
-    if (k / BLK < KB && k % BLK == 0) a.scale[(k / BLK) * a.M + m] = s;
+    const float s = scale_of(amax_row(y));
+    if (in) store_codes(a.q + m * a.D + k, y, s);
+    if (in && t % LPB == 0) a.scale[(k / BLK) * a.M + m] = s;
   };
   if constexpr (C > 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) finish(((int64_t)c * THREADS + t) * CH, v[c]);
+    for (int c = 0; c < C; ++c) finish(((int64_t)c * LANES + t) * CH, v[c], wr[c]);
   } else {
-    // whole rounds, so that the eight lanes of a block stay together
-    for (int64_t k = (int64_t)t * CH; k - t * CH < a.D; k += THREADS * CH) {
-      if (k < a.D) norm_input(x, res, k, v[0]);
-      finish(k, v[0]);
+    // whole rounds, so that the lanes of a block stay together
+    for (int64_t k = (int64_t)t * CH; k - t * CH < a.D; k += LANES * CH) {
+      if (k < a.D) {
+        wr[0].load(w + k);
+        norm_input(x, res, k, v[0]);
+      }
+      finish(k, v[0], wr[0]);
     }
   }
 }
 
+template <class T, int LANES, int C>
+void norm_go(const NormArgs& a, hipStream_t st) {
+  constexpr int ROWS = NT / LANES;
+  hipLaunchKernelGGL((k_rmsnorm_fp8<T, LANES, C>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)),
+                     dim3(NT), 0, st, a);
+}
 template <class T>
 ar_status norm_launch(const NormArgs& a, hipStream_t st) {
-  const dim3 g((unsigned)a.M);
-  if (a.D <= 64 * CH)
-    hipLaunchKernelGGL((k_rmsnorm_fp8<T, 64, 1>), g, dim3(64), 0, st, a);
-  else if (a.D <= 256 * CH)
-    hipLaunchKernelGGL((k_rmsnorm_fp8<T, 256, 1>), g, dim3(256), 0, st, a);
-  else if (a.D <= 512 * CH)
-    hipLaunchKernelGGL((k_rmsnorm_fp8<T, 256, 2>), g, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_rmsnorm_fp8<T, 256, 0>), g, dim3(256), 0, st, a);
+  const int64_t D = a.D;
+  if (D <= 512) norm_go<T, 64, 1>(a, st);
+  else if (D <= 1024) norm_go<T, 64, 2>(a, st);
+  else if (D <= 2048) norm_go<T, 64, 4>(a, st);
+  else if (D <= 4096) norm_go<T, NT, 2>(a, st);
+  else if (D <= 8192) norm_go<T, NT, 4>(a, st);
+  else if (D <= 16384) norm_go<T, NT, 8>(a, st);
+  else norm_go<T, NT, 0>(a, st);
   return last_status();
 }
 
+template <class T, bool GATE, int ITERS>
+ar_status act_go(const void* X, int64_t M, int64_t K, uint8_t* q, float* scale, hipStream_t st) {
+  constexpr int UNITS = ITERS * NT / LPB;
+  const int64_t KB = (K + BLK - 1) / BLK;
+  int RT = 1;
+  while (RT < 16 && RT < M) RT *= 2;
+  const int BT = (int)(KB < UNITS / RT ? KB : UNITS / RT);
+  RT = UNITS / BT;
+  const int64_t chunks = (KB + BT - 1) / BT, n = chunks * ((M + RT - 1) / RT);
+  if (n >= int64_t(1) << 24) return AR_ERR_SHAPE;
+  hipLaunchKernelGGL((k_fp8_quant_act<T, GATE, ITERS>), dim3((unsigned)n), dim3(NT), 0, st,
+                     static_cast<const T*>(X), M, K, q, scale, RT, BT, (int)chunks);
+  return last_status();
+}
 template <class T, bool GATE>
-void act_launch(const void* X, int64_t M, int64_t K, uint8_t* q, float* scale, hipStream_t st) {
-  const int64_t KB = (K + BLK - 1) / BLK, rows = (M + 31) / 32;
-  // four blocks per workgroup where that still leaves enough of them for 256 CUs
-  const int bpw = rows * KB >= 4 * 2048 ? 4 : 1;
-  hipLaunchKernelGGL((k_fp8_quant_act<T, GATE>), dim3((unsigned)rows, (unsigned)((KB + bpw - 1) / bpw)),
-                     dim3(NT), 0, st, static_cast<const T*>(X), M, K, q, scale, bpw);
+ar_status act_launch(const void* X, int64_t M, int64_t K, uint8_t* q, float* scale, hipStream_t st) {
+  return M * K <= 1024 * 16 * BLK ? act_go<T, GATE, 1>(X, M, K, q, scale, st)
+                                  : act_go<T, GATE, 4>(X, M, K, q, scale, st);
+}
+template <class T>
+void weight_launch(const void* W, int64_t E, int64_t N, int64_t K, uint8_t* q, float* scale,
+                   hipStream_t st) {
+  const int64_t NB = (N + BLK - 1) / BLK, KB = (K + BLK - 1) / BLK;
+  hipLaunchKernelGGL((k_fp8_quant_weight<T>), dim3((unsigned)(E * NB * KB)), dim3(NT), 0, st,
+                     static_cast<const T*>(W), N, K, q, scale, (int)NB, (int)KB);
 }
 
 }  // namespace
 
 ar_status ar_launch_fp8_quant_act(int xdt, const void* X, int gate, int64_t M, int64_t K,
                                   uint8_t* q, float* scale, hipStream_t st) {
-  if (xdt == AR_BF16) {
-    if (gate) act_launch<uint16_t, true>(X, M, K, q, scale, st);
-    else act_launch<uint16_t, false>(X, M, K, q, scale, st);
-  } else {
-    if (gate) act_launch<float, true>(X, M, K, q, scale, st);
-    else act_launch<float, false>(X, M, K, q, scale, st);
-  }
-  return last_status();
+  if (xdt == AR_BF16)
+    return gate ? act_launch<uint16_t, true>(X, M, K, q, scale, st)
+                : act_launch<uint16_t, false>(X, M, K, q, scale, st);
+  return gate ? act_launch<float, true>(X, M, K, q, scale, st)
+              : act_launch<float, false>(X, M, K, q, scale, st);
 }
 
 ar_status ar_launch_fp8_quant_weight(int wdt, const void* W, int64_t E, int64_t N, int64_t K,
                                      uint8_t* q, float* scale, hipStream_t st) {
-  const int64_t NB = (N + BLK - 1) / BLK, KB = (K + BLK - 1) / BLK;
-  const dim3 g((unsigned)(E * NB * KB));
-  if (wdt == AR_BF16)
-    hipLaunchKernelGGL((k_fp8_quant_weight<uint16_t>), g, dim3(NT), 0, st,
-                       static_cast<const uint16_t*>(W), N, K, q, scale, (int)NB, (int)KB);
-  else
-    hipLaunchKernelGGL((k_fp8_quant_weight<float>), g, dim3(NT), 0, st,
-                       static_cast<const float*>(W), N, K, q, scale, (int)NB, (int)KB);
+  if (wdt == AR_BF16) weight_launch<uint16_t>(W, E, N, K, q, scale, st);
+  else weight_launch<float>(W, E, N, K, q, scale, st);
   return last_status();
 }
 

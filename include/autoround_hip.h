@@ -255,13 +255,13 @@ ar_status ar_dequant_gemm(int32_t bits, int32_t group_size, const uint16_t* X, i
 
    Scale of a block: s = 1 if its largest magnitude amax is 0, else
    max(amax/448, 2^-126); code = e4m3(x·(1/s)), round to nearest even, float32
-   steps. A NaN gives a NaN code and does not enter amax. An infinity makes s
+   steps (1/s to one unit in the last place). A NaN gives a NaN code and does not enter amax. An infinity makes s
    infinite and its own code NaN, and with s every product of the block NaN. */
 
 /* Activations: q [M, K], scale [KB, M] (one row of scales per block of 128
    channels). gate = 0: the codes of X [M, K]. gate = 1: X is [M, 2K] and the
    codes are those of SiLU(X[:, :K])·X[:, K:], computed in float32 and not rounded
-   before. xdt: AR_F32 or AR_BF16. M*K = 0 is a no-op. */
+   before. xdt: AR_F32 or AR_BF16. M*K = 0 is a no-op; M*K < 2^36. */
 ar_status ar_fp8_quant_act(int32_t xdt, const void* X, int32_t gate, int64_t M, int64_t K,
                            uint8_t* q, float* scale, void* stream);
 
