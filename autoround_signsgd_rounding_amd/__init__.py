@@ -577,7 +577,7 @@ def _on(stream, *tensors):
                 if t is not None:
                     t.record_stream(stream)
         return torch.cuda.stream(stream)
-    return _HERE_AND_NOW if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE_AND_NOW if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _stream_of(t) -> int:
@@ -668,7 +668,7 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
 
 
 def _fp8_operands(Xq, xs, Wq, ws, dims: int):
-    """Shapes of the two operands and their scales, checked."""
+    """(T, K, N) of the two operands, checked with their scales."""
     torch = _torch()
     f8, f32 = torch.float8_e4m3fn, torch.float32
     if Xq is None or Xq.dim() != 2:
@@ -676,13 +676,20 @@ def _fp8_operands(Xq, xs, Wq, ws, dims: int):
     if Wq is None or Wq.dim() != dims:
         raise ValueError("Wq must be a [%sN, K] tensor" % ("E, " if dims == 3 else ""))
     T, K = Xq.shape
-    lead, N = Wq.shape[:-2], Wq.shape[-2]
+    *lead, N, KW = Wq.shape
     KB = _fp8_scales(K)
-    _want(Xq, "Xq", (T, K), f8)
-    _want(xs, "xs", (KB, T), f32)
-    _want(Wq, "Wq", (*lead, N, K), f8)
-    _want(ws, "ws", (*lead, _fp8_scales(N), KB), f32)
-    return T, K, N
+    scales = (*lead, _fp8_scales(N), KB)
+    if KW == K and xs is not None and ws is not None and xs.shape == (KB, T) and \
+            ws.shape == scales and Xq.dtype is f8 and Wq.dtype is f8 and xs.dtype is f32 and \
+            ws.dtype is f32 and Xq.is_cuda and xs.is_cuda and Wq.is_cuda and ws.is_cuda and \
+            Xq.is_contiguous() and xs.is_contiguous() and Wq.is_contiguous() and \
+            ws.is_contiguous():
+        return T, K, N
+    _need(Xq, "Xq", (T, K), f8)             # one of these says what is wrong
+    _need(xs, "xs", (KB, T), f32)
+    _need(Wq, "Wq", (*lead, N, K), f8)
+    _need(ws, "ws", scales, f32)
+    raise ValueError("operands do not match")
 
 
 def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):

@@ -166,10 +166,10 @@ __global__ __launch_bounds__(NT) void k_fp8_quant_weight(const T* W, int64_t N, 
 // v = x + residual rounded to T (the stored sum is what is normalised, as the
 // block's separate addition has it), the sum of squares in float64 (the block's
 // norm does the same, and no square of a finite input overflows), y = (v·r)·w in
-// float32, codes from the unrounded y. A row is a wave's (four rows to a
-// workgroup; rows of up to 2048) or a workgroup's, and stays in registers, C
-// chunks of 8 values per lane; C = 0 reads it twice. Every lane reads an element
-// before it writes any output at that place, so h may be x or the residual itself.
+// float32, codes from the unrounded y. A row of up to 2048 is a wave's or a part
+// of a wave's, a longer one a workgroup's. It stays in registers, C chunks of 8
+// values per lane; C = 0 reads it twice. Every lane reads an element before it
+// writes any output at that place, so h may be x or the residual itself.
 template <class T>
 __device__ __forceinline__ void norm_input(const T* x, const T* res, int64_t o, float (&v)[CH]) {
   load8(x + o, v);
@@ -212,7 +212,7 @@ struct NormArgs {
   float eps;
 };
 
-template <class T, int LANES, int C>   // LANES per row: 64 or NT
+template <class T, int LANES, int C>   // LANES per row: 16, 32, 64 or NT
 __global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
   __shared__ double red[NT / 64];
   constexpr int ROWS = NT / LANES;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
   const int64_t xcd = blockIdx.x & 7;
   const int64_t g = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
   const int64_t m = g * ROWS + threadIdx.x / LANES;
-  if (m >= a.M) return;   // whole waves (ROWS > 1 has no barrier below)
+  if (m >= a.M) return;   // whole rows (ROWS > 1 has no barrier below)
   const T *x = static_cast<const T*>(a.x) + m * a.D;
   const T *res = a.res ? static_cast<const T*>(a.res) + m * a.D : nullptr;
   const T* w = static_cast<const T*>(a.w);
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
       add(v[0]);
     }
   }
-  ss = group_sum_f64<64>(ss);
+  ss = group_sum_f64<LANES < 64 ? LANES : 64>(ss);
   if constexpr (LANES > 64) {
     if ((t & 63) == 0) red[t >> 6] = ss;
     __syncthreads();
@@ -297,7 +297,9 @@ void norm_go(const NormArgs& a, hipStream_t st) {
 template <class T>
 ar_status norm_launch(const NormArgs& a, hipStream_t st) {
   const int64_t D = a.D;
-  if (D <= 512) norm_go<T, 64, 1>(a, st);
+  if (D <= 128) norm_go<T, 16, 1>(a, st);
+  else if (D <= 256) norm_go<T, 32, 1>(a, st);
+  else if (D <= 512) norm_go<T, 64, 1>(a, st);
   else if (D <= 1024) norm_go<T, 64, 2>(a, st);
   else if (D <= 2048) norm_go<T, 64, 4>(a, st);
   else if (D <= 4096) norm_go<T, NT, 2>(a, st);

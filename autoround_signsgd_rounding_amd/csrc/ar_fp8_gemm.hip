@@ -16,6 +16,7 @@
 // over, so any will do).
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "ar_device.h"
@@ -660,9 +661,17 @@ static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
   if (tilesM * tilesN >= (int64_t(1) << 22)) return AR_ERR_SHAPE;
-  const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>);
-  if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess)
-    return AR_ERR_HIP;
+  // more than the default 64 KiB of LDS has to be asked for, once per device
+  static std::atomic<uint64_t> asked{0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return AR_ERR_HIP;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
+    const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>);
+    if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess)
+      return AR_ERR_HIP;
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
   hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>), dim3((unsigned)(tilesM * tilesN)),
                      dim3(C::THREADS), C::LDS, st, a, (int)tilesN);
   return last_status();
