@@ -560,6 +560,15 @@ def _want(t, name, shape, dtype):
         _need(t, name, shape, dtype)
 
 
+def _matrix(t, name):
+    """_weight, with a quick look first."""
+    torch = _torch()
+    if t is None or t.dim() != 2 or not t.is_cuda or not t.is_contiguous() or \
+            (t.dtype is not torch.bfloat16 and t.dtype is not torch.float32):
+        _weight(t, name)
+    return t.shape
+
+
 def _on(stream, *tensors):
     """Context in which a call on these tensors allocates and launches: their
     device, and ``stream`` (its current stream if None). ValueError when the
@@ -600,13 +609,14 @@ def fp8_quant_act(X, *, gate: bool = False, stream=None):
     ``gate``: X is [M, 2K], the gate and the up half side by side, and the codes
     are those of SiLU(gate)·up."""
     torch = _torch()
-    M, K = _weight(X, "X")
+    M, K = _matrix(X, "X")
     if gate:
         if K % 2:
             raise ValueError("gate needs an even number of channels")
         K //= 2
     with _on(stream, X):
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device) if gate else \
+            torch.empty_like(X, dtype=torch.float8_e4m3fn)
         s = torch.empty((_fp8_scales(K), M), dtype=torch.float32, device=X.device)
         _check(lib.ar_fp8_quant_act(_dt(X), _at(X), int(gate), M, K, _at(q), _at(s),
                                     _stream_of(X)), "ar_fp8_quant_act")
@@ -646,7 +656,7 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
     stream is then updated in place); ``want_y`` also returns the norm's output
     in x's dtype."""
     torch = _torch()
-    M, D = _weight(x, "x")
+    M, D = _matrix(x, "x")
     _want(weight, "weight", (D,), x.dtype)
     if residual is not None:
         _want(residual, "residual", (M, D), x.dtype)
@@ -655,7 +665,7 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
             raise ValueError("h_out needs a residual")
         _want(h_out, "h_out", (M, D), x.dtype)
     with _on(stream, x, weight, residual, h_out):
-        q = torch.empty((M, D), dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         s = torch.empty((_fp8_scales(D), M), dtype=torch.float32, device=x.device)
         h = h_out
         if residual is not None and h is None:

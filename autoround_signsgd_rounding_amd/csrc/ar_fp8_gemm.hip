@@ -292,14 +292,18 @@ __device__ __forceinline__ void wait_loads() {
 }
 constexpr uint32_t kNone = 0xFFFFFFF0u;   // past every buffer: the load writes zeros
 
-// Workgroup -> (m tile, n tile). The dispatcher places workgroup w on XCD w mod 8:
-// each XCD gets one contiguous range of the tile sequence, walked in groups of
-// GI tile rows, so the tiles that run on one XCD at a time share operands in its
-// L2.
+// Workgroup -> (m tile, n tile). The dispatcher places workgroup w on XCD w mod 8.
+// The tile sequence walks groups of GI tile rows, column by column; of each 256
+// tiles in a row (one for every CU) an XCD gets 32 neighbours, which share
+// operands in its L2, and all XCDs stay near one place of the sequence, so that
+// what they stream (an expert's W above all) is in the last-level cache when
+// the second one asks. Measured on 8192 tokens, 2 of 8 experts, 11008 x 4096: 746
+// us against 789 with an eighth of the whole sequence per XCD.
 __device__ __forceinline__ void tile_of(int w, int n, int tilesM, int tilesN, int& tm, int& tn) {
-  constexpr int GI = 4;
-  const int xcd = w & 7, q = n >> 3, r = n & 7;
-  const int L = xcd * q + min(xcd, r) + (w >> 3);
+  constexpr int GI = 4, WINDOW = 256;
+  const int base = w & ~(WINDOW - 1), in_w = w - base, size_w = min(n - base, WINDOW);
+  const int xcd = in_w & 7, q = size_w >> 3, r = size_w & 7;
+  const int L = base + xcd * q + min(xcd, r) + (in_w >> 3);
   const int g = L / (GI * tilesN), first = g * GI;
   const int size = min(tilesM - first, GI), in = L - g * GI * tilesN;
   tm = first + in % size;
@@ -579,38 +583,34 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
 
 }  // namespace
 
-// Tiles of TM rows that R rows in E ranges can need at most.
-static int64_t max_tiles(int64_t R, int64_t E, int64_t TM) {
-  const int64_t t = R / TM + E;   // every range adds at most one ragged tile
-  return t < R ? t : R;
-}
-
-// Which kernel: the one with the least estimated time. A tile's step (128 of K)
-// takes `step` us of a CU when two workgroups share it, and `step2` us of a
-// workgroup with two K sets that has a CU to itself (two steps of K at once);
-// the two sets are taken when no CU gets a second workgroup. Streaming from
-// memory (5.3 TB/s measured) and from the caches into LDS (14 TB/s) bound the
-// time from below. Measured (us), M x N x K:           the rule's pick   next size up / down
-//   64 x 11008 x 4096, bf16     64x64, two sets    12.2  14.9 / 17.0
-//   512 x 4096 x 4096           64x128, two sets   15.2  20.6 / 17.5
-//   1024 x 4096 x 4096          128x128, two sets  22.9  48.1 / 24.7
-//   4096 x 4096 x 4096          256x256            59.8   -   / 69.8
-//   16 x 4096 x 4096            rows                6.6   8.8
-//   16 x 11008 x 4096           32x64, two sets    10.4  11.7 / 13.9 (rows)
-//   333 x 4096 x 4096, float32  64x128, two sets   22.9  33.1 / 28.1
-// The float32 form runs at half the matrix rate and on more registers: it has
-// its own times, and no 256 x 256 tile.
+// Which kernel: the one with the least estimated time. A tile takes `step` us of a
+// CU per block of K when two workgroups share it, and `ends` us for its prologue
+// and epilogue; with two K sets, which are taken when no CU gets a second
+// workgroup, a workgroup takes `step2` us for two blocks. Streaming from memory
+// (5.3 TB/s measured; 12% less with two sets) and from the caches into LDS (14
+// TB/s) bound the time from below. Measured (us), M x N x K, the rule's pick first:
+//   16 x 4096 x 4096            rows              6.5   32x64, two sets 8.8
+//   16 x 11008 x 4096           32x64, two sets  10.4   rows 13.9, 64x64 two sets 11.7
+//   64 x 11008 x 4096           64x64, two sets  12.3   one set 13.4, 32x64 14.7
+//   512 x 4096 x 4096           64x128, two sets 15.1   one set 17.5, 128x128 20.6
+//   1024 x 4096 x 4096          128x128, two     22.7   one set 25.4, 64x128 24.7
+//   4096 x 4096 x 4096          256x256          59.8   128x128 69.8
+//   24 tokens, 4 of 64 experts, 2048 x 2048: 64x128 22.7, 32x64 25.2, rows 37.0
+//   333 x 4096 x 4096, float32  64x128, two sets 23.4   one set 28.2, 128x128 33.1
+// Over 52 shapes, dense and by expert, the pick takes 1.04 times the best one's
+// time in the mean. The float32 form runs at half the matrix rate and on more
+// registers: it has its own times, and no 256 x 256 tile.
 namespace {
 enum Kind { kRows, k32x64, k64x64, k64x128, k128x128, k256x256, kKinds };
 struct Times {
   int tm, tn;
-  float step, step2;
+  float step, ends, step2;
 };
 constexpr Times kTimes[2][kKinds] = {
-    {{16, 16, 0, 0}, {32, 64, .155f, .30f}, {64, 64, .23f, .43f}, {64, 128, .362f, .62f},
-     {128, 128, .55f, .92f}, {256, 256, 1.80f, 0}},
-    {{16, 16, 0, 0}, {32, 64, .24f, .50f}, {64, 64, .37f, .75f}, {64, 128, .58f, 1.15f},
-     {128, 128, .94f, 1.80f}, {0, 0, 0, 0}}};
+    {{16, 16, 0, 0, 0}, {32, 64, .1425f, .4f, .30f}, {64, 64, .214f, .5f, .43f},
+     {64, 128, .34f, .7f, .62f}, {128, 128, .516f, 1.1f, .92f}, {256, 256, 1.52f, 9.0f, 0}},
+    {{16, 16, 0, 0, 0}, {32, 64, .228f, .4f, .50f}, {64, 64, .354f, .5f, .75f},
+     {64, 128, .558f, .7f, 1.15f}, {128, 128, .906f, 1.1f, 1.80f}, {0, 0, 0, 0, 0}}};
 
 // Tiles of tm rows to expect: what E ranges of equal size need, and half a tile more
 // for each where sizes differ.
@@ -620,6 +620,12 @@ double expected_tiles(const ArFp8Gemm& g, int tm) {
   const double t = (double)g.R / tm + 0.5 * used;
   return t > used ? t : used;
 }
+// Tiles of tm rows that there can be at most.
+int64_t most_tiles(const ArFp8Gemm& g, int64_t tm) {
+  if (!g.offsets) return (g.R + tm - 1) / tm;
+  const int64_t t = g.R / tm + g.E;   // every range adds at most one ragged tile
+  return t < g.R ? t : g.R;
+}
 
 struct Plan {
   Kind kind;
@@ -627,25 +633,29 @@ struct Plan {
 };
 Plan plan_of(const ArFp8Gemm& g) {
   const double K = (double)g.K, N = (double)g.N, KB = (double)((g.K + BLK - 1) / BLK);
-  const double used = (double)(g.E < g.R ? g.E : g.R);
+  const double used = (double)(g.E < g.R ? g.E : g.R), mean = (double)g.R / used;
   const double memory = (used * N + (double)g.R) * K / 5.3e6;
-  Plan best{kRows, false};
+  Plan best{k32x64, false};
   double least = -1.0;
-  // rows: every tile of 16 rows streams W at 5.8 TB/s, less X's share of the loads
-  const double mean = (double)g.R / used;
-  if (mean <= 64) {
+  // Rows: every tile of 16 rows streams W, at 5.8 TB/s less X's share of the loads;
+  // by expert at 5.2 with a row each, at 4.0 with more.
+  if (mean <= 256 && most_tiles(g, 16) <= 65535) {
     const double share = 1.0 + 0.4 * (mean < 16 ? mean : 16) / 16;
-    const double stream = expected_tiles(g, 16) * N * K * share / 5.8e6, chain = KB / 8 * 0.45;
+    const double rate = !g.offsets ? 5.8e6 : g.R <= g.E ? 5.2e6 : 4.0e6;
+    const double stream = expected_tiles(g, 16) * N * K * share / rate, chain = KB / 8 * 0.45;
     least = 3.0 + (stream > chain ? stream : chain);
+    best.kind = kRows;
   }
   for (int k = k32x64; k < kKinds; ++k) {
     const Times& c = kTimes[g.ydt == AR_F32][k];
     if (!c.tm) continue;
     const double t = expected_tiles(g, c.tm) * (double)((g.N + c.tn - 1) / c.tn);
     const bool two = c.step2 > 0 && t <= 256;
-    double us = two ? 4.0 + 0.5 * (KB + 1) * c.step2 : 3.0 + KB * c.step * ceil(t / 256);
+    const double rounds = ceil(t / 256);
+    double us = two ? 4.0 + 0.5 * (KB + 1) * c.step2 : 3.0 + rounds * (KB * c.step + c.ends);
+    const double stream = two ? 3.0 + 1.12 * memory : 3.0 + memory + rounds * c.ends;
     const double cache = 3.0 + t * KB * (c.tm + c.tn) * BLK / 14e6;
-    if (us < 3.0 + memory) us = 3.0 + memory;
+    if (us < stream) us = stream;
     if (us < cache) us = cache;
     if (least < 0 || us < least) {
       least = us;
@@ -700,7 +710,7 @@ ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
                (int)g.E, (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
   const Plan p = plan_of(g);
   const int tm = kTimes[g.ydt == AR_F32][p.kind].tm;
-  const int64_t tiles = g.offsets ? max_tiles(g.R, g.E, tm) : (g.R + tm - 1) / tm;
+  const int64_t tiles = most_tiles(g, tm);
   switch (p.kind) {
     case kRows: return rows_launch(a, tiles, st);
     case k32x64: return tile_pick<2, 2, 1, 2, 4, 4>(a, tiles, p.two, st);
