@@ -32,7 +32,8 @@ FLAGS = [
 # Kernels whose speed depends on running without register spills: the MFMA
 # contractions sit at the register file's limit. A spill (to scratch memory,
 # behind a full vector-memory wait) is reported as a warning.
-HOT = ("k_fwd_stream", "k_gemm", "k_gemm_small", "k_dq_mfma", "k_attention")
+HOT = ("k_fwd_stream", "k_gemm", "k_gemm_small", "k_dq_mfma", "k_attention", "k_fp8_tile",
+       "k_fp8_rows")
 _FN = re.compile(r"Function Name: (\S+)")
 _SPILL = re.compile(r"VGPRs Spill: (\d+)")
 

@@ -8,15 +8,29 @@
 //
 // The inner sum of one block comes from the matrix unit, from a zero
 // accumulator, and joins a float32 accumulator with one fma by the product of the
-// two scales.
-// W is the A operand and X the B operand, so a lane holds four neighbouring
-// n of one row r: the row's scale is one value per lane, W's scale is one
-// value for a whole wave, and Y is stored four values at a time. A and B use
-// one assignment of k to lanes (32 consecutive bytes per lane: K is summed
-// over, so any will do).
+// two scales. W is the A operand and X the B operand, so a lane holds four
+// neighbouring n of one row r: the row's scale is one value per lane, W's scale
+// is one value for a whole wave, and Y is stored four values at a time. A and B
+// use one assignment of k to lanes (two 16-byte chunks, 64 bytes apart: K is
+// summed over, so any will do).
+//
+// Two kernels: k_fp8_rows for few rows, where W's bytes are the cost, and k_fp8_tile
+// for the rest; plan_of chooses. What bounds them, with a large copy at 4.8 TB/s
+// and a library e4m3 product with one scale per operand at 2.41 PFLOP/s
+// (16384 x 4096 x 4096) on the same card:
+//   rows, 1 x 29568 x 8192            43.9 us, 5.5 TB/s: memory
+//   32x64 tiles, 16 x 29568 x 8192    46 us, 5.3 TB/s: memory
+//   64x128 tiles, 24 tokens, 4 of 64 experts, 2048 x 2048: 22.7 us, 5.3 TB/s: memory
+//   256x256 tiles, 16384 x 4096 x 4096    237 us, 2.32 PFLOP/s; 8192^3 443 us, 2.49
+//   the same by expert, 8192 tokens, 2 of 8, 11008 x 4096: 746 us, 1.98 PFLOP/s
+//   128x128 tiles, float32 Y, 16384 x 4096 x 4096: 473 us, 1.16 PFLOP/s
+// The 256x256 tile keeps the matrix unit busy 53% of the time at 2.18 GHz. Of its
+// 242 us the loop's loads cost 48 (timed without them), the scale fmas 22 and Y's
+// stores 35: all CUs end their tiles at about the same time, and a round of tiles
+// is 33 MB of Y. The float32 form converts every code a wave reads; its matrix
+// work alone would take 250 us.
 #include <math.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "ar_device.h"
@@ -82,8 +96,10 @@ __device__ __forceinline__ void find_tile(const Args& a, int t, int& e, int64_t&
       const int elo = __shfl(lo, l, 64), ehi = __shfl(hi, l, 64);
       e = __builtin_amdgcn_readfirstlane(base + l);
       const int at = __builtin_amdgcn_readfirstlane(elo + (t - first) * TM);
+      // (offsets that decrease may count more tiles than an int holds: no row then)
+      const int lo0 = __builtin_amdgcn_readfirstlane(elo);
       r0 = at;
-      rows = min(__builtin_amdgcn_readfirstlane(ehi) - at, TM);
+      rows = at >= lo0 ? min(__builtin_amdgcn_readfirstlane(ehi) - at, TM) : 0;
       return;
     }
     before += __shfl(sum, 63, 64);
@@ -328,16 +344,16 @@ __device__ __forceinline__ int count_tiles(const Args& a) {
 }
 
 template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int tilesN) {
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int mostM, int tilesN) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
   typedef FragOf<WIDE> Op;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds_all[];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[C::LDS];
   const int lane = threadIdx.x & 63;
   const int gwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int set = gwave / C::NW, wave = gwave % C::NW;
   uint8_t* lds = lds_all + set * C::RING;
   const int wm = wave % WM, wn = wave / WM;
-  const int tilesM = count_tiles<C::TM>(a);
+  const int tilesM = min(count_tiles<C::TM>(a), mostM);
   if ((int)blockIdx.x >= tilesM * tilesN) return;   // more workgroups than tiles: ragged ranges
   int tm, tn, e, rows;
   int64_t r0;
@@ -418,7 +434,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
     const uint8_t* st = lds + stage;
     const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(st + at);
     const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(st + (at ^ 64u));
-    return Op::of(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
   // W's scales of this wave's columns (one block of 128), 64 blocks of K at a time
@@ -448,11 +464,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
   meet();
   // W fragment t of a step is in fw[t % 4] (with NA = 2, where a step's last two
   // fragments are all it has, the next step's two come in through fw[2] and fw[3])
-  typename Op::type fx[MB], fw[4];
+  // Fragments are kept as read, and widened (WIDE) where they are used: a conversion
+  // at the read would wait for it.
+  i32x8_t rx[MB], fw[4];
   float sx[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
-    fx[b] = rd(0, ax + b * 16 * BLK);
+    rx[b] = rd(0, ax + b * 16 * BLK);
     sx[b] = *reinterpret_cast<const float*>(lds + as + b * 64);
   }
   fw[0] = rd(0, aw);
@@ -461,8 +479,12 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
   auto step = [&](int kt) {
     const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), (kt - kb0) & 63));
     float s[MB];
+    typename Op::type fx[MB], w0, w1;   // w0, w1: the W fragments in use
 #pragma unroll
-    for (int b = 0; b < MB; ++b) s[b] = sw * sx[b];
+    for (int b = 0; b < MB; ++b) {
+      s[b] = sw * sx[b];
+      fx[b] = Op::of(rx[b]);
+    }
     // Items: W fragment by W fragment up to the last two, those X fragment by X
     // fragment. Products join the accumulators three items behind the matrix
     // unit's issue.
@@ -483,7 +505,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
         wait_loads<(NS - 2) * C::LOADS>();
         meet();
       }
-      p[u % 4] = Op::mul(fw[t % 4], fx[b]);
+      if (u < LAST ? b == 0 : u == LAST) w0 = Op::of(fw[t % 4]);
+      if (u == LAST + 1) w1 = Op::of(fw[t % 4]);
+      p[u % 4] = Op::mul(u > LAST && t == NA - 1 ? w1 : w0, fx[b]);
       if (u < LAST) {
         if (b == 0) fw[(t + 2) % 4] = rd(cur, aw + (t + 2) * 16 * BLK);
       } else {
@@ -492,7 +516,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int t
         for (int i = 0; i < EACH; ++i)
           if ((u - LAST) * EACH + i < C::LOADS) issue(kt + NS, cur, (u - LAST) * EACH + i);
         if (t == NA - 1) {   // the next step's fragments replace these
-          fx[b] = rd(nxt, ax + b * 16 * BLK);
+          rx[b] = rd(nxt, ax + b * 16 * BLK);
           sx[b] = *reinterpret_cast<const float*>(lds + nxt + as + b * 64);
           if (b == 0) fw[NA % 4] = rd(nxt, aw);
           if (b == MB - 1) fw[(NA + 1) % 4] = rd(nxt, aw + 16 * BLK);
@@ -670,20 +694,9 @@ template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
 static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
-  if (tilesM * tilesN >= (int64_t(1) << 22)) return AR_ERR_SHAPE;
-  // more than the default 64 KiB of LDS has to be asked for, once per device
-  static std::atomic<uint64_t> asked{0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return AR_ERR_HIP;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
-    const void* f = reinterpret_cast<const void*>(&k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>);
-    if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess)
-      return AR_ERR_HIP;
-    asked.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (tilesM * tilesN * C::THREADS >= (int64_t(1) << 32)) return AR_ERR_SHAPE;   // HIP's limit
   hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>), dim3((unsigned)(tilesM * tilesN)),
-                     dim3(C::THREADS), C::LDS, st, a, (int)tilesN);
+                     dim3(C::THREADS), 0, st, a, (int)tilesM, (int)tilesN);
   return last_status();
 }
 

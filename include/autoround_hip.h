@@ -285,8 +285,12 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
 /* Y [M, N] = Σ_j xs[j, m]·ws[n/128, j]·Σ_{k in block j} Xq[m, k]·Wq[n, k]: Xq
    [M, K] with xs [KB, M] (ar_fp8_quant_act or ar_rmsnorm_fp8), Wq [N, K] with ws
    [NB, KB] (ar_fp8_quant_weight, E = 1). float32 accumulation, in a fixed order;
-   ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE. No
-   workspace. */
+   ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE, and so
+   is a product whose launch would pass 2^32 threads (M*N beyond 2^36 or so). No
+   workspace.
+   A float32 Y is summed in float32 throughout. For a bf16 Y the 128 products of a
+   block are added in the matrix unit's narrower sum (measured: off by up to 4e-5
+   of its size) and the blocks in float32; both are far below a bf16 rounding. */
 ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
                       const float* ws, int64_t N, void* Y, int32_t ydt, void* stream);
 

@@ -205,6 +205,9 @@ GEMM = [
     (128, 256, 256, "f32"), (130, 514, 384, "bf16"), (256, 512, 1024, "f32"),
     (300, 2050, 1360, "f32"), (513, 260, 112, "bf16"), (1000, 1030, 528, "bf16"),
     (2048, 768, 640, "bf16"), (3000, 64, 256, "f32"),
+    # more than 64 and 128 blocks of K, whole and short last blocks, on every path
+    (5, 40, 17008, "bf16"), (40, 130, 17008, "bf16"), (300, 200, 11008, "f32"),
+    (600, 1100, 8336, "bf16"), (4100, 4200, 8464, "bf16"),
 ]
 
 
