@@ -552,7 +552,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
   // The wave's part of Y goes through LDS (the stages are free once everyone is
   // here) so that rows leave as whole runs of 128 or 256 bytes, past the caches:
   // the tiles of all CUs end at about the same time. Measured at 16384 x 4096 x
-  // 4096 against storing from the accumulators: 253 us instead of 267.
+  // 4096 against storing from the accumulators: 253 us instead of 267. Rows of Y
+  // that are not 16-byte aligned leave in smaller units and through the caches
+  // (12468 x 4831 x 256 on 256x256 tiles: 63 us, past them 78).
   __syncthreads();
   if constexpr (KG > 1) {
     static_assert((KG - 1) * C::TM * C::TN * 4 <= C::LDS, "the other sets' sums in LDS");
@@ -600,9 +602,12 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
 #pragma unroll 8
     for (int i = lane; i < MB * 16 * UPR; i += 64) {
       const int r = i / UPR, u = i % UPR;
-      if (r < mleft && u * PER < nleft)
-        __builtin_nontemporal_store(*reinterpret_cast<const V*>(at(r, u * (int)sizeof(V))),
-                                    reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u);
+      if (r < mleft && u * PER < nleft) {
+        const V v = *reinterpret_cast<const V*>(at(r, u * (int)sizeof(V)));
+        V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
+        if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
+        else *d = v;   // runs that end inside a line are joined in L2
+      }
     }
   };
   const int64_t pitch = a.N * (int64_t)sizeof(O);
