@@ -7,7 +7,6 @@ Entry points mirror include/autoround_hip.h.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -548,58 +547,46 @@ def unpack(qweight, qzeros, bits: int, N: int, K: int, G: int, stream=None):
 
 
 # ------------------------------------------------------------------ e4m3 operands
-# These calls run in microseconds, so the checks below ask each question of a
-# tensor once and build no objects on the way that succeeds.
-_HERE_AND_NOW = contextlib.nullcontext()
-
-
-def _want(t, name, shape, dtype):
-    """_need for one dtype: its message, where this quick look finds a fault."""
-    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_cuda or \
-            not t.is_contiguous():
-        _need(t, name, shape, dtype)
-
-
-def _matrix(t, name):
-    """_weight, with a quick look first."""
-    torch = _torch()
-    if t is None or t.dim() != 2 or not t.is_cuda or not t.is_contiguous() or \
-            (t.dtype is not torch.bfloat16 and t.dtype is not torch.float32):
-        _weight(t, name)
-    return t.shape
-
-
-def _on(stream, *tensors):
-    """Context in which a call on these tensors allocates and launches: their
-    device, and ``stream`` (its current stream if None). ValueError when the
-    tensors or the stream are on different devices."""
+# These calls take microseconds, and so does asking a tensor about itself: the
+# usual case (tensors of the current device, its current stream) is recognised
+# with one look at each, and everything else goes through _elsewhere and the
+# full checks, which say what is wrong.
+def _elsewhere(stream, *tensors):
+    """Context in which to repeat a call whose tensors are not on the current
+    device, or that names a stream: their device, and the stream as the current one.
+    ValueError when the tensors or the stream are on different devices."""
     torch = _torch()
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must live on one GPU, got cuda:{dev} and {t.device}")
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
-        if stream != torch.cuda.current_stream(dev):
-            for t in tensors:   # the allocator must not hand the memory on before the call ends
-                if t is not None:
-                    t.record_stream(stream)
-        return torch.cuda.stream(stream)
-    return _HERE_AND_NOW if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    if stream != torch.cuda.current_stream(dev):
+        for t in tensors:   # the allocator must not hand the memory on before the call ends
+            if t is not None:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
-def _stream_of(t) -> int:
-    """Handle of the current stream of t's device (torch.cuda.current_stream builds
-    an object around the same number, 2.7 us a time)."""
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+def _is(t, shape, dtype, dev) -> bool:
+    """t is a contiguous tensor of this shape and dtype on GPU `dev`."""
+    return t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _matrix(t, name):
+    """(rows, columns, device index) of a float32 / bf16 GPU matrix."""
+    torch = _torch()
+    if t is None or t.dim() != 2 or not t.is_contiguous() or t.get_device() < 0 or \
+            (t.dtype is not torch.bfloat16 and t.dtype is not torch.float32):
+        _weight(t, name)
+    M, K = t.shape
+    return M, K, t.get_device()
 
 
-def _fp8_scales(K: int) -> int:
+def _scales(K: int) -> int:
     return -(-K // FP8_BLOCK)
 
 
@@ -609,17 +596,22 @@ def fp8_quant_act(X, *, gate: bool = False, stream=None):
     ``gate``: X is [M, 2K], the gate and the up half side by side, and the codes
     are those of SiLU(gate)·up."""
     torch = _torch()
-    M, K = _matrix(X, "X")
+    M, K, dev = _matrix(X, "X")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, X):
+            return fp8_quant_act(X, gate=gate)
     if gate:
         if K % 2:
             raise ValueError("gate needs an even number of channels")
         K //= 2
-    with _on(stream, X):
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device) if gate else \
-            torch.empty_like(X, dtype=torch.float8_e4m3fn)
-        s = torch.empty((_fp8_scales(K), M), dtype=torch.float32, device=X.device)
-        _check(lib.ar_fp8_quant_act(_dt(X), _at(X), int(gate), M, K, _at(q), _at(s),
-                                    _stream_of(X)), "ar_fp8_quant_act")
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        q = torch.empty_like(X, dtype=torch.float8_e4m3fn)
+    s = torch.empty((_scales(K), M), dtype=torch.float32, device=dev)
+    st = lib.ar_fp8_quant_act(_dt(X), X.data_ptr(), 1 if gate else 0, M, K, q.data_ptr(),
+                              s.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_fp8_quant_act")
     return q, s
 
 
@@ -631,13 +623,17 @@ def fp8_quant_weight(W, *, stream=None):
     if W is None or W.dim() not in (2, 3):
         raise ValueError("W must be a [N, K] or [E, N, K] tensor")
     _need(W, "W", W.shape, (torch.float32, torch.bfloat16))
+    dev = W.get_device()
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, W):
+            return fp8_quant_weight(W)
     lead, (N, K) = W.shape[:-2], W.shape[-2:]
-    with _on(stream, W):
-        q = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device)
-        s = torch.empty((*lead, _fp8_scales(N), _fp8_scales(K)), dtype=torch.float32,
-                        device=W.device)
-        _check(lib.ar_fp8_quant_weight(_dt(W), _at(W), lead[0] if lead else 1, N, K, _at(q),
-                                       _at(s), _stream_of(W)), "ar_fp8_quant_weight")
+    q = torch.empty_like(W, dtype=torch.float8_e4m3fn)
+    s = torch.empty((*lead, _scales(N), _scales(K)), dtype=torch.float32, device=dev)
+    _check(lib.ar_fp8_quant_weight(_dt(W), W.data_ptr(), lead[0] if lead else 1, N, K,
+                                   q.data_ptr(), s.data_ptr(),
+                                   torch._C._cuda_getCurrentRawStream(dev)),
+           "ar_fp8_quant_weight")
     return q, s
 
 
@@ -656,50 +652,61 @@ def rmsnorm_fp8(x, weight, eps: float = 1e-6, *, residual=None, want_y: bool = F
     stream is then updated in place); ``want_y`` also returns the norm's output
     in x's dtype."""
     torch = _torch()
-    M, D = _matrix(x, "x")
-    _want(weight, "weight", (D,), x.dtype)
+    M, D, dev = _matrix(x, "x")
+    dt, shape = x.dtype, x.shape
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, x, weight, residual, h_out):
+            return rmsnorm_fp8(x, weight, eps, residual=residual, want_y=want_y, h_out=h_out)
+    if weight is None or not _is(weight, (D,), dt, dev):
+        _refuse(weight, "weight", (D,), dt)
+    h = h_out
     if residual is not None:
-        _want(residual, "residual", (M, D), x.dtype)
-    if h_out is not None:
-        if residual is None:
-            raise ValueError("h_out needs a residual")
-        _want(h_out, "h_out", (M, D), x.dtype)
-    with _on(stream, x, weight, residual, h_out):
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        s = torch.empty((_fp8_scales(D), M), dtype=torch.float32, device=x.device)
-        h = h_out
-        if residual is not None and h is None:
+        if not _is(residual, shape, dt, dev):
+            _refuse(residual, "residual", shape, dt)
+        if h is None:
             h = torch.empty_like(x)
-        y = torch.empty_like(x) if want_y else None
-        _check(lib.ar_rmsnorm_fp8(_dt(x), _at(x), _at(residual), _at(weight), M, D, eps,
-                                  _at(h), _at(y), _at(q), _at(s), _stream_of(x)),
-               "ar_rmsnorm_fp8")
+        elif not _is(h, shape, dt, dev):
+            _refuse(h, "h_out", shape, dt)
+    elif h is not None:
+        raise ValueError("h_out needs a residual")
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    s = torch.empty((_scales(D), M), dtype=torch.float32, device=dev)
+    y = torch.empty_like(x) if want_y else None
+    st = lib.ar_rmsnorm_fp8(_dt(x), x.data_ptr(), None if residual is None else residual.data_ptr(),
+                            weight.data_ptr(), M, D, eps, None if h is None else h.data_ptr(),
+                            None if y is None else y.data_ptr(), q.data_ptr(), s.data_ptr(),
+                            torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_rmsnorm_fp8")
     return NormOutput(q, s, h, y)
 
 
+def _refuse(t, name, shape, dtype):
+    """ValueError for a tensor that _is not what the call needs."""
+    _need(t, name, shape, dtype)
+    raise ValueError(f"{name} must live on the other tensors' GPU, got {t.device}")
+
+
 def _fp8_operands(Xq, xs, Wq, ws, dims: int):
-    """(T, K, N) of the two operands, checked with their scales."""
+    """(T, K, N, device index) of the two operands, checked with their scales."""
     torch = _torch()
     f8, f32 = torch.float8_e4m3fn, torch.float32
     if Xq is None or Xq.dim() != 2:
         raise ValueError("Xq must be a 2-D [T, K] tensor")
     if Wq is None or Wq.dim() != dims:
         raise ValueError("Wq must be a [%sN, K] tensor" % ("E, " if dims == 3 else ""))
-    T, K = Xq.shape
-    *lead, N, KW = Wq.shape
-    KB = _fp8_scales(K)
-    scales = (*lead, _fp8_scales(N), KB)
-    if KW == K and xs is not None and ws is not None and xs.shape == (KB, T) and \
-            ws.shape == scales and Xq.dtype is f8 and Wq.dtype is f8 and xs.dtype is f32 and \
-            ws.dtype is f32 and Xq.is_cuda and xs.is_cuda and Wq.is_cuda and ws.is_cuda and \
-            Xq.is_contiguous() and xs.is_contiguous() and Wq.is_contiguous() and \
-            ws.is_contiguous():
-        return T, K, N
-    _need(Xq, "Xq", (T, K), f8)             # one of these says what is wrong
-    _need(xs, "xs", (KB, T), f32)
-    _need(Wq, "Wq", (*lead, N, K), f8)
-    _need(ws, "ws", scales, f32)
-    raise ValueError("operands do not match")
+    if xs is None or ws is None:
+        raise ValueError("xs and ws are required")
+    T, K = shape = Xq.shape
+    *lead, N, _ = Wq.shape
+    KB, dev = _scales(K), Xq.get_device()
+    wants = (("Xq", Xq, shape, f8), ("xs", xs, (KB, T), f32), ("Wq", Wq, (*lead, N, K), f8),
+             ("ws", ws, (*lead, _scales(N), KB), f32))
+    for name, t, size, dtype in wants:
+        if t.shape != size or t.dtype is not dtype or t.get_device() != dev or \
+                not t.is_contiguous() or dev < 0:
+            _refuse(t, name, size, dtype)
+    return T, K, N, dev
 
 
 def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
@@ -707,16 +714,19 @@ def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
     operands with their block scales (ar_fp8_gemm): Xq [M, K], xs [ceil(K/128), M]
     from fp8_quant_act or rmsnorm_fp8; Wq [N, K], ws from fp8_quant_weight."""
     torch = _torch()
-    M, K, N = _fp8_operands(Xq, xs, Wq, ws, 2)
-    if out is not None:
-        _need(out, "out", (M, N), (torch.float32, torch.bfloat16))
-    with _on(stream, Xq, xs, Wq, ws, out):
-        Y = out
-        if Y is None:
-            Y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=Xq.device)
-        _check(lib.ar_fp8_gemm(_at(Xq), _at(xs), M, K, _at(Wq), _at(ws), N, _at(Y), _dt(Y),
-                               _stream_of(Xq)), "ar_fp8_gemm")
-    return Y
+    M, K, N, dev = _fp8_operands(Xq, xs, Wq, ws, 2)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, Xq, xs, Wq, ws, out):
+            return fp8_gemm(Xq, xs, Wq, ws, out_dtype=out_dtype, out=out)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif not _is(out, (M, N), out.dtype, dev) or out.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(out, "out", (M, N), (torch.float32, torch.bfloat16))
+    st = lib.ar_fp8_gemm(Xq.data_ptr(), xs.data_ptr(), M, K, Wq.data_ptr(), ws.data_ptr(), N,
+                         out.data_ptr(), _dt(out), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_fp8_gemm")
+    return out
 
 
 def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None, out=None,
@@ -728,25 +738,32 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
     the offsets keep what ``out`` held (without ``out`` they hold nothing
     meaningful)."""
     torch = _torch()
-    T, K, N = _fp8_operands(Xq, xs, Wq, ws, 3)
+    T, K, N, dev = _fp8_operands(Xq, xs, Wq, ws, 3)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, Xq, xs, Wq, ws, offsets, row_index, out):
+            return fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, row_index=row_index,
+                                    out_dtype=out_dtype, out=out)
     E = Wq.shape[0]
-    _want(offsets, "offsets", (E + 1,), torch.int32)
-    R = T
+    if offsets is None or not _is(offsets, (E + 1,), torch.int32, dev):
+        _refuse(offsets, "offsets", (E + 1,), torch.int32)
+    R, index = T, None
     if row_index is not None:
         if row_index.dim() != 1:
             raise ValueError("row_index must be a 1-D [R] tensor")
         R = row_index.shape[0]
-        _want(row_index, "row_index", (R,), torch.int32)
-    if out is not None:
-        _need(out, "out", (R, N), (torch.float32, torch.bfloat16))
-    with _on(stream, Xq, xs, Wq, ws, offsets, row_index, out):
-        Y = out
-        if Y is None:
-            Y = torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=Xq.device)
-        _check(lib.ar_fp8_gemm_grouped(_at(Xq), _at(xs), T, K, _at(Wq), _at(ws), E, N,
-                                       _at(offsets), _at(row_index), R, _at(Y), _dt(Y),
-                                       _stream_of(Xq)), "ar_fp8_gemm_grouped")
-    return Y
+        if not _is(row_index, (R,), torch.int32, dev):
+            _refuse(row_index, "row_index", (R,), torch.int32)
+        index = row_index.data_ptr()
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif not _is(out, (R, N), out.dtype, dev) or out.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(out, "out", (R, N), (torch.float32, torch.bfloat16))
+    st = lib.ar_fp8_gemm_grouped(Xq.data_ptr(), xs.data_ptr(), T, K, Wq.data_ptr(), ws.data_ptr(),
+                                 E, N, offsets.data_ptr(), index, R, out.data_ptr(), _dt(out),
+                                 torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_fp8_gemm_grouped")
+    return out
 
 
 # ------------------------------------------------------------------ per-layer config
