@@ -95,7 +95,10 @@ def product_bound(K):
     A term's product is exact; a block adds 128 terms to zero, its sum and the
     scale product (rounded once) meet the accumulator in one rounding, and up to
     KB + 8 accumulations follow, each rounding by at most 2^-23 of what it holds
-    (twice the half step of float32: the matrix unit need not round to nearest)."""
+    (twice the half step of float32: the matrix unit need not round to nearest).
+    Where a bf16 result lets the e4m3 unit add a block in its own narrower sum, that
+    sum is off by up to 4e-5 of its size; the magnitudes of 128 terms add up to
+    several times the size of a sum of random signs, so the bound holds there too."""
     return (BLOCK + blocks(K) + 10) * 2.0 ** -23
 
 

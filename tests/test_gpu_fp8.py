@@ -115,7 +115,7 @@ def test_quant_of_extreme_values():
 
 
 NORM = [(1, 16), (1, 4096), (3, 144), (5, 1024), (70, 1040), (9, 4112), (4, 8192), (3, 8208),
-        (2, 20000), (1100, 256)]
+        (2, 20000), (1100, 256), (37, 128), (6, 2048)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -150,9 +150,9 @@ def test_rmsnorm(M, D, dtype):
 
 def test_rmsnorm_of_large_values_and_in_place():
     """Squares past float32's range; the residual stream updated in place gives
-    the same bits as into a new tensor, at a width held in registers and one
-    that is read twice."""
-    for D in (512, 8400):
+    the same bits as into a new tensor, at widths held in registers and one that
+    is read twice."""
+    for D in (512, 8400, 16400):
         rng = np.random.default_rng(D)
         X, _ = given(1e30 * rng.standard_normal((5, D)), "f32")
         Rs, _ = given(1e30 * rng.standard_normal((5, D)), "f32")
@@ -208,6 +208,8 @@ GEMM = [
     # more than 64 and 128 blocks of K, whole and short last blocks, on every path
     (5, 40, 17008, "bf16"), (40, 130, 17008, "bf16"), (300, 200, 11008, "f32"),
     (600, 1100, 8336, "bf16"), (4100, 4200, 8464, "bf16"),
+    # large tiles with rows of Y that start at any 2 bytes, and at any 4
+    (6200, 4831, 528, "bf16"), (6200, 4830, 272, "bf16"),
 ]
 
 
@@ -273,6 +275,10 @@ GROUPED = [
     ([513, 2, 0, 255, 257], 384, 640, False, "f32"),
     ([2000, 0, 3, 1100], 300, 384, True, "bf16"),
     ([0, 0, 0], 64, 128, False, "f32"),
+    # more experts than a wave has lanes, and than four times that
+    ([1, 0, 2] * 100, 130, 144, True, "bf16"),
+    ([70, 0, 3] * 90, 140, 272, False, "bf16"),
+    ([0] * 299 + [40], 64, 128, True, "f32"),
 ]
 
 
