@@ -576,6 +576,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
     static_assert((KG - 1) * C::TM * C::TN * 4 + C::TM * C::TN * 4 <= C::LDS, "beside Y's tile");
     lds = lds_all + (KG - 1) * C::TM * C::TN * 4;
   }
+  // A row that names none is zero even where W holds a NaN or an infinite scale.
+  if (a.idx) {
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int r = wm * MB * 16 + 16 * b + l16;
+      if (r < rows && x_row(a, r0 + r) < 0)
+#pragma unroll
+        for (int t = 0; t < NA; ++t) acc[t][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
   typedef std::conditional_t<WIDE, float, uint16_t> O;
   constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
   static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
@@ -635,7 +645,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
 //   2048 x 4096 x 4096          128x128          36.1   64x128 46.2, 256x256 50.0
 //   3806 x 2584 x 8656          256x256         118     128x128 139
 //   4096 x 4096 x 4096          256x256          59.8   128x128 69.8
-//   24 tokens, 4 of 64 experts, 2048 x 2048: 32x64 25.2, 64x128 22.7, rows 37.0
+//   24 tokens, 4 of 64 experts, 2048 x 2048: 64x128 22.7, 32x64 25.2, rows 37.0
 //   333 x 4096 x 4096, float32  64x128, two sets 23.4   one set 28.2, 128x128 33.1
 // Over 78 shapes, dense and by expert, the pick takes 1.04 times the best one's
 // time in the mean, and 1.3 times it at the most. The float32 form runs at half

@@ -329,6 +329,25 @@ def test_grouped_bad_offsets_stay_inside(off):
     assert torch.all(big[:G] == 3.0) and torch.all(big[G + R:] == 3.0)
 
 
+@pytest.mark.parametrize("counts,N,K,out", [
+    ([20, 0, 13], 140, 272, "f32"), ([1, 1], 40, 256, "bf16"), ([700, 40], 260, 256, "bf16"),
+    ([400], 300, 528, "f32"), ([6000], 4100, 128, "bf16")])
+def test_grouped_rows_without_a_token_beside_nonfinite_weights(counts, N, K, out):
+    """A row whose index names no token is zero, also where its expert's weight holds
+    NaN codes and infinite scales; the other rows show them."""
+    log(f"fp8_gemm_grouped no token, nonfinite W {counts} N={N} K={K} {out}")
+    ops, off, idx, offd, _, R = grouped_case(counts, N, K, True, 77)
+    idx[::3] = -1
+    idx[1::7] = ops[0].shape[0]
+    ops[2].view(torch.uint8)[:, N // 2, K - 3] = 0x7F
+    ops[3][:, 0, 0] = float("inf")
+    Y = to_np(ar.fp8_gemm_grouped(*ops, offd, row_index=torch.from_numpy(idx).to(dev()),
+                                  out_dtype=OUT[out]))
+    none = (idx < 0) | (idx >= ops[0].shape[0])
+    assert np.all(Y[none] == 0.0)
+    assert np.isnan(Y[~none][:, N // 2]).all() and not np.isfinite(Y[~none][:, 0]).any()
+
+
 def test_empty_calls():
     z = lambda *s, d=torch.float32: torch.zeros(s, dtype=d, device=dev())   # noqa: E731
     q, s = ar.fp8_quant_act(z(0, 64))
