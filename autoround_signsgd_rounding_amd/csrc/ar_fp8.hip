@@ -77,10 +77,12 @@ __device__ __forceinline__ void store_row(float* p, const float (&v)[CH]) {
 }
 
 // SiLU(g)·u in float32: the exponential's argument is rounded once (a relative
-// error of |g|·2^-24 in the result, for negative g), the reciprocal to 1 ulp.
+// error of |g|·2^-24 in the result, for negative g), the reciprocal to 1 ulp. The
+// reciprocal unit flushes subnormal results, which sigmoids of g < -87.3 are, so
+// it works 2^32 higher.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+  return g * (__builtin_amdgcn_rcpf(fmaf(e, 0x1p-32f, 0x1p-32f)) * 0x1p-32f) * u;
 }
 
 // ------------------------------------------------------------------ activations

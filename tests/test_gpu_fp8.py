@@ -79,6 +79,23 @@ def test_quant_act(M, K, dtype, gate):
     check_codes(q, s, exact, want, F.spread_act(want, K), np.full(1, 2 * rel))
 
 
+@pytest.mark.parametrize("M", [3, 2200])
+def test_quant_act_of_gates_far_below_zero(M):
+    """Sigmoids below 2^-126 (a gate under -87.3) times a large up half: the
+    result is a normal number, in blocks of nothing else. The exponential's argument
+    is off by |gate| U, the sigmoid as a subnormal of 2^-128 by 2^-22."""
+    log(f"quant_act of gates far below zero M={M}")
+    rng = np.random.default_rng(M)
+    x = np.concatenate([rng.uniform(-88.7, -86.0, (M, 256)),
+                        1e30 * rng.uniform(0.5, 1.0, (M, 256))], 1)
+    X, x = given(x, "f32")
+    q, s = ar.fp8_quant_act(X, gate=True)
+    torch.cuda.synchronize()
+    exact = F.silu_mul(x)
+    want = F.act_scales(exact)
+    check_codes(q, s, exact, want, F.spread_act(want, 256), np.full(1, 2 * (2 * 88.7 + 16) * U))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("E,N,K", [(1, 1, 16), (3, 130, 272), (1, 256, 512), (9, 128, 128),
                                    (2, 77, 1040)])
