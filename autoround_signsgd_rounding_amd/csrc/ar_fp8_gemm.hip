@@ -137,9 +137,11 @@ __device__ __forceinline__ void store_y(const Args& a, int64_t r, int64_t n, con
 
 // One block's products. A fragment is 32 codes of one row; the unscaled
 // v_mfma_f32_16x16x128_f8f6f4 (scale operands 0) multiplies two of them at twice
-// the bf16 rate, but adds its 128 products to about 16 bits: measured 1.3e-5 to
-// 3.7e-5 of the sum's size, a hundredth of the half step of a bf16 output
-// (2^-9 on average). For a float32 output that would be the largest error by far,
+// the bf16 rate, but adds 8 neighbouring products with 13 bits below the exponent of
+// the largest, cutting the rest off (measured with single products beside a pair that
+// cancels), and only those sums in float32: 1.3e-5 to 3.7e-5 of the block's sum on
+// random operands, a hundredth of the half step of a bf16 output (2^-9 on
+// average). For a float32 output that would be the largest error by far,
 // so there the codes are widened to bf16 (exact) and multiplied by
 // v_mfma_f32_16x16x32_bf16 (1e-8, measured), at half the rate.
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));

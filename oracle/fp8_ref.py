@@ -97,9 +97,23 @@ def product_bound(K):
     KB + 8 accumulations follow, each rounding by at most 2^-23 of what it holds
     (twice the half step of float32: the matrix unit need not round to nearest).
     Where a bf16 result lets the e4m3 unit add a block in its own narrower sum, that
-    sum is off by up to 4e-5 of its size; the magnitudes of 128 terms add up to
-    several times the size of a sum of random signs, so the bound holds there too."""
+    sum is off by up to 4e-5 of its size for products of like sizes; the magnitudes of
+    128 terms add up to several times the size of a sum of random signs, so the bound
+    holds there too. Products of very different sizes: unit_bound()."""
     return (BLOCK + blocks(K) + 10) * 2.0 ** -23
+
+
+def unit_bound(xq, xs, wq, ws):
+    """What the e4m3 unit may lose beyond product_bound() in a bf16 result. It adds
+    the products of 8 neighbouring channels first, cut off 13 bits below the largest
+    one's exponent: up to 7 of them lose less than 2^-13 of that one each."""
+    M, (N, K) = xq.shape[0], wq.shape
+    x = np.abs(xq * spread_act(np.asarray(xs, np.float64), K))
+    w = np.abs(wq * spread_weight(np.asarray(ws, np.float64), N, K))
+    lost = np.zeros((M, N))
+    for k in range(0, K, 8):
+        lost += (x[:, None, k:k + 8] * w[None, :, k:k + 8]).max(2)
+    return lost * 7 * 2.0 ** -13
 
 
 def grouped_product(xq, xs, wq, ws, offsets, row_index, out):

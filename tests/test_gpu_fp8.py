@@ -263,6 +263,30 @@ def test_gemm_full_size_sampled(M, N, K):
     check_product(to_np(Y[r][:, c]), y, mag, K, "f32")
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(3, 100), (200, 140), (700, 300)])
+def test_gemm_of_outliers_that_cancel(M, N, out):
+    """Two products of 448^2 in each block of K cancel, among products near 1: a bf16
+    result may lose what the matrix unit cuts off, a float32 one nothing of it."""
+    log(f"fp8_gemm outliers that cancel M={M} N={N} {out}")
+    rng = np.random.default_rng(M)
+    K = 400
+    xq, xs, wq, ws = operands(rng, M, 1, N, K)
+    x, w = rng.standard_normal((M, K)), rng.standard_normal((N, K))
+    for j in range(F.blocks(K)):
+        p, q = 128 * j + rng.choice(min(128, K - 128 * j), 2, replace=False)
+        x[:, p], x[:, q], w[:, p], w[:, q] = 448.0, -448.0, 448.0, 448.0
+    xq.copy_(torch.from_numpy(x).to(dev()).to(F8))
+    wq.copy_(torch.from_numpy(w).to(dev()).to(F8)[None])
+    Y = to_np(ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])).astype(np.float64)
+    a, s, b, t = values(xq, xs, wq, ws)
+    y, mag = F.product(a, s, b[0], t[0])
+    tol = F.product_bound(K) * mag
+    if out == "bf16":
+        tol = tol + F.unit_bound(a, s, b[0], t[0]) + 2.0 ** -8 * np.abs(y)
+    assert np.all(np.abs(Y - y) <= tol), (np.abs(Y - y) / tol).max()
+
+
 def test_gemm_zero_and_nonfinite():
     """A NaN code reaches its row (or column) only; an infinite scale too."""
     rng = np.random.default_rng(1)
