@@ -254,9 +254,10 @@ ar_status ar_dequant_gemm(int32_t bits, int32_t group_size, const uint16_t* X, i
    4-byte alignment only.
 
    Scale of a block: s = 1 if its largest magnitude amax is 0, else
-   max(amax/448, 2^-126); code = e4m3(x·(1/s)), round to nearest even, float32
-   steps (1/s to one unit in the last place). A NaN gives a NaN code and does not enter amax. An infinity makes s
-   infinite and its own code NaN, and with s every product of the block NaN. */
+   max(amax/448, 2^-126); code = e4m3(x/s), round to nearest even. Both quotients
+   are float32, rounded once (to 2^-46). A NaN gives a NaN code and does not enter
+   amax. An infinity makes s infinite and its own code NaN, and with s every
+   product of the block NaN. */
 
 /* Activations: q [M, K], scale [KB, M] (one row of scales per block of 128
    channels). gate = 0: the codes of X [M, K]. gate = 1: X is [M, 2K] and the

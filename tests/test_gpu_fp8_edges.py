@@ -1,0 +1,67 @@
+"""The e4m3 operators where float32 steps, ranges and arguments run out: quotients
+halfway between two codes."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import F32, dev, log, to_np
+from oracle import fp8_ref as F
+from test_gpu_fp8 import activations, codes_of, given
+
+pytestmark = pytest.mark.gpu
+ar = pytest.importorskip("autoround_signsgd_rounding_amd")
+
+
+# ------------------------------------------------------------------ codes
+def want_codes(x, s):
+    """Bytes of the e4m3 codes of float32 x over float32 scales s (spread), by division."""
+    t = np.asarray(x, F32) / np.asarray(s, F32)
+    v = F.e4m3_round(t.astype(np.float64).clip(-448, 448))
+    mag = np.searchsorted(F.GRID, np.abs(v)).astype(np.uint8)
+    return mag | (np.signbit(t).astype(np.uint8) << 7)
+
+
+def halfway(rows):
+    """Rows of 128 values whose quotients by the row's scale, 1, 3, 5, .., lie halfway between
+    two codes (the first value makes the scale; every value is exact in float32)."""
+    mid = ((F.GRID[1:] + F.GRID[:-1]) / 2)[:-1]
+    s = 2.0 * np.arange(rows) + 1.0
+    x = np.concatenate([np.full((rows, 1), 448.0), np.tile(mid, (rows, 1)),
+                        np.zeros((rows, 2))], 1) * s[:, None]
+    x[:, 2::2] *= -1.0
+    assert np.array_equal(x.astype(F32), x)
+    return x, s
+
+
+@pytest.mark.parametrize("rows", [2000, 20000])
+@pytest.mark.parametrize("exponent", [-132, -120, -80, 0, 90])
+def test_codes_of_quotients_halfway_between_two(rows, exponent):
+    """Ties go to the even code, whatever the scale's reciprocal is. The larger call
+    takes the kernel of long prompts."""
+    log(f"halfway rows={rows} exponent={exponent}")
+    x, s = halfway(rows)
+    x, s = np.ldexp(x, exponent), np.ldexp(s, exponent)
+    keep = s >= 2.0 ** -126
+    x, s = x[keep], s[keep]
+    X, _ = given(x, "f32")
+    q, sc = ar.fp8_quant_act(X)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(to_np(sc)[0], s.astype(F32))
+    np.testing.assert_array_equal(codes_of(q), want_codes(x, s[:, None]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(7, 4096), (2200, 1040)])
+def test_codes_are_those_of_the_division(M, K, dtype):
+    """Every code of both quantizers and of the norm is that of the rounded quotient."""
+    log(f"codes by division M={M} K={K} {dtype}")
+    rng = np.random.default_rng(M + K)
+    X, x = given(activations(rng, M, K), dtype)
+    q, s = ar.fp8_quant_act(X)
+    wq, ws = ar.fp8_quant_weight(X)
+    n = ar.rmsnorm_fp8(X.float(), torch.ones(K, device=dev()), want_y=True)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(codes_of(q), want_codes(x, F.spread_act(to_np(s), K)))
+    np.testing.assert_array_equal(codes_of(wq), want_codes(x, F.spread_weight(to_np(ws), M, K)))
+    np.testing.assert_array_equal(codes_of(n.q),
+                                  want_codes(to_np(n.y), F.spread_act(to_np(n.scale), K)))
