@@ -91,12 +91,16 @@ __device__ __forceinline__ void store_row(float* p, const float (&v)[CH]) {
   __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, d + 1);
 }
 
-// SiLU(g)·u in float32: the exponential's argument is rounded once (a relative
-// error of |g|·2^-24 in the result, for negative g), the reciprocal to 1 ulp. The
-// reciprocal unit flushes subnormal results, which sigmoids of g < -87.3 are, so
-// it works 2^32 higher.
+// SiLU(g)·u in float32, to 8·2^-24: exp(-g) = 2^hi·(1 + lo·ln 2), hi the rounded product
+// of g and log2 e and lo the rest of it, without which the result would be off by
+// |g|·2^-24. The reciprocal unit flushes subnormal results, which sigmoids of g < -87.3
+// are, so it works 2^32 higher. (The clamp keeps lo finite.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
+  constexpr float L = -1.44269504f, LREST = -1.92596303e-8f, LN2 = 0.69314718f;   // L + LREST: -log2 e
+  const float x = __builtin_amdgcn_fmed3f(g, -300.0f, 300.0f);
+  const float hi = x * L, lo = fmaf(x, LREST, fmaf(x, L, -hi));
+  const float p = __builtin_amdgcn_exp2f(hi);
+  const float e = p < __builtin_inff() ? fmaf(p, lo * LN2, p) : p;
   return g * (__builtin_amdgcn_rcpf(fmaf(e, 0x1p-32f, 0x1p-32f)) * 0x1p-32f) * u;
 }
 

@@ -1,5 +1,5 @@
 """The e4m3 operators where float32 steps, ranges and arguments run out: quotients
-halfway between two codes."""
+halfway between two codes, SiLU of gates far from zero."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +65,50 @@ def test_codes_are_those_of_the_division(M, K, dtype):
     np.testing.assert_array_equal(codes_of(wq), want_codes(x, F.spread_weight(to_np(ws), M, K)))
     np.testing.assert_array_equal(codes_of(n.q),
                                   want_codes(to_np(n.y), F.spread_act(to_np(n.scale), K)))
+
+
+# ------------------------------------------------------------------ SiLU
+U = 2.0 ** -24
+
+
+def gated_alone(g, u):
+    """Scales and codes [M, KB] of SiLU(g)·u, each alone in a block of zeros."""
+    M, KB = g.shape
+    x = np.zeros((M, 2, KB, 128), F32)
+    x[:, 0], x[:, 1, :, 77] = g[:, :, None], u
+    q, s = ar.fp8_quant_act(torch.from_numpy(x.reshape(M, -1)).to(dev()), gate=True)
+    torch.cuda.synchronize()
+    return to_np(s).T.astype(np.float64), F.e4m3_values(codes_of(q)).reshape(M, KB, 128)[:, :, 77]
+
+
+def check_gated_alone(g, u):
+    """A value alone in its block is 448 times the scale: exp and the reciprocal are good to
+    2^-23 each, the sum with 1, exp's correction and two products round once, and so does the
+    scale: 9·2^-24, and second orders."""
+    g, u = g.astype(F32), u.astype(F32)
+    s, code = gated_alone(g, u)
+    z = F.silu_mul(np.concatenate([g, u], 1))
+    assert np.all(np.abs(z) >= 448 * 2.0 ** -125)         # the scale is a normal number
+    err = np.abs(s * 448 / np.abs(z) - 1) / U
+    log(f"  worst {err.max():.1f} half units in the last place")
+    assert err.max() <= 9.01
+    np.testing.assert_array_equal(code, 448.0 * np.sign(z))
+
+
+@pytest.mark.parametrize("M", [200, 1500])                # 1500: the kernel of long prompts
+def test_silu_of_every_gate_to_float32(M):
+    log(f"silu of gates M={M}")
+    rng = np.random.default_rng(M)
+    check_gated_alone(rng.uniform(-82, 60, (M, 16)), rng.uniform(0.5, 2, (M, 16)))
+    check_gated_alone(rng.normal(size=(M, 16)), -rng.uniform(0.5, 2, (M, 16)))
+
+
+def test_silu_of_nonfinite_and_huge_gates():
+    inf = np.inf
+    g = np.array([[inf, inf, -inf, np.nan, 1.0, 1.0, -1000.0, -3e38, 3e38, 1000.0, 0.0]])
+    u = np.array([[2.0, -2.0, 2.0, 2.0, inf, np.nan, 3e38, 3e38, 2.0, 2.0, 2.0]])
+    s, code = gated_alone(g.astype(F32), u.astype(F32))
+    assert np.isposinf(s[0, [0, 1, 4, 8]]).all()
+    assert np.all(s[0, [2, 3, 5, 6, 7, 10]] == 1.0)
+    assert np.isnan(code[0, [0, 1, 2, 3, 4, 5, 8]]).all() and np.all(code[0, [6, 7, 10]] == 0.0)
+    assert s[0, 9] == F32(2000.0) / F32(448.0)
