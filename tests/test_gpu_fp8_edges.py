@@ -103,6 +103,17 @@ def test_silu_of_every_gate_to_float32(M):
     check_gated_alone(rng.normal(size=(M, 16)), -rng.uniform(0.5, 2, (M, 16)))
 
 
+@pytest.mark.parametrize("M", [200, 1500])
+def test_silu_of_gates_whose_sigmoid_is_no_float32(M):
+    """Sigmoids down to 2^-250 times an up half that makes a normal number of them."""
+    log(f"silu of far gates M={M}")
+    rng = np.random.default_rng(M)
+    g = rng.uniform(-170, -80, (M, 16))
+    low = np.maximum(g / np.log(2) * -1 - 120, 0)          # z >= 2^-115
+    u = 2.0 ** (low + (127 - low) * rng.random((M, 16)))
+    check_gated_alone(g, u * rng.choice([-1, 1], (M, 16)))
+
+
 def test_silu_of_nonfinite_and_huge_gates():
     inf = np.inf
     g = np.array([[inf, inf, -inf, np.nan, 1.0, 1.0, -1000.0, -3e38, 3e38, 1000.0, 0.0]])
