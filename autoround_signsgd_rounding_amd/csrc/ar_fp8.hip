@@ -206,7 +206,7 @@ __global__ __launch_bounds__(NT) void k_fp8_quant_weight(const T* W, int64_t N, 
 // ------------------------------------------------------------------ RMSNorm
 // v = x + residual rounded to T (the stored sum is what is normalised, as the
 // block's separate addition has it), the sum of squares in float64 (the block's
-// norm does the same, and no square of a finite input overflows), y = (v·r)·w in
+// norm does the same, and no square of a finite input overflows), y = (v/rms)·w in
 // float32, codes from the unrounded y. A row of up to 2048 is a wave's or a part
 // of a wave's, a longer one a workgroup's. It stays in registers, C chunks of 8
 // values per lane; C = 0 reads it twice. Every lane reads an element before it
@@ -297,7 +297,11 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
     __syncthreads();
     ss = ((red[0] + red[1]) + red[2]) + red[3];
   }
-  const float r = (float)(1.0 / sqrt(ss / (double)a.D + (double)a.eps));
+  // 1/rms as mantissa and exponent: without an eps it may lie outside float32's normal
+  // range while the normalised values, at most sqrt(D), do not
+  const double inv = 1.0 / sqrt(ss / (double)a.D + (double)a.eps);
+  const float r = (float)__builtin_amdgcn_frexp_mant(inv);
+  const int rexp = __builtin_amdgcn_frexp_exp(inv);
   auto finish = [&](int64_t k, const float (&u)[CH], const RowOf<T>& wv) {
     const bool in = k < a.D;
     float y[CH];
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_fp8(NormArgs a) {
       if (a.h) store_row(static_cast<T*>(a.h) + m * a.D + k, u);
       wv.get(y);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) y[i] = (u[i] * r) * y[i];
+      for (int i = 0; i < CH; ++i) y[i] = (ldexpf(u[i], rexp) * r) * y[i];
       if (a.y) store_row(static_cast<T*>(a.y) + m * a.D + k, y);
     }
     const float s = scale_of(amax_row(y));

@@ -1,12 +1,13 @@
 """The e4m3 operators where float32 steps, ranges and arguments run out: quotients
-halfway between two codes, SiLU of gates far from zero."""
+halfway between two codes, SiLU of gates far from zero, norms of rows at the ends of the
+range."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_common import F32, dev, log, to_np
 from oracle import fp8_ref as F
-from test_gpu_fp8 import activations, codes_of, given
+from test_gpu_fp8 import activations, check_codes, codes_of, given
 
 pytestmark = pytest.mark.gpu
 ar = pytest.importorskip("autoround_signsgd_rounding_amd")
@@ -123,3 +124,29 @@ def test_silu_of_nonfinite_and_huge_gates():
     assert np.all(s[0, [2, 3, 5, 6, 7, 10]] == 1.0)
     assert np.isnan(code[0, [0, 1, 2, 3, 4, 5, 8]]).all() and np.all(code[0, [6, 7, 10]] == 0.0)
     assert s[0, 9] == F32(2000.0) / F32(448.0)
+
+
+# ------------------------------------------------------------------ RMSNorm
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,D", [(40, 16), (7, 512), (3, 2048), (3, 8400), (2, 16400)])
+def test_rmsnorm_of_rows_at_the_ends_of_the_range(M, D, dtype):
+    """Without an eps a row of subnormal numbers is normalised like any other, and so is one
+    near the largest float; a row of zeros is 0/0. Tolerances as for other rows: y is within
+    4·2^-24 (and half a step of bf16), codes within 9·2^-24 of x/s."""
+    log(f"rmsnorm at the ends M={M} D={D} {dtype}")
+    rng = np.random.default_rng(M + D)
+    W, w = given(1 + 0.2 * rng.standard_normal(D), dtype)
+    for lift in (-146, -131, -127, 120, 125):
+        X, x = given(np.ldexp(np.round(4 * rng.standard_normal((M, D))).clip(-7, 7), lift), dtype)
+        keep = np.abs(x).max(1) > 0
+        o = ar.rmsnorm_fp8(X, W, 0.0, want_y=True)
+        torch.cuda.synchronize()
+        y = F.rmsnorm(x[keep], w, 0.0)
+        half = 2.0 ** -8 if dtype == "bf16" else 0.0
+        got = to_np(o.y).astype(np.float64)
+        assert np.all(np.abs(got[keep] - y) <= (half + 4 * U) * np.abs(y)), lift
+        want = F.act_scales(y)
+        q = o.q[torch.from_numpy(keep).to(dev()).nonzero()[:, 0]] if not keep.all() else o.q
+        s = o.scale[:, torch.from_numpy(keep).to(dev())]
+        check_codes(q, s, y, want, F.spread_act(want, D), np.full(1, 9 * U))
+        assert np.isnan(got[~keep]).all()
