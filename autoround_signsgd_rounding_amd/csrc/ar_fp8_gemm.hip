@@ -15,7 +15,7 @@
 // summed over, so any will do).
 //
 // Two kernels: k_fp8_rows for few rows, where W's bytes are the cost, and k_fp8_tile
-// for the rest; plan_of chooses. What bounds them, with a large copy at 4.8 TB/s
+// for the rest; ar_fp8_plan.h chooses. What bounds them, with a large copy at 4.8 TB/s
 // and a library e4m3 product with one scale per operand at 2.41 PFLOP/s
 // (16384 x 4096 x 4096) on the same card:
 //   rows, 1 x 29568 x 8192            43.9 us, 5.5 TB/s: memory
@@ -29,11 +29,10 @@
 // stores 35: all CUs end their tiles at about the same time, and a round of tiles
 // is 33 MB of Y. The float32 form converts every code a wave reads; its matrix
 // work alone would take 250 us.
-#include <math.h>
-
 #include <type_traits>
 
 #include "ar_device.h"
+#include "ar_fp8_plan.h"
 #include "ar_launch.h"
 
 namespace {
@@ -638,107 +637,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
 
 }  // namespace
 
-// Which kernel: the one with the least estimated time, in us. A tile takes `step`
-// of a CU per block of K when two workgroups share it, and `ends` for its prologue
-// and epilogue (`gap` of it where W's streaming is the cost and the rest is hidden
-// under it); with two K sets, which are taken when no CU gets a second workgroup,
-// a workgroup takes `step2` for two blocks. Streaming from memory (5.3 TB/s
-// measured; 12% less with two sets) and from the caches into LDS (14 TB/s; 12
-// where rows of K bytes break the 64-byte sectors) bound the time from below.
-// Measured (us), M x N x K, the rule's pick first:
-//   16 x 4096 x 4096            rows              6.5   32x64, two sets 8.8
-//   16 x 11008 x 4096           32x64, two sets  10.4   rows 13.9, 64x64 two sets 11.7
-//   64 x 11008 x 4096           64x64, two sets  12.3   one set 13.4, 32x64 14.7
-//   512 x 4096 x 4096           64x128, two sets 15.1   one set 17.5, 128x128 20.6
-//   1024 x 4096 x 4096          128x128, two     22.7   one set 25.4, 64x128 24.7
-//   2048 x 4096 x 4096          128x128          36.1   64x128 46.2, 256x256 50.0
-//   3806 x 2584 x 8656          256x256         118     128x128 139
-//   4096 x 4096 x 4096          256x256          59.8   128x128 69.8
-//   24 tokens, 4 of 64 experts, 2048 x 2048: 64x128 22.7, 32x64 25.2, rows 37.0
-//   333 x 4096 x 4096, float32  64x128, two sets 23.4   one set 28.2, 128x128 33.1
-// Over 78 shapes, dense and by expert, the pick takes 1.04 times the best one's
-// time in the mean, and 1.3 times it at the most. The float32 form runs at half
-// the matrix rate and on more registers: it has its own times, and no 256 x 256
-// tile.
-namespace {
-enum Kind { kRows, k32x64, k64x64, k64x128, k128x128, k256x256, kKinds };
-struct Times {
-  int tm, tn;
-  float step, ends, gap, step2;
-};
-constexpr Times kTimes[2][kKinds] = {
-    {{16, 16, 0, 0, 0, 0}, {32, 64, .1175f, 1.2f, .4f, .30f}, {64, 64, .1675f, 2.0f, .5f, .43f},
-     {64, 128, .287f, 2.4f, .7f, .62f}, {128, 128, .456f, 3.0f, 1.1f, .92f},
-     {256, 256, 1.52f, 9.0f, 9.0f, 0}},
-    {{16, 16, 0, 0, 0, 0}, {32, 64, .2025f, 1.2f, .4f, .50f}, {64, 64, .28f, 2.0f, .5f, .72f},
-     {64, 128, .505f, 2.4f, .7f, 1.12f}, {128, 128, .83f, 3.0f, 1.1f, 1.75f}, {}}};
-
-// Tiles of tm rows to expect: what E ranges of equal size need, and half a tile more
-// for each where sizes differ.
-double expected_tiles(const ArFp8Gemm& g, int tm) {
-  if (!g.offsets) return (double)((g.R + tm - 1) / tm);
-  const double used = (double)(g.E < g.R ? g.E : g.R);
-  const double t = (double)g.R / tm + 0.5 * used;
-  return t > used ? t : used;
-}
-// Tiles of tm rows that there can be at most.
-int64_t most_tiles(const ArFp8Gemm& g, int64_t tm) {
-  if (!g.offsets) return (g.R + tm - 1) / tm;
-  const int64_t t = g.R / tm + g.E;   // every range adds at most one ragged tile
-  return t < g.R ? t : g.R;
-}
-
-struct Plan {
-  Kind kind;
-  bool two;   // two K sets
-};
-Plan plan_of(const ArFp8Gemm& g) {
-  const double K = (double)g.K, N = (double)g.N, KB = (double)((g.K + BLK - 1) / BLK);
-  const double used = (double)(g.E < g.R ? g.E : g.R), mean = (double)g.R / used;
-  const double memory = (used * N + (double)g.R) * K / 5.3e6;
-  Plan best{k32x64, false};
-  double least = -1.0;
-  // Rows: every tile of 16 rows streams W, at 5.8 TB/s less X's share of the loads;
-  // by expert at 4.6 with a row each, at 4.0 with more. A CU takes 0.7 us per
-  // workgroup.
-  const double columns = (double)((g.N + 15) / 16);
-  if (mean <= 256 && most_tiles(g, 16) <= 65535) {
-    const double tiles = expected_tiles(g, 16);
-    const double share = 1.0 + 0.4 * (mean < 16 ? mean : 16) / 16;
-    const double rate = !g.offsets ? 5.8e6 : g.R <= g.E ? 4.6e6 : 4.0e6;
-    const double stream = tiles * N * K * share / rate;
-    least = KB / 8 * 0.45;
-    if (least < stream) least = stream;
-    if (least < tiles * columns / 256 * 0.7) least = tiles * columns / 256 * 0.7;
-    least += 3.0;
-    best.kind = kRows;
-  }
-  const double cache_rate = g.K % 64 == 0 ? 14e6 : 12e6;
-  for (int k = k32x64; k < kKinds; ++k) {
-    const Times& c = kTimes[g.ydt == AR_F32][k];
-    if (!c.tm) continue;
-    // by expert: some of the ragged tiles that uneven ranges add
-    const double t = expected_tiles(g, c.tm) * (double)((g.N + c.tn - 1) / c.tn) *
-                     (g.offsets ? 1.15 : 1.0);
-    const bool two = c.step2 > 0 && t <= 256;
-    const double rounds = ceil(t / 256);
-    double us = two ? 4.0 + 0.5 * (KB + 1) * c.step2 : 3.0 + rounds * (KB * c.step + c.ends);
-    const double stream = two ? 3.0 + 1.12 * memory : 3.0 + memory + rounds * c.gap;
-    const double cache = 3.0 + t * KB * (c.tm + c.tn) * BLK / cache_rate;
-    if (us < stream) us = stream;
-    if (us < cache) us = cache;
-    if (least < 0 || us < least) {
-      least = us;
-      best = Plan{(Kind)k, two};
-    }
-  }
-  return best;
-}
-}  // namespace
-
 template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
-static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
+static ar_status tile_launch(const Args& a, const ArFp8Shape& g, hipStream_t st) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
+  const int64_t tilesM = ar_fp8_most_tiles(g, C::TM);
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
   if (tilesM * tilesN * C::THREADS >= (int64_t(1) << 32)) return AR_ERR_SHAPE;   // HIP's limit
   hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>), dim3((unsigned)(tilesM * tilesN)),
@@ -746,36 +648,35 @@ static ar_status tile_launch(const Args& a, int64_t tilesM, hipStream_t st) {
   return last_status();
 }
 
-static ar_status rows_launch(const Args& a, int64_t tilesM, hipStream_t st) {
-  const dim3 g((unsigned)((a.N + 15) / 16), (unsigned)tilesM);
+static ar_status rows_launch(const Args& a, const ArFp8Shape& g, hipStream_t st) {
+  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)ar_fp8_most_tiles(g, 16));
   if (a.ydt == AR_BF16)
-    hipLaunchKernelGGL((k_fp8_rows<false>), g, dim3(64 * DW), 0, st, a);
+    hipLaunchKernelGGL((k_fp8_rows<false>), grid, dim3(64 * DW), 0, st, a);
   else
-    hipLaunchKernelGGL((k_fp8_rows<true>), g, dim3(64 * DW), 0, st, a);
+    hipLaunchKernelGGL((k_fp8_rows<true>), grid, dim3(64 * DW), 0, st, a);
   return last_status();
 }
 
 template <int WM, int WN, int MB, int NA, int NS1, int NS2>
-static ar_status tile_pick(const Args& a, int64_t tilesM, bool two, hipStream_t st) {
+static ar_status tile_pick(const Args& a, const ArFp8Shape& g, bool two, hipStream_t st) {
   if (a.ydt == AR_F32)
-    return two ? tile_launch<WM, WN, MB, NA, NS2, 2, true>(a, tilesM, st)
-               : tile_launch<WM, WN, MB, NA, NS1, 1, true>(a, tilesM, st);
-  return two ? tile_launch<WM, WN, MB, NA, NS2, 2, false>(a, tilesM, st)
-             : tile_launch<WM, WN, MB, NA, NS1, 1, false>(a, tilesM, st);
+    return two ? tile_launch<WM, WN, MB, NA, NS2, 2, true>(a, g, st)
+               : tile_launch<WM, WN, MB, NA, NS1, 1, true>(a, g, st);
+  return two ? tile_launch<WM, WN, MB, NA, NS2, 2, false>(a, g, st)
+             : tile_launch<WM, WN, MB, NA, NS1, 1, false>(a, g, st);
 }
 
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
   const Args a{g.X, g.xs, g.W, g.ws, g.offsets, g.row_index, g.Y, g.ydt, g.T, g.R, g.N, g.K,
                (int)g.E, (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
-  const Plan p = plan_of(g);
-  const int tm = kTimes[g.ydt == AR_F32][p.kind].tm;
-  const int64_t tiles = most_tiles(g, tm);
+  const ArFp8Shape shape{g.offsets != nullptr, g.ydt == AR_F32, g.R, g.N, g.K, g.E};
+  const ArFp8Plan p = ar_fp8_plan(shape);
   switch (p.kind) {
-    case kRows: return rows_launch(a, tiles, st);
-    case k32x64: return tile_pick<2, 2, 1, 2, 4, 4>(a, tiles, p.two, st);
-    case k64x64: return tile_pick<2, 2, 2, 2, 4, 4>(a, tiles, p.two, st);
-    case k64x128: return tile_pick<2, 2, 2, 4, 3, 3>(a, tiles, p.two, st);
-    case k128x128: return tile_pick<2, 2, 4, 4, 2, 2>(a, tiles, p.two, st);
-    default: return tile_launch<4, 2, 4, 8, 2, 1, false>(a, tiles, st);
+    case kRows: return rows_launch(a, shape, st);
+    case k32x64: return tile_pick<2, 2, 1, 2, 4, 4>(a, shape, p.two, st);
+    case k64x64: return tile_pick<2, 2, 2, 2, 4, 4>(a, shape, p.two, st);
+    case k64x128: return tile_pick<2, 2, 2, 4, 3, 3>(a, shape, p.two, st);
+    case k128x128: return tile_pick<2, 2, 4, 4, 2, 2>(a, shape, p.two, st);
+    default: return tile_launch<4, 2, 4, 8, 2, 1, false>(a, shape, st);
   }
 }

@@ -1,0 +1,174 @@
+"""Every kernel of the block-scaled e4m3 products, dense and by expert, on the shapes of
+fp8_shapes.py: whole outputs against float64 products on the GPU, bounds as in
+test_gpu_fp8.py (fp8_ref.product_bound over the sum of the terms' magnitudes, half a step
+of bf16 where the output is rounded to it), and offsets that name no valid ranges."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_shapes import DENSE, GROUPED
+from gpu_common import dev, log
+from oracle import fp8_ref as F
+
+pytestmark = pytest.mark.gpu
+ar = pytest.importorskip("autoround_signsgd_rounding_amd")
+
+F8 = torch.float8_e4m3fn
+OUT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def generator(*seed):
+    g = torch.Generator(device=dev())
+    g.manual_seed(sum(seed))
+    return g
+
+
+def codes(g, *shape):
+    return (112.0 * torch.randn(shape, generator=g, device=dev())).clamp_(-448, 448).to(F8)
+
+
+def scales(g, size, *shape):
+    return size * (0.5 + 1.5 * torch.rand(shape, generator=g, device=dev()))
+
+
+def operands(g, T, E, N, K):
+    return (codes(g, T, K), scales(g, 0.01, F.blocks(K), T), codes(g, E, N, K),
+            scales(g, 0.001, E, F.blocks(N), F.blocks(K)))
+
+
+def product64(xq, xs, wq, ws):
+    """(Y, sum of the terms' magnitudes) in float64."""
+    N, K = wq.shape
+    x = xq.double() * xs.double().repeat_interleave(128, 0)[:K].t()
+    w = wq.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    wt = w.t().contiguous()
+    return x @ wt, x.abs() @ wt.abs()
+
+
+def check(got, y, mag, K, out):
+    tol = F.product_bound(K) * mag
+    if out == "bf16":
+        tol = tol + 2.0 ** -8 * y.abs()
+    err = (got.double() - y).abs()
+    bad = err > tol
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist(), float(err.max()))
+
+
+def routed(rng, R, E):
+    """Offsets of E ranges of very different sizes, some empty, in rows 2 .. R - 4."""
+    p = np.exp(1.5 * rng.standard_normal(E)) * (rng.random(E) < 0.8)
+    p[rng.integers(E)] += 1e-3
+    counts = rng.multinomial(R - 5, p / p.sum())
+    return (2 + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
+
+
+@pytest.mark.parametrize("tile,sets,out,M,N,K", DENSE)
+def test_dense(tile, sets, out, M, N, K):
+    log(f"fp8_gemm {tile} x{sets} {out} M={M} N={N} K={K}")
+    xq, xs, wq, ws = operands(generator(M, N, K), M, 1, N, K)
+    Y = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])
+    again = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])
+    assert torch.equal(Y, again)
+    check(Y, *product64(xq, xs, wq[0], ws[0]), K, out)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("tile,sets,out,R,N,K,E", GROUPED)
+def test_by_expert(tile, sets, out, R, N, K, E, gather):
+    """Ragged ranges, empty experts, rows of no expert, rows that name no token and tokens
+    that several rows name."""
+    log(f"fp8_gemm_grouped {tile} x{sets} {out} R={R} N={N} K={K} E={E} gather={gather}")
+    g, rng = generator(R, N, K, E), np.random.default_rng(R + N + K + E)
+    off = routed(rng, R, E)
+    T = max(R // 3, 1) if gather else R
+    xq, xs, wq, ws = operands(g, T, E, N, K)
+    idx = None
+    if gather:
+        src = rng.integers(0, T, R).astype(np.int32)
+        src[rng.random(R) < 0.05] = -1
+        src[rng.random(R) < 0.05] = T
+        idx = torch.from_numpy(src).to(dev())
+    Y = torch.full((R, N), 5.0, dtype=OUT[out], device=dev())
+    ar.fp8_gemm_grouped(xq, xs, wq, ws, torch.from_numpy(off).to(dev()), row_index=idx, out=Y)
+    y, mag = torch.full((R, N), 5.0, dtype=torch.float64, device=dev()), torch.zeros(
+        (R, N), dtype=torch.float64, device=dev())
+    for e in range(E):
+        if off[e] == off[e + 1]:
+            continue
+        rows = torch.arange(off[e], off[e + 1], device=dev())
+        of = rows if idx is None else idx[rows].long()
+        y[rows] = 0.0
+        ok = (of >= 0) & (of < T)
+        if not ok.any():
+            continue
+        of = of[ok]
+        y[rows[ok]], mag[rows[ok]] = product64(xq.view(torch.uint8)[of].view(F8), xs[:, of],
+                                               wq[e], ws[e])
+    check(Y, y, mag, K, out)
+    assert torch.all(Y[:off[0]] == 5.0) and torch.all(Y[off[-1]:] == 5.0)
+
+
+def smallest():
+    """One shape by expert of each kernel."""
+    best = {}
+    for c in GROUPED:
+        k, size = c[:3], c[3] * c[4] * c[5] + c[4] * c[5] * c[6]
+        if k not in best or size < best[k][0]:
+            best[k] = (size, c)
+    return [c for _, c in best.values()]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("tile,sets,out,R,N,K,E", smallest())
+def test_offsets_without_valid_ranges_stay_inside(tile, sets, out, R, N, K, E, gather):
+    """Offsets outside [0, R], falling ones, ranges that overlap: rows are unspecified, but
+    nothing around Y changes and the call ends. (The kernels clamp each offset to [0, R], and
+    take at most as many tiles as were launched.)"""
+    log(f"bad offsets {tile} x{sets} {out} R={R} N={N} K={K} E={E} gather={gather}")
+    g, rng, G = generator(R, N, K, E), np.random.default_rng(R + N), 16
+    T = R // 2 if gather else R
+    ops = operands(g, T, E, N, K)
+    idx = None
+    if gather:
+        idx = torch.from_numpy(rng.integers(-9, T + 9, R).astype(np.int32)).to(dev())
+    inside = np.sort(rng.integers(0, R + 1, E + 1))
+    beyond = inside.copy()
+    beyond[0], beyond[-1] = -2 ** 31, 2 ** 31 - 1
+    big = torch.full((R + 2 * G, N), 3.0, dtype=OUT[out], device=dev())
+    for off in (beyond, inside[::-1], np.where(np.arange(E + 1) % 2, R, 0),
+                rng.integers(-R, 2 * R, E + 1)):
+        o = torch.from_numpy(np.ascontiguousarray(off).astype(np.int32)).to(dev())
+        ar.fp8_gemm_grouped(*ops, o, row_index=idx, out=big[G:G + R])
+        torch.cuda.synchronize()
+        assert torch.all(big[:G] == 3.0) and torch.all(big[G + R:] == 3.0)
+
+
+# ------------------------------------------------------------------ quantizer of long prompts
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(2050, 1040), (70, 30000), (1, 2200000), (16400, 144)])
+def test_quant_act_of_long_prompts(M, K, dtype, gate):
+    """More than 2^21 values: codes next to x/s, scales of their blocks. Ungated, both are those
+    of float32 divisions; gated, z is within 8·2^-24 and the scale within one more."""
+    log(f"quant_act M={M} K={K} {dtype} gate={gate}")
+    g = generator(M, K)
+    X = torch.randn((M, 2 * K if gate else K), generator=g, device=dev())
+    X *= torch.where(torch.rand((X.shape[1],), generator=g, device=dev()) < 0.02, 20.0, 1.0)
+    X[M // 2, : K // 2] = 0.0
+    X = X.to(OUT[dtype])
+    q, s = ar.fp8_quant_act(X, gate=gate)
+    z = X.double()
+    if gate:
+        z = z[:, :K] * torch.sigmoid(z[:, :K]) * z[:, K:]
+    KB = F.blocks(K)
+    pad = torch.nn.functional.pad(z, (0, KB * 128 - K)).view(M, KB, 128)
+    amax = pad.abs().amax(2).t()
+    want = torch.where(amax == 0, torch.ones_like(amax), amax / 448)
+    assert s.shape == want.shape
+    u = 2.0 ** -24
+    assert torch.all((s.double() - want).abs() <= (9.01 if gate else 1.0) * u * want)
+    t = z / s.double().t().repeat_interleave(128, 1)[:, :K]
+    v = q.double()
+    near = t.clamp(-448, 448).float().to(F8).double()
+    slack = (near - t).abs() + (2 * 9.01 if gate else 2) * u * t.abs() + 1e-30
+    assert torch.all((v - t).abs() <= slack)
