@@ -39,6 +39,7 @@ namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int BLK = 128;
 
@@ -184,6 +185,44 @@ struct FragOf<true> {
   }
 };
 
+// A block's term is p·(sw·sx), |p| in 2^-18 .. 2^25 or 0, and one fma adds it. Where s = sw·sx
+// leaves float32's normal range, though, the term need not. Below, s is off by up
+// to 2^-150 and the term by 2^-125, all of K's (2^15 blocks) by 2^-110: no half step of a
+// sum of 2^-86 or more. Above, the sum is infinite or NaN. So the kernels look at their sums when
+// all is added: where one is below 2^-80 or no finite number, they go through the scales
+// once Y is stored, and where there is such an s they sum that part of Y again, with
+// the scales' mantissas and exponents apart. (Tested at every block instead, 2 to 5% slower.)
+__device__ __forceinline__ bool out_of_range(float s) {
+  return __builtin_amdgcn_classf(s, 0x2F4);   // infinite, subnormal or zero
+}
+__device__ __forceinline__ f32x4_t add_block(f32x4_t acc, const f32x4_t& p, float sw, float sx) {
+  const float s = sw * sx;
+  const float m = __builtin_amdgcn_frexp_mantf(sw) * __builtin_amdgcn_frexp_mantf(sx);
+  const int e = __builtin_amdgcn_frexp_expf(sw) + __builtin_amdgcn_frexp_expf(sx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc[i] = out_of_range(s) ? acc[i] + ldexpf(p[i] * m, e) : fmaf(p[i], s, acc[i]);
+  return acc;
+}
+// Whether an element of Y is below 2^-80 or no finite number, in the bits as they are stored:
+// twice the magnitude's bits less twice 2^-80's, which a smaller magnitude makes wrap.
+struct Seen {
+  uint32_t f32 = 0;
+  u16x2_t bf16 = {0, 0};
+  template <bool BF16>
+  __device__ __forceinline__ void take(uint32_t v) {
+    if constexpr (BF16) {
+      const u16x2_t t = __builtin_bit_cast(u16x2_t, v) * (uint16_t)2 - (uint16_t)(2 * 0x1780);
+      bf16 = __builtin_elementwise_max(bf16, t);
+    } else {
+      f32 = max(f32, (v << 1) - 2u * 0x17800000u);
+    }
+  }
+  __device__ __forceinline__ bool odd() const {
+    return __any(f32 >= 0xFF000000u - 2u * 0x17800000u || max(bf16[0], bf16[1]) >= 0xFF00 - 2 * 0x1780);
+  }
+};
+
 // Two 16-byte chunks of a row, 64 bytes apart (p 16-byte aligned); in a row's last,
 // short block the chunks past the `left` bytes from p on are zero (K % 16 == 0).
 __device__ __forceinline__ i32x8_t frag(const uint8_t* p) {
@@ -203,6 +242,67 @@ __device__ __forceinline__ int64_t x_row(const Args& a, int64_t r) {
   if (!a.idx) return r;
   const int i = a.idx[r];
   return i >= 0 && i < a.T ? i : -1;
+}
+
+// The part of Y of rows r0 + r1 .. (16·MB of them, `rows` in the tile from r0 on) and columns n1 ..
+// (16·NA): whether the product of two scales is out of range.
+__device__ __forceinline__ bool far_scales(const Args& a, int64_t r0, int r1, int MB, int rows,
+                                           const float* wsp) {
+  const int lane = threadIdx.x & 63;
+  bool far = false;
+#pragma unroll 1
+  for (int b = 0; b < MB; ++b) {
+    const int r = r1 + b * 16 + (lane & 15);
+    const int64_t xr = r < rows ? x_row(a, r0 + r) : -1;
+    if (xr < 0) continue;
+#pragma unroll 4
+    for (int k = lane >> 4; k < a.KB; k += 4) {
+      const float sw = wsp[k], sx = a.xs[k * a.T + xr];
+      // (a zero, infinite or NaN scale gives the same either way)
+      far |= out_of_range(sw * sx) && !__builtin_amdgcn_classf(sw, 0x267) &&
+             !__builtin_amdgcn_classf(sx, 0x267);
+    }
+  }
+  return __any(far);
+}
+// The same part summed again straight from memory, 16 x 16 at a time, by add_block. K is
+// summed in `sets` parts and these are added in order, as in the kernel that calls, so that other
+// rows and columns keep their bits: set g takes the blocks from g·first on, `stride` apart,
+// up to `count` of them. What the wave stored there before has arrived first: other lanes did.
+template <bool WIDE>
+__device__ __forceinline__ void sum_again(const Args& a, int e, int64_t r0, int r1, int MB, int rows,
+                                          int64_t n1, int NA, const float* wsp, int sets, int first,
+                                          int stride, int count) {
+  typedef FragOf<WIDE> Op;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, kc = 16 * (lane >> 4);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll 1
+  for (int u = 0; u < MB * NA; ++u) {
+    const int r = r1 + u % MB * 16 + l16;
+    const int64_t n = n1 + u / MB * 16;
+    const int64_t xr = x_row(a, r0 + min(r, rows - 1));
+    const uint8_t* wp = a.W + ((int64_t)e * a.N + min(n + l16, a.N - 1)) * a.K + kc;
+    const uint8_t* xp = a.X + max(xr, (int64_t)0) * a.K + kc;
+    const float* xsp = a.xs + max(xr, (int64_t)0);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int g = 0; g < sets; ++g) {
+      f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        const int k = g * first + i * stride;
+        if (k >= a.KB) break;
+        const int left = (int)(a.K - (int64_t)k * BLK) - kc;
+        const f32x4_t p = Op::mul(Op::of(frag_tail(wp + (int64_t)k * BLK, left)),
+                                  Op::of(frag_tail(xp + (int64_t)k * BLK, left)));
+        acc = add_block(acc, p, wsp[k], xsp[(int64_t)k * a.T]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += acc[i];
+    }
+    if (xr < 0) v[0] = v[1] = v[2] = v[3] = 0.0f;
+    if (r < rows) store_y(a, r0 + r, n + 4 * (lane >> 4), v);
+  }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -272,7 +372,15 @@ __global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += red[w][lane][i];
     if (xr < 0) v[0] = v[1] = v[2] = v[3] = 0.0f;
-    if (l16 < rows) store_y(a, r0 + l16, n0 + 4 * (lane >> 4), v);
+    Seen seen;
+    if (l16 < rows) {
+      store_y(a, r0 + l16, n0 + 4 * (lane >> 4), v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n0 + 4 * (lane >> 4) + i < a.N) seen.take<false>(__float_as_uint(v[i]));
+    }
+    if (seen.odd() && far_scales(a, r0, 0, 1, rows, wsp))
+      sum_again<WIDE>(a, e, r0, 0, 1, rows, n0, 1, wsp, DW, 1, DW, (a.KB + DW - 1) / DW);
   }
 }
 
@@ -614,6 +722,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
     }
   O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
   const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
+  Seen seen;
   auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
     typedef decltype(unit) V;
     constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
@@ -625,6 +734,15 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
         V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
         if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
         else *d = v;   // runs that end inside a line are joined in L2
+        if constexpr (sizeof(V) < 4) {
+          seen.take<true>(v * 0x10001u);
+        } else {
+#pragma unroll
+          for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
+            if constexpr (sizeof(V) == 4) seen.take<sizeof(O) == 2>(v);
+            else seen.take<sizeof(O) == 2>(v[w]);
+          }
+        }
       }
     }
   };
@@ -633,6 +751,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
   else if (pitch % 8 == 0) write(u32x2_t{});
   else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
   else write(uint16_t{});
+  if (seen.odd() && far_scales(a, r0, wm * MB * 16, MB, rows, wsp))
+    sum_again<WIDE>(a, e, r0, wm * MB * 16, MB, rows, n0 + wn * NA * 16, NA, wsp, KG, steps, 1,
+                    steps);
 }
 
 }  // namespace

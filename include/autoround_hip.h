@@ -288,7 +288,8 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
    [NB, KB] (ar_fp8_quant_weight, E = 1). float32 accumulation, in a fixed order;
    ydt AR_F32 or AR_BF16. M = 0 or N = 0 is a no-op; K = 0 is AR_ERR_SHAPE, and so
    is a product whose launch would pass 2^32 threads (M*N beyond 2^36 or so). No
-   workspace.
+   workspace. The scales may be any float32: where the product of two leaves the
+   normal range, the block's term is formed without it.
    A float32 Y is summed in float32 throughout. For a bf16 Y the matrix unit adds
    the products of 8 neighbouring channels with 13 bits below the largest one's
    exponent, cutting the rest off, and everything else in float32: off by up to

@@ -143,6 +143,114 @@ def test_offsets_without_valid_ranges_stay_inside(tile, sets, out, R, N, K, E, g
         assert torch.all(big[:G] == 3.0) and torch.all(big[G + R:] == 3.0)
 
 
+# ------------------------------------------------------------------ ranges of the scales
+def smallest_dense():
+    """One dense shape of each kernel."""
+    best = {}
+    for c in DENSE:
+        k, size = c[:3], c[3] * c[4] * c[5] + c[4] * c[5]
+        if k not in best or size < best[k][0]:
+            best[k] = (size, c)
+    return [c for _, c in best.values()]
+
+
+def far_scales(g, rng, kind, xq, wq, T, E, N, K):
+    """Scales whose products leave float32's normal range, and codes that bring the terms back:
+    "tiny" near 2^-140 beside codes of every size; "huge" near 2^130 beside codes of 2^-9;
+    "mixed" 2^-185 to 2^60, another exponent for each row and block."""
+    xs, ws = scales(g, 1.0, F.blocks(K), T), scales(g, 1.0, E, F.blocks(N), F.blocks(K))
+    if kind == "tiny":
+        xs, ws = torch.ldexp(xs, torch.tensor(-90)), torch.ldexp(ws, torch.tensor(-50))
+    elif kind == "huge":
+        xs, ws = torch.ldexp(xs, torch.tensor(72)), torch.ldexp(ws, torch.tensor(58))
+        for q in (xq, wq):
+            q.copy_((q.float().sign() * 2.0 ** -9).to(F8))
+        xq.view(torch.uint8)[::3] = 0                         # their sums are 0, not 0·inf
+    else:
+        def by(of, shape):
+            return torch.from_numpy(2.0 ** rng.choice(of, shape).astype(np.float64)).to(
+                dev()).float()
+        xs, ws = xs * by([-124, -60, 0, 60], xs.shape), ws * by([-60, -1], ws.shape)
+    return xs, ws
+
+
+def cut_off(xq, xs, wq, ws):
+    """fp8_ref.unit_bound of the operands: the e4m3 unit adds 8 products at a time, and 7 of
+    them lose less than 2^-13 of the largest each."""
+    (M, K), N = xq.shape, wq.shape[0]
+    x = xq.double() * xs.double().repeat_interleave(128, 0)[:K].t()
+    w = wq.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    x, w = x.abs().view(M, K // 8, 8), w.abs().view(N, K // 8, 8)
+    lost, step = torch.zeros((M, N), dtype=torch.float64, device=dev()), max(1, 2 ** 24 // (M * N))
+    for k in range(0, K // 8, step):
+        lost += (x[:, None, k:k + step] * w[None, :, k:k + step]).amax(3).sum(2)
+    return lost * 7 * 2.0 ** -13
+
+
+def check_far(got, xq, xs, wq, ws, out):
+    """The bounds of test_gpu_fp8.py, a bf16 result's with what the e4m3 unit cuts off (one
+    block of few channels may be all that counts here), and what terms and results below the
+    normal range lose: half a step of the smallest float32 (2^-150) per term and sum, and half
+    the smallest bf16's (2^-134)."""
+    K = xq.shape[1]
+    y, mag = product64(xq, xs, wq, ws)
+    assert torch.isfinite(y).all() and y.abs().max() < 2.0 ** 127
+    tol = F.product_bound(K) * mag + (2 * F.blocks(K) + 2) * 2.0 ** -150
+    if out == "bf16":
+        tol = tol + cut_off(xq, xs, wq, ws) + 2.0 ** -8 * y.abs() + 2.0 ** -134
+    err = (got.double() - y).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("kind", ["tiny", "huge", "mixed"])
+@pytest.mark.parametrize("tile,sets,out,M,N,K", smallest_dense())
+def test_scales_whose_product_is_no_float32(tile, sets, out, M, N, K, kind):
+    log(f"fp8_gemm far scales {kind} {tile} x{sets} {out} M={M} N={N} K={K}")
+    g, rng = generator(M, N, K), np.random.default_rng(M + N + K)
+    xq, _, wq, _ = operands(g, M, 1, N, K)
+    xs, ws = far_scales(g, rng, kind, xq, wq, M, 1, N, K)
+    Y = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])
+    check_far(Y, xq, xs, wq[0], ws[0], out)
+
+
+@pytest.mark.parametrize("kind", ["tiny", "huge", "mixed"])
+@pytest.mark.parametrize("tile,sets,out,R,N,K,E", smallest())
+def test_scales_whose_product_is_no_float32_by_expert(tile, sets, out, R, N, K, E, kind):
+    """Rows of no expert keep what they held, rows without a token are zero, here too."""
+    log(f"fp8_gemm_grouped far scales {kind} {tile} x{sets} {out} R={R} N={N} K={K} E={E}")
+    g, rng = generator(R, N, K, E), np.random.default_rng(R + N + K + E)
+    off, T = routed(rng, R, E), R // 2
+    xq, _, wq, _ = operands(g, T, E, N, K)
+    xs, ws = far_scales(g, rng, kind, xq, wq, T, E, N, K)
+    src = rng.integers(0, T, R).astype(np.int32)
+    src[rng.random(R) < 0.1] = -1
+    idx = torch.from_numpy(src).to(dev())
+    Y = torch.full((R, N), 5.0, dtype=OUT[out], device=dev())
+    ar.fp8_gemm_grouped(xq, xs, wq, ws, torch.from_numpy(off).to(dev()), row_index=idx, out=Y)
+    for e in range(E):
+        rows = torch.arange(off[e], off[e + 1], device=dev())
+        of = idx[rows].long()
+        assert torch.all(Y[rows[of < 0]] == 0.0)
+        rows, of = rows[of >= 0], of[of >= 0]
+        if len(rows):
+            check_far(Y[rows], xq.view(torch.uint8)[of].view(F8), xs[:, of], wq[e], ws[e], out)
+    assert torch.all(Y[:off[0]] == 5.0) and torch.all(Y[off[-1]:] == 5.0)
+
+
+@pytest.mark.parametrize("tile,sets,out,M,N,K", [c for c in smallest_dense() if c[0] != "rows"])
+def test_rows_beside_far_scales_keep_their_bits(tile, sets, out, M, N, K):
+    """A far scale in one row, and an infinite one in another: every other row as without."""
+    log(f"fp8_gemm beside far scales {tile} x{sets} {out} M={M} N={N} K={K}")
+    xq, xs, wq, ws = operands(generator(M, N, K), M, 1, N, K)
+    clean = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])
+    xs[-1, 1], xs[0, 3] = 2.0 ** -125, float("inf")
+    Y = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=OUT[out])
+    keep = torch.ones(M, dtype=torch.bool, device=dev())
+    keep[1] = keep[3] = False
+    assert torch.equal(Y[keep], clean[keep]) and not torch.isfinite(Y[3]).any()
+
+
 # ------------------------------------------------------------------ quantizer of long prompts
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
