@@ -729,6 +729,8 @@ def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
         out = torch.empty_strided((M, N), (N, 1), dtype=out_dtype or torch.bfloat16, device=dev)
     elif not _is(out, (M, N), out.dtype, dev) or out.dtype not in (torch.float32, torch.bfloat16):
         _refuse(out, "out", (M, N), (torch.float32, torch.bfloat16))
+    elif out_dtype is not None and out_dtype is not out.dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     st = lib.ar_fp8_gemm(Xq.data_ptr(), xs.data_ptr(), M, K, Wq.data_ptr(), ws.data_ptr(), N,
                          out.data_ptr(), _dt(out), torch._C._cuda_getCurrentRawStream(dev))
     if st:
@@ -765,6 +767,8 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
         out = torch.empty_strided((R, N), (N, 1), dtype=out_dtype or torch.bfloat16, device=dev)
     elif not _is(out, (R, N), out.dtype, dev) or out.dtype not in (torch.float32, torch.bfloat16):
         _refuse(out, "out", (R, N), (torch.float32, torch.bfloat16))
+    elif out_dtype is not None and out_dtype is not out.dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     st = lib.ar_fp8_gemm_grouped(Xq.data_ptr(), xs.data_ptr(), T, K, Wq.data_ptr(), ws.data_ptr(),
                                  E, N, offsets.data_ptr(), index, R, out.data_ptr(), _dt(out),
                                  torch._C._cuda_getCurrentRawStream(dev))

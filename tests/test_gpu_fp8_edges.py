@@ -1,6 +1,6 @@
 """The e4m3 operators where float32 steps, ranges and arguments run out: quotients
 halfway between two codes, SiLU of gates far from zero, norms of rows at the ends of the
-range."""
+range; arguments that contradict each other."""
 import numpy as np
 import pytest
 import torch
@@ -150,3 +150,30 @@ def test_rmsnorm_of_rows_at_the_ends_of_the_range(M, D, dtype):
         s = o.scale[:, torch.from_numpy(keep).to(dev())]
         check_codes(q, s, y, want, F.spread_act(want, D), np.full(1, 9 * U))
         assert np.isnan(got[~keep]).all()
+
+
+# ------------------------------------------------------------------ arguments
+def products(M=8, N=144, K=256, E=3):
+    """The two products as functions of their keywords, on operands of zeros."""
+    z = lambda *s, d=torch.float32: torch.zeros(s, dtype=d, device=dev())   # noqa: E731
+    f8 = torch.float8_e4m3fn
+    x, w, w3 = (z(M, K, d=f8), z(2, M)), (z(N, K, d=f8), z(2, 2)), (z(E, N, K, d=f8), z(E, 2, 2))
+    off = z(E + 1, d=torch.int32)
+    return (lambda **kw: ar.fp8_gemm(*x, *w, **kw),
+            lambda **kw: ar.fp8_gemm_grouped(*x, *w3, off, **kw))
+
+
+def test_out_dtype_agrees_with_out():
+    """An out_dtype beside an out of another type is refused, in both products."""
+    types = (torch.float32, torch.bfloat16)
+    for call in products():
+        for a in types:
+            out = torch.empty((8, 144), dtype=a, device=dev())
+            assert call(out=out) is out and call(out=out, out_dtype=a) is out
+            for b in types + (torch.float16,):
+                if b is not a:
+                    with pytest.raises(ValueError, match="out_dtype"):
+                        call(out=out, out_dtype=b)
+                    with pytest.raises(ValueError, match="out_dtype"):
+                        call(out=out, out_dtype=b, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
