@@ -37,6 +37,8 @@ EXPORTS = (
 
 # input channels per scale of the e4m3 operands
 FP8_BLOCK = 128
+# added to the dtype of an e4m3 product's bf16 output: summed like a float32 one
+AR_F32_SUMS = 0x100
 
 # fixed scratch of ar_tune_step_noalloc per GPU (AR_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -714,17 +716,20 @@ def _fp8_operands(Xq, xs, Wq, ws, dims: int):
     return T, K, N, dev
 
 
-def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
+def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, float32_sums: bool = False,
+             stream=None):
     """Y [M, N] (bf16 unless ``out_dtype`` or ``out`` say float32) = X·Wᵀ of e4m3
     operands with their block scales (ar_fp8_gemm): Xq [M, K], xs [ceil(K/128), M]
     from fp8_quant_act or rmsnorm_fp8; Wq [N, K], ws from fp8_quant_weight. A float32
-    Y is summed in float32 throughout, at half the matrix rate; for a bf16 one the
-    matrix unit adds 8 products at a time with 13 bits below the largest."""
+    Y is summed in float32 throughout, at half the matrix rate, and so is a bf16 one
+    with ``float32_sums``; without it the matrix unit adds 8 products at a time with 13
+    bits below the largest."""
     torch = _torch()
     M, K, N, dev = _fp8_operands(Xq, xs, Wq, ws, 2)
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _elsewhere(stream, Xq, xs, Wq, ws, out):
-            return fp8_gemm(Xq, xs, Wq, ws, out_dtype=out_dtype, out=out)
+            return fp8_gemm(Xq, xs, Wq, ws, out_dtype=out_dtype, out=out,
+                            float32_sums=float32_sums)
     if out is None:
         out = torch.empty_strided((M, N), (N, 1), dtype=out_dtype or torch.bfloat16, device=dev)
     elif not _is(out, (M, N), out.dtype, dev) or out.dtype not in (torch.float32, torch.bfloat16):
@@ -732,26 +737,27 @@ def fp8_gemm(Xq, xs, Wq, ws, *, out_dtype=None, out=None, stream=None):
     elif out_dtype is not None and out_dtype is not out.dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     st = lib.ar_fp8_gemm(Xq.data_ptr(), xs.data_ptr(), M, K, Wq.data_ptr(), ws.data_ptr(), N,
-                         out.data_ptr(), _dt(out), torch._C._cuda_getCurrentRawStream(dev))
+                         out.data_ptr(), _dt(out) | (AR_F32_SUMS if float32_sums else 0),
+                         torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "ar_fp8_gemm")
     return out
 
 
 def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None, out=None,
-                     stream=None):
+                     float32_sums: bool = False, stream=None):
     """Y [R, N]: rows offsets[e]..offsets[e+1] are the product with expert e's
     weight (ar_fp8_gemm_grouped): Wq [E, N, K] and ws from fp8_quant_weight,
     offsets [E + 1] int32 on the GPU. ``row_index`` [R] int32 names the row of
     Xq behind each row of Y (None: R = Xq's rows, in order). Rows of Y outside
     the offsets keep what ``out`` held (without ``out`` they hold nothing
-    meaningful)."""
+    meaningful). ``float32_sums`` as in fp8_gemm."""
     torch = _torch()
     T, K, N, dev = _fp8_operands(Xq, xs, Wq, ws, 3)
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _elsewhere(stream, Xq, xs, Wq, ws, offsets, row_index, out):
             return fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, row_index=row_index,
-                                    out_dtype=out_dtype, out=out)
+                                    out_dtype=out_dtype, out=out, float32_sums=float32_sums)
     E = Wq.shape[0]
     if offsets is None or not _is(offsets, (E + 1,), torch.int32, dev):
         _refuse(offsets, "offsets", (E + 1,), torch.int32)
@@ -770,7 +776,8 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
     elif out_dtype is not None and out_dtype is not out.dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     st = lib.ar_fp8_gemm_grouped(Xq.data_ptr(), xs.data_ptr(), T, K, Wq.data_ptr(), ws.data_ptr(),
-                                 E, N, offsets.data_ptr(), index, R, out.data_ptr(), _dt(out),
+                                 E, N, offsets.data_ptr(), index, R, out.data_ptr(),
+                                 _dt(out) | (AR_F32_SUMS if float32_sums else 0),
                                  torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "ar_fp8_gemm_grouped")

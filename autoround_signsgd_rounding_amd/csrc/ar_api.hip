@@ -1010,6 +1010,13 @@ ar_status check_fp8_rows(int64_t M, int64_t K) {
   return K % 16 == 0 && K < kMaxLd ? AR_OK : AR_ERR_SHAPE;
 }
 
+// Y's type and whether its sums are float32 throughout.
+ar_status fp8_out(int32_t* ydt, bool* wide) {
+  *wide = (*ydt & AR_F32_SUMS) != 0 || *ydt == AR_F32;
+  *ydt &= ~AR_F32_SUMS;
+  return dtype_ok(*ydt) ? AR_OK : AR_ERR_UNSUPPORTED;
+}
+
 ar_status check_fp8_gemm(int64_t E, int64_t R, int64_t N, int64_t K) {
   if (E < 1 || E > kMaxExperts || K == 0) return AR_ERR_SHAPE;
   AR_TRY(check_fp8_rows(R, K));
@@ -1059,11 +1066,12 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
 ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
                       const float* ws, int64_t N, void* Y, int32_t ydt, void* stream) {
   AR_TRY(check_fp8_gemm(1, M, N, K));
-  if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
+  bool wide;
+  AR_TRY(fp8_out(&ydt, &wide));
   if (M == 0 || N == 0) return AR_OK;
   if (!Xq || !xs || !Wq || !ws || !Y) return AR_ERR_INVALID_ARG;
   if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a16(Y)) return AR_ERR_INVALID_ARG;
-  return ar_launch_fp8_gemm(ArFp8Gemm{Xq, xs, Wq, ws, nullptr, nullptr, Y, ydt, M, M, N, K, 1},
+  return ar_launch_fp8_gemm(ArFp8Gemm{Xq, xs, Wq, ws, nullptr, nullptr, Y, ydt, M, M, N, K, 1, wide},
                             static_cast<hipStream_t>(stream));
 }
 
@@ -1073,7 +1081,8 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
                               int32_t ydt, void* stream) {
   AR_TRY(check_fp8_gemm(E, R, N, K));
   AR_TRY(check_fp8_rows(T, K));
-  if (!dtype_ok(ydt)) return AR_ERR_UNSUPPORTED;
+  bool wide;
+  AR_TRY(fp8_out(&ydt, &wide));
   if (R == 0 || N == 0) return AR_OK;
   if (row_index ? T * K >= (int64_t(1) << 32) : T != R) return AR_ERR_SHAPE;
   if (T == 0) return AR_ERR_SHAPE;   // an index needs a row to point at
@@ -1081,7 +1090,7 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
   if (!a16(Xq) || !a4(xs) || !a16(Wq) || !a4(ws) || !a4(offsets) || !a4(row_index) || !a16(Y))
     return AR_ERR_INVALID_ARG;
   return ar_launch_fp8_gemm(
-      ArFp8Gemm{Xq, xs, Wq, ws, offsets, row_index, Y, ydt, T, R, N, K, E},
+      ArFp8Gemm{Xq, xs, Wq, ws, offsets, row_index, Y, ydt, T, R, N, K, E, wide},
       static_cast<hipStream_t>(stream));
 }
 

@@ -141,8 +141,9 @@ __device__ __forceinline__ void store_y(const Args& a, int64_t r, int64_t n, con
 // the largest, cutting the rest off (measured with single products beside a pair that
 // cancels), and only those sums in float32: 1.3e-5 to 3.7e-5 of the block's sum on
 // random operands, a hundredth of the half step of a bf16 output (2^-9 on
-// average). For a float32 output that would be the largest error by far,
-// so there the codes are widened to bf16 (exact) and multiplied by
+// average), and far below the operands' own rounding to e4m3 (2^-4 of a product). For
+// a float32 output that would be the largest error by far, so there, and where float32
+// sums are asked for, the codes are widened to bf16 (exact) and multiplied by
 // v_mfma_f32_16x16x32_bf16 (1e-8, measured), at half the rate.
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 struct WideFrag {
@@ -702,55 +703,60 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
         for (int t = 0; t < NA; ++t) acc[t][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
   }
-  typedef std::conditional_t<WIDE, float, uint16_t> O;
-  constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
-  static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
-  uint8_t* own = lds + wave * (MB * 16 * RB);
-  auto at = [&](int r, int byte) {   // 16-byte chunks spread over the banks by row
-    return own + r * RB + (byte ^ ((r & (RB / 16 - 1)) * 16));
-  };
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int t = 0; t < NA; ++t) {
-      const f32x4_t v = acc[t][b];
-      uint8_t* d = at(16 * b + l16, (16 * t + 4 * q) * (int)sizeof(O));
-      if constexpr (sizeof(O) == 2)
-        *reinterpret_cast<u32x2_t*>(d) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-      else
-        *reinterpret_cast<f32x4_t*>(d) = v;
-    }
-  O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
-  const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
   Seen seen;
-  auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
-    typedef decltype(unit) V;
-    constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
-#pragma unroll 8
-    for (int i = lane; i < MB * 16 * UPR; i += 64) {
-      const int r = i / UPR, u = i % UPR;
-      if (r < mleft && u * PER < nleft) {
-        const V v = *reinterpret_cast<const V*>(at(r, u * (int)sizeof(V)));
-        V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
-        if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
-        else *d = v;   // runs that end inside a line are joined in L2
-        if constexpr (sizeof(V) < 4) {
-          seen.take<true>(v * 0x10001u);
-        } else {
+  auto leave = [&](auto zero) {      // Y's rows as its type O
+    typedef decltype(zero) O;
+    constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
+    static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
+    uint8_t* own = lds + wave * (MB * 16 * RB);
+    auto at = [&](int r, int byte) {   // 16-byte chunks spread over the banks by row
+      return own + r * RB + (byte ^ ((r & (RB / 16 - 1)) * 16));
+    };
 #pragma unroll
-          for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
-            if constexpr (sizeof(V) == 4) seen.take<sizeof(O) == 2>(v);
-            else seen.take<sizeof(O) == 2>(v[w]);
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int t = 0; t < NA; ++t) {
+        const f32x4_t v = acc[t][b];
+        uint8_t* d = at(16 * b + l16, (16 * t + 4 * q) * (int)sizeof(O));
+        if constexpr (sizeof(O) == 2)
+          *reinterpret_cast<u32x2_t*>(d) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        else
+          *reinterpret_cast<f32x4_t*>(d) = v;
+      }
+    O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
+    const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
+    auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
+      typedef decltype(unit) V;
+      constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
+#pragma unroll 8
+      for (int i = lane; i < MB * 16 * UPR; i += 64) {
+        const int r = i / UPR, u = i % UPR;
+        if (r < mleft && u * PER < nleft) {
+          const V v = *reinterpret_cast<const V*>(at(r, u * (int)sizeof(V)));
+          V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
+          if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
+          else *d = v;   // runs that end inside a line are joined in L2
+          if constexpr (sizeof(V) < 4) {
+            seen.take<true>(v * 0x10001u);
+          } else {
+#pragma unroll
+            for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
+              if constexpr (sizeof(V) == 4) seen.take<sizeof(O) == 2>(v);
+              else seen.take<sizeof(O) == 2>(v[w]);
+            }
           }
         }
       }
-    }
+    };
+    const int64_t pitch = a.N * (int64_t)sizeof(O);
+    if (pitch % 16 == 0) write(u32x4_t{});
+    else if (pitch % 8 == 0) write(u32x2_t{});
+    else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
+    else write(uint16_t{});
   };
-  const int64_t pitch = a.N * (int64_t)sizeof(O);
-  if (pitch % 16 == 0) write(u32x4_t{});
-  else if (pitch % 8 == 0) write(u32x2_t{});
-  else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
-  else write(uint16_t{});
+  if constexpr (!WIDE) leave(uint16_t{});
+  else if (a.ydt == AR_BF16) leave(uint16_t{});
+  else leave(0.0f);
   if (seen.odd() && far_scales(a, r0, wm * MB * 16, MB, rows, wsp))
     sum_again<WIDE>(a, e, r0, wm * MB * 16, MB, rows, n0 + wn * NA * 16, NA, wsp, KG, steps, 1,
                     steps);
@@ -771,16 +777,16 @@ static ar_status tile_launch(const Args& a, const ArFp8Shape& g, hipStream_t st)
 
 static ar_status rows_launch(const Args& a, const ArFp8Shape& g, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)ar_fp8_most_tiles(g, 16));
-  if (a.ydt == AR_BF16)
-    hipLaunchKernelGGL((k_fp8_rows<false>), grid, dim3(64 * DW), 0, st, a);
-  else
+  if (g.wide)
     hipLaunchKernelGGL((k_fp8_rows<true>), grid, dim3(64 * DW), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_fp8_rows<false>), grid, dim3(64 * DW), 0, st, a);
   return last_status();
 }
 
 template <int WM, int WN, int MB, int NA, int NS1, int NS2>
 static ar_status tile_pick(const Args& a, const ArFp8Shape& g, bool two, hipStream_t st) {
-  if (a.ydt == AR_F32)
+  if (g.wide)
     return two ? tile_launch<WM, WN, MB, NA, NS2, 2, true>(a, g, st)
                : tile_launch<WM, WN, MB, NA, NS1, 1, true>(a, g, st);
   return two ? tile_launch<WM, WN, MB, NA, NS2, 2, false>(a, g, st)
@@ -790,7 +796,7 @@ static ar_status tile_pick(const Args& a, const ArFp8Shape& g, bool two, hipStre
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
   const Args a{g.X, g.xs, g.W, g.ws, g.offsets, g.row_index, g.Y, g.ydt, g.T, g.R, g.N, g.K,
                (int)g.E, (int)((g.N + BLK - 1) / BLK), (int)((g.K + BLK - 1) / BLK)};
-  const ArFp8Shape shape{g.offsets != nullptr, g.ydt == AR_F32, g.R, g.N, g.K, g.E};
+  const ArFp8Shape shape{g.offsets != nullptr, g.wide, g.R, g.N, g.K, g.E};
   const ArFp8Plan p = ar_fp8_plan(shape);
   switch (p.kind) {
     case kRows: return rows_launch(a, shape, st);

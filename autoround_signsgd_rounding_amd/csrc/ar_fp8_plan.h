@@ -7,7 +7,7 @@
 
 struct ArFp8Shape {
   bool grouped;   // by expert
-  bool wide;      // float32 sums throughout (a float32 Y)
+  bool wide;      // float32 sums throughout (a float32 Y, or asked for)
   int64_t R, N, K, E;
 };
 

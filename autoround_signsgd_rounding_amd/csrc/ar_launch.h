@@ -215,7 +215,7 @@ ar_status ar_launch_rmsnorm_fp8(int dt, const void* x, const void* res, const vo
 
 // Block-scaled e4m3 product (ar_fp8_gemm.hip): Y [R, N] from X [T, K] and
 // W [E, N, K]; offsets [E + 1] NULL for one expert with all R rows, row_index
-// [R] NULL for row r of X.
+// [R] NULL for row r of X; wide: sums in float32 throughout (always so for a float32 Y).
 struct ArFp8Gemm {
   const uint8_t* X;
   const float* xs;
@@ -226,5 +226,6 @@ struct ArFp8Gemm {
   void* Y;
   int ydt;
   int64_t T, R, N, K, E;
+  bool wide;
 };
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st);

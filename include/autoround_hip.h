@@ -295,12 +295,14 @@ ar_status ar_rmsnorm_fp8(int32_t dt, const void* x, const void* residual, const 
    exponent, cutting the rest off, and everything else in float32: off by up to
    4e-5 of a block's sum for products of like sizes, far below a bf16 rounding.
    Where large products cancel within 8 channels and the small ones are what
-   counts, take a float32 Y. */
+   counts, take a float32 Y, or AR_BF16 | AR_F32_SUMS for ydt: a bf16 Y summed like
+   a float32 one and rounded once, at half the matrix rate. */
+#define AR_F32_SUMS 0x100
 ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, const uint8_t* Wq,
                       const float* ws, int64_t N, void* Y, int32_t ydt, void* stream);
 
 /* The product by expert: rows offsets[e] <= r < offsets[e+1] of Y [R, N] are
-   X_row(r)·Wq[e]ᵀ as above, with Wq [E, N, K], ws [E, NB, KB], Xq [T, K], xs [KB, T].
+   X_row(r)·Wq[e]ᵀ as above, ydt too, with Wq [E, N, K], ws [E, NB, KB], Xq [T, K], xs [KB, T].
    offsets [E+1] int32 on the device, non-decreasing, in [0, R]; an expert may have
    no rows; rows outside [offsets[0], offsets[E]) keep what they held. row_index
    [R] int32 on the device: row(r) = row_index[r], so a token's codes serve each of

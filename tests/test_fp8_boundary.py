@@ -95,3 +95,12 @@ def test_grouped_validation():
         assert grouped(**kw) == INV
     assert grouped(T=0, R=0) == grouped(T=9, idx=P, R=0) == OK
 
+
+
+@pytest.mark.parametrize("f", [gemm, grouped])
+def test_sums_flag_validation(f):
+    """AR_F32_SUMS goes with either output type; other bits are refused."""
+    for ydt in (0, 1, 0x100, 0x101):
+        assert f(ydt=ydt, N=0) == OK and f(ydt=ydt, Y=NULL) == INV
+    for ydt in (2, 0x102, 0x200, 0x201, 0x301, -1, -256):
+        assert f(ydt=ydt) == f(ydt=ydt, N=0) == UNSUP

@@ -251,6 +251,54 @@ def test_rows_beside_far_scales_keep_their_bits(tile, sets, out, M, N, K):
     assert torch.equal(Y[keep], clean[keep]) and not torch.isfinite(Y[3]).any()
 
 
+# ------------------------------------------------------------------ float32 sums
+@pytest.mark.parametrize("tile,sets,out,M,N,K", [c for c in DENSE if c[2] == "f32"])
+def test_float32_sums_of_a_bf16_output(tile, sets, out, M, N, K):
+    """The bits of a float32 output, rounded."""
+    log(f"fp8_gemm float32 sums {tile} x{sets} M={M} N={N} K={K}")
+    xq, xs, wq, ws = operands(generator(M, N, K), M, 1, N, K)
+    want = ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=torch.float32)
+    assert torch.equal(ar.fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=torch.float32,
+                                   float32_sums=True), want)
+    got = ar.fp8_gemm(xq, xs, wq[0], ws[0], float32_sums=True)
+    assert got.dtype is torch.bfloat16 and torch.equal(got, want.bfloat16())
+    got.fill_(3.0)
+    ar.fp8_gemm(xq, xs, wq[0], ws[0], float32_sums=True, out=got, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want.bfloat16())
+
+
+@pytest.mark.parametrize("tile,sets,out,R,N,K,E", [c for c in GROUPED if c[2] == "f32"])
+def test_float32_sums_of_a_bf16_output_by_expert(tile, sets, out, R, N, K, E):
+    log(f"fp8_gemm_grouped float32 sums {tile} x{sets} R={R} N={N} K={K} E={E}")
+    rng = np.random.default_rng(R + N + K + E)
+    off, T = torch.from_numpy(routed(rng, R, E)).to(dev()), R // 2
+    ops = operands(generator(R, N, K, E), T, E, N, K)
+    idx = torch.from_numpy(rng.integers(-1, T + 1, R).astype(np.int32)).to(dev())
+    want, got = (torch.full((R, N), 5.0, dtype=d, device=dev())
+                 for d in (torch.float32, torch.bfloat16))
+    ar.fp8_gemm_grouped(*ops, off, row_index=idx, out=want)
+    ar.fp8_gemm_grouped(*ops, off, row_index=idx, out=got, float32_sums=True)
+    assert torch.equal(got, want.bfloat16())
+
+
+@pytest.mark.parametrize("M,N", [(3, 100), (200, 140), (700, 300), (3100, 4100)])
+def test_float32_sums_of_outliers_that_cancel(M, N):
+    """Products of 448^2 that cancel beside products near 1: a bf16 result of float32 sums is
+    within a float32 result's bound and its own rounding, which the e4m3 unit's sums miss."""
+    log(f"fp8_gemm float32 sums of outliers M={M} N={N}")
+    g, K = generator(M, N), 400
+    xq, xs, wq, ws = operands(g, M, 1, N, K)
+    x, w = (torch.randn((n, K), generator=g, device=dev()) for n in (M, N))
+    for j in range(F.blocks(K)):
+        x[:, 128 * j + 5], x[:, 128 * j + 6], w[:, 128 * j + 5:128 * j + 7] = 448.0, -448.0, 448.0
+    xq, wq = x.to(F8), w.to(F8)[None]
+    y, mag = product64(xq, xs, wq[0], ws[0])
+    check(ar.fp8_gemm(xq, xs, wq[0], ws[0], float32_sums=True), y, mag, K, "bf16")
+    off = torch.tensor([0, M], dtype=torch.int32, device=dev())
+    check(ar.fp8_gemm_grouped(xq, xs, wq, ws, off, float32_sums=True), y, mag, K, "bf16")
+
+
 # ------------------------------------------------------------------ quantizer of long prompts
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
