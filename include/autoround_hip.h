@@ -250,8 +250,9 @@ ar_status ar_dequant_gemm(int32_t bits, int32_t group_size, const uint16_t* X, i
    ar_rmsnorm_fp8 beside the block's RMSNorm, ar_fp8_gemm and
    ar_fp8_gemm_grouped beside ar_dequant_gemm. Codes are passed as uint8 bit
    patterns. KB = ceil(K/128) and NB = ceil(N/128); K (and D) must be a multiple
-   of 16, and a last block may be shorter than 128. Scale and index arrays need
-   4-byte alignment only.
+   of 16 below 2^22, rows and N stay below 2^23, and a last block may be shorter
+   than 128; other sizes are AR_ERR_SHAPE. Scale and index arrays need 4-byte
+   alignment, the others 16.
 
    Scale of a block: s = 1 if its largest magnitude amax is 0, else
    max(amax/448, 2^-126); code = e4m3(x/s), round to nearest even. Both quotients
@@ -268,7 +269,7 @@ ar_status ar_fp8_quant_act(int32_t xdt, const void* X, int32_t gate, int64_t M, 
 
 /* Weights of E layers (E = 1: one Linear; more: the experts of a fused layer):
    W [E, N, K] -> q [E, N, K], scale [E, NB, KB], one scale per 128 x 128 block.
-   E*N*K = 0 is a no-op. */
+   E*N*K = 0 is a no-op; E*NB*KB < 2^24. */
 ar_status ar_fp8_quant_weight(int32_t wdt, const void* W, int64_t E, int64_t N, int64_t K,
                               uint8_t* q, float* scale, void* stream);
 
@@ -310,8 +311,8 @@ ar_status ar_fp8_gemm(const uint8_t* Xq, const float* xs, int64_t M, int64_t K, 
    a row of zeros); NULL: row(r) = r, and T must equal R. The contents of offsets
    are not checked on the host: offsets outside [0, R] are clamped to it, and
    with decreasing ones the rows of Y are unspecified, but nothing outside the
-   arrays is read or written. 1 <= E <= 8192; with row_index T*K < 2^32. R = 0
-   or N = 0 is a no-op. No workspace and no host synchronisation: the call can be
+   arrays is read or written. 1 <= E <= 8192; with row_index T*K < 2^32, and T >= 1
+   where R is. R = 0 or N = 0 is a no-op. No workspace and no host synchronisation: the call can be
    captured in a HIP graph and replayed with other offsets. */
 ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int64_t K,
                               const uint8_t* Wq, const float* ws, int64_t E, int64_t N,
