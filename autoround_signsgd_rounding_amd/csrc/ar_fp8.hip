@@ -54,8 +54,7 @@ __device__ __forceinline__ float scale_of(float amax) {
 // 1/s in two floats, the first never above it: x·hi + x·lo is x/s to 2^-46 before it is
 // rounded, where x·hi alone is off by up to 1.5 units in the last place and sends a
 // quotient halfway between two codes to the wrong one. With lo >= 0 a zero keeps
-// its sign. Of an infinite scale finite values become 0, an infinity NaN. (A
-// second product per value: 16384 x 4096 bf16 activations 33.6 us, one product 32.7.)
+// its sign. Of an infinite scale finite values become 0, an infinity NaN.
 struct Inverse {
   float hi, lo;
 };
@@ -96,7 +95,7 @@ __device__ __forceinline__ void store_row(float* p, const float (&v)[CH]) {
 // |g|·2^-24. As it stands that is good for |g| <= 64, which a wave's gates
 // hardly ever leave together; with FAR, for every gate: where 2^hi would leave float32's
 // range (and the sigmoid, of which a large u may still make a normal number), it is taken
-// 2^160 lower, and u as mantissa and exponent. 2048 x 11008 bf16 takes 23.7 us.
+// 2^160 lower, and u as mantissa and exponent. 2048 x 11008 bf16 takes 20.9 us.
 template <bool FAR>
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float L = -1.44269502f, LREST = -1.92596299e-8f, LN2 = 0.69314718f;   // L + LREST: -log2 e
@@ -127,11 +126,31 @@ __device__ __forceinline__ void silu_mul(float (&g)[CH], const float (&u)[CH]) {
   }
 }
 
+// Eight values of T as they lie in memory.
+template <class T>
+struct RowOf {
+  u32x4_t raw[sizeof(T) / 2] = {};
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = reinterpret_cast<const u32x4_t*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float (&o)[CH]) const {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if constexpr (sizeof(T) == 4)
+        o[i] = __uint_as_float(raw[i / 4][i % 4]);
+      else
+        o[i] = __uint_as_float(i % 2 ? raw[0][i / 2] & 0xFFFF0000u : raw[0][i / 2] << 16);
+    }
+  }
+};
+
 // ------------------------------------------------------------------ activations
 // Units of one block of one row, 16 lanes each. A workgroup takes RT rows by BT
 // blocks of them, row by row, a wave four units (1 KiB of bf16) at a time and
 // ITERS times; the scales leave through LDS, the RT rows of a block side by
-// side. ITERS = 1 spreads small inputs over more CUs: 16 x 11008, gated, takes 2.9 us
+// side. Values wait as they were loaded (62 registers at bf16, gated, where as floats they take
+// 86 and five waves fit a SIMD instead of eight: 2048 x 11008 20.9 us instead of 23.7). ITERS = 1 spreads small inputs over more CUs: 16 x 11008, gated, takes 2.9 us
 // instead of 6.5 at 32 rows a workgroup.
 template <class T, bool GATE, int ITERS>
 __global__ __launch_bounds__(NT) void k_fp8_quant_act(const T* X, int64_t M, int64_t K, uint8_t* q,
@@ -142,26 +161,30 @@ __global__ __launch_bounds__(NT) void k_fp8_quant_act(const T* X, int64_t M, int
   const int mt = blockIdx.x / chunks;   // consecutive workgroups share rows
   const int64_t j0 = (int64_t)(blockIdx.x - mt * chunks) * BT, m0 = (int64_t)mt * RT;
   const int c = threadIdx.x % LPB * CH;
-  float v[ITERS][CH], u[ITERS][CH];
+  RowOf<T> v[ITERS], u[ITERS];
   int64_t at[ITERS];   // offset of the lane's values in q, -1: none
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const int unit = i * (NT / LPB) + threadIdx.x / LPB, r = unit / BT;
     const int64_t m = m0 + r, k = (j0 + unit - r * BT) * BLK + c;
-#pragma unroll
-    for (int e = 0; e < CH; ++e) v[i][e] = u[i][e] = 0.0f;
     at[i] = -1;
     if (r < RT && m < M && k < K) {   // K % 16 == 0: the 8 values are in or out
       at[i] = m * K + k;
-      load8(X + m * K * (GATE ? 2 : 1) + k, v[i]);
-      if constexpr (GATE) load8(X + (2 * m + 1) * K + k, u[i]);
+      v[i].load(X + m * K * (GATE ? 2 : 1) + k);
+      if constexpr (GATE) u[i].load(X + (2 * m + 1) * K + k);
     }
   }
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    if constexpr (GATE) silu_mul(v[i], u[i]);
-    const float s = scale_of(amax_row(v[i]));
-    if (at[i] >= 0) store_codes(q + at[i], v[i], s);
+    float x[CH];
+    v[i].get(x);
+    if constexpr (GATE) {
+      float up[CH];
+      u[i].get(up);
+      silu_mul(x, up);
+    }
+    const float s = scale_of(amax_row(x));
+    if (at[i] >= 0) store_codes(q + at[i], x, s);
     if (threadIdx.x % LPB == 0) sc[i * (NT / LPB) + threadIdx.x / LPB] = s;
   }
   __syncthreads();
@@ -224,25 +247,6 @@ __device__ __forceinline__ void norm_input(const T* x, const T* res, int64_t o, 
     }
   }
 }
-
-// Eight values of T as they lie in memory.
-template <class T>
-struct RowOf {
-  u32x4_t raw[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = reinterpret_cast<const u32x4_t*>(p)[i];
-  }
-  __device__ __forceinline__ void get(float (&o)[CH]) const {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if constexpr (sizeof(T) == 4)
-        o[i] = __uint_as_float(raw[i / 4][i % 4]);
-      else
-        o[i] = __uint_as_float(i % 2 ? raw[0][i / 2] & 0xFFFF0000u : raw[0][i / 2] << 16);
-    }
-  }
-};
 
 struct NormArgs {
   const void *x, *res, *w;
