@@ -737,7 +737,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
           if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
           else *d = v;   // runs that end inside a line are joined in L2
           if constexpr (sizeof(V) < 4) {
-            seen.take<true>(v * 0x10001u);
+            seen.take<false>((uint32_t)v << 16);   // (a bf16's bits, as a float32's)
           } else {
 #pragma unroll
             for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
