@@ -149,8 +149,9 @@ struct RowOf {
 // Units of one block of one row, 16 lanes each. A workgroup takes RT rows by BT
 // blocks of them, row by row, a wave four units (1 KiB of bf16) at a time and
 // ITERS times; the scales leave through LDS, the RT rows of a block side by
-// side. Values wait as they were loaded (62 registers at bf16, gated, where as floats they take
-// 86 and five waves fit a SIMD instead of eight: 2048 x 11008 20.9 us instead of 23.7). ITERS = 1 spreads small inputs over more CUs: 16 x 11008, gated, takes 2.9 us
+// side. Values wait as they were loaded: 62 registers at bf16, gated, where as floats
+// they take 86 and five waves fit a SIMD instead of eight (2048 x 11008: 20.9 us instead
+// of 23.7). ITERS = 1 spreads small inputs over more CUs: 16 x 11008, gated, takes 2.9 us
 // instead of 6.5 at 32 rows a workgroup.
 template <class T, bool GATE, int ITERS>
 __global__ __launch_bounds__(NT) void k_fp8_quant_act(const T* X, int64_t M, int64_t K, uint8_t* q,

@@ -15,20 +15,20 @@
 // summed over, so any will do).
 //
 // Two kernels: k_fp8_rows for few rows, where W's bytes are the cost, and k_fp8_tile
-// for the rest; ar_fp8_plan.h chooses. What bounds them, with a large copy at 4.8 TB/s
-// and a library e4m3 product with one scale per operand at 2.41 PFLOP/s
-// (16384 x 4096 x 4096) on the same card:
-//   rows, 1 x 29568 x 8192            43.9 us, 5.5 TB/s: memory
-//   32x64 tiles, 16 x 29568 x 8192    46 us, 5.3 TB/s: memory
-//   64x128 tiles, 24 tokens, 4 of 64 experts, 2048 x 2048: 22.7 us, 5.3 TB/s: memory
-//   256x256 tiles, 16384 x 4096 x 4096    237 us, 2.32 PFLOP/s; 8192^3 443 us, 2.49
-//   the same by expert, 8192 tokens, 2 of 8, 11008 x 4096: 746 us, 1.98 PFLOP/s
-//   128x128 tiles, float32 Y, 16384 x 4096 x 4096: 473 us, 1.16 PFLOP/s
-// The 256x256 tile keeps the matrix unit busy 53% of the time at 2.18 GHz. Of its
-// 242 us the loop's loads cost 48 (timed without them), the scale fmas 22 and Y's
-// stores 35: all CUs end their tiles at about the same time, and a round of tiles
-// is 33 MB of Y. The float32 form converts every code a wave reads; its matrix
-// work alone would take 250 us.
+// for the rest; ar_fp8_plan.h chooses. What bounds them, in a stream of calls on two
+// inputs in turn, with a large copy at 4.85 TB/s and a library e4m3 product with one scale
+// per operand at 2.41 PFLOP/s (16384 x 4096 x 4096) on the same card:
+//   rows, 1 x 29568 x 8192            44 us, 5.5 TB/s: memory
+//   32x64 tiles, 16 x 29568 x 8192    47 us, 5.1 TB/s: memory
+//   64x128 tiles, 24 tokens, 4 of 64 experts (about 30 used), 2048 x 2048: 28 us, 4.5 TB/s: memory
+//   256x256 tiles, 16384 x 4096 x 4096    232 us, 2.37 PFLOP/s; 8192^3 438 us, 2.51
+//   the same by expert, 8192 tokens, 2 of 8, 11008 x 4096: 730 us, 2.02 PFLOP/s
+//   128x128 tiles, float32 Y, 16384 x 4096 x 4096: 475 us, 1.16 PFLOP/s
+// The 256x256 tile keeps the matrix unit busy 56% of the time at 1.85 GHz. On random codes, where
+// it takes 265 us, it takes 220 without the loop's loads, 242 without the scale fmas
+// and 247 without Y's stores: all CUs end their tiles at about the same time, and a
+// round of tiles is 33 MB of Y. The float32 form converts every code a wave reads; its
+// matrix work alone would take 250 us.
 #include <type_traits>
 
 #include "ar_device.h"
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(64 * DW) void k_fp8_rows(Args a) {
 // H run, the stage just left is filled for NS steps ahead and the next step's
 // fragments are read, each X fragment as the old one is done with. H = 3 spreads
 // these reads, half of all, over more products, where registers allow it and a
-// step is long: 256x256 tiles, 46.6 -> 45.4 us at 512 x 4096 x 4096, 457 -> 448 at 8192^3;
+// step is long: 256x256 tiles, 234 -> 231 us at 16384 x 4096 x 4096;
 // 64x128 tiles are 2% slower with it.
 //
 // With KG > 1 a workgroup has KG such sets of waves and stages, each on its own
@@ -434,9 +434,9 @@ constexpr uint32_t kNone = 0xFFFFFFF0u;   // past every buffer: the load writes 
 // neighbours, which share operands in its L2, and all XCDs stay near one place
 // of the sequence, so that what they stream (an expert's W above all) is in the
 // last-level cache when the second one asks. Measured on 8192 tokens, 2 of 8
-// experts, 11008 x 4096: 746 us against 789 with an eighth of the whole sequence
+// experts, 11008 x 4096: 722 us against 768 with an eighth of the whole sequence
 // per XCD. With one tile row nothing is read twice, and an eighth of W each is
-// faster: 16 x 29568 x 8192, 44 us against 51.
+// faster: 16 x 29568 x 8192, 46 us against 51.
 __device__ __forceinline__ void tile_of(int w, int n, int tilesM, int tilesN, int& tm, int& tn) {
   constexpr int GI = 4, WINDOW = 256;
   const int base = tilesM == 1 ? 0 : w & ~(WINDOW - 1);
@@ -669,9 +669,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
   // The wave's part of Y goes through LDS (the stages are free once everyone is
   // here) so that rows leave as whole runs of 128 or 256 bytes, past the caches:
   // the tiles of all CUs end at about the same time. Measured at 16384 x 4096 x
-  // 4096 against storing from the accumulators: 253 us instead of 267. Rows of Y
+  // 4096 against storing from the accumulators: 253 us instead of 267 (and through the
+  // caches 239 instead of 232). Rows of Y
   // that are not 16-byte aligned leave in smaller units and through the caches
-  // (12468 x 4831 x 256 on 256x256 tiles: 63 us, past them 78).
+  // (12468 x 4831 x 256 on 256x256 tiles: 64 us, past them 78).
   __syncthreads();
   if constexpr (KG > 1) {
     static_assert((KG - 1) * C::TM * C::TN * 4 <= C::LDS, "the other sets' sums in LDS");

@@ -19,20 +19,22 @@ struct ArFp8Shape {
 // measured; 12% less with two sets) and from the caches into LDS (14 TB/s; 12
 // where rows of K bytes break the 64-byte sectors) bound the time from below.
 // Measured (us), M x N x K, the rule's pick first:
-//   16 x 4096 x 4096            rows              6.5   32x64, two sets 8.8
-//   16 x 11008 x 4096           32x64, two sets  10.4   rows 13.9, 64x64 two sets 11.7
-//   64 x 11008 x 4096           64x64, two sets  12.3   one set 13.4, 32x64 14.7
-//   512 x 4096 x 4096           64x128, two sets 15.1   one set 17.5, 128x128 20.6
-//   1024 x 4096 x 4096          128x128, two     22.7   one set 25.4, 64x128 24.7
-//   2048 x 4096 x 4096          128x128          36.1   64x128 46.2, 256x256 50.0
-//   3806 x 2584 x 8656          256x256         118     128x128 139
-//   4096 x 4096 x 4096          256x256          59.8   128x128 69.8
-//   24 tokens, 4 of 64 experts, 2048 x 2048: 64x128 22.7, 32x64 25.2, rows 37.0
-//   333 x 4096 x 4096, float32  64x128, two sets 23.4   one set 28.2, 128x128 33.1
-// Over 78 shapes, dense and by expert, the pick takes 1.04 times the best one's
-// time in the mean, and 1.3 times it at the most. The float32 form runs at half
-// the matrix rate and on more registers: it has its own times, and no 256 x 256
-// tile.
+//   16 x 4096 x 4096            rows                6.2   32x64, two sets 8.7, 32x64 10.6
+//   16 x 11008 x 4096           32x64, two sets    10.3   32x64 10.9, 64x64, two sets 11.5
+//   64 x 11008 x 4096           64x64, two sets    12.0   64x64 13.2, 32x64 14.4
+//   512 x 4096 x 4096           64x128, two sets   15.2   64x128 17.2, 64x64 18.1
+//   1024 x 4096 x 4096          128x128, two sets  22.4   64x128 24.3, 128x128 24.8
+//   2048 x 4096 x 4096          128x128            37.2   128x128, two sets 43.9, 256x256 46.7
+//   3806 x 2584 x 8656          256x256             111   128x128 137, 64x128 153
+//   4096 x 4096 x 4096          256x256            58.9   128x128 75.2, 128x128, two sets 88.1
+//   24 tokens, 4 of 64 experts, 2048 x 2048: 64x128 21.2; 32x64 23.2, 128x128 23.4
+//   333 x 4096 x 4096, float32  64x128, two sets   22.1   64x64 24.7, 64x128 26.1
+// Over 106 shapes, dense and by expert, with even and with very uneven routing, the
+// pick takes 1.03 times the best one's time in the mean, and 1.53 times it at the most
+// (50 rows of 100 experts, 500 x 800: 11.3 us by rows, 7.4 by 32x64 tiles). The rule
+// knows how many experts and rows there are, not how the rows are spread. The float32
+// form runs at half the matrix rate and on more registers: it has its own times, and
+// no 256 x 256 tile.
 enum ArFp8Kind { kRows, k32x64, k64x64, k64x128, k128x128, k256x256, kKinds };
 struct ArFp8Times {
   int tm, tn;
