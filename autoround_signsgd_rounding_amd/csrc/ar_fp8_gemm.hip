@@ -464,7 +464,7 @@ __device__ __forceinline__ int count_tiles(const Args& a) {
   return __builtin_amdgcn_readfirstlane(n);
 }
 
-template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
+template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE, class O>   // O: Y's type
 __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int mostM, int tilesN) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
   typedef FragOf<WIDE> Op;
@@ -705,59 +705,53 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
     }
   }
   Seen seen;
-  auto leave = [&](auto zero) {      // Y's rows as its type O
-    typedef decltype(zero) O;
-    constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
-    static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
-    uint8_t* own = lds + wave * (MB * 16 * RB);
-    auto at = [&](int r, int byte) {   // 16-byte chunks spread over the banks by row
-      return own + r * RB + (byte ^ ((r & (RB / 16 - 1)) * 16));
-    };
+  constexpr int RB = NA * 16 * (int)sizeof(O);             // bytes of a row of the part
+  static_assert(C::NW * MB * 16 * RB <= C::LDS, "the tile of Y in LDS");
+  uint8_t* own = lds + wave * (MB * 16 * RB);
+  auto at = [&](int r, int byte) {   // 16-byte chunks spread over the banks by row
+    return own + r * RB + (byte ^ ((r & (RB / 16 - 1)) * 16));
+  };
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int t = 0; t < NA; ++t) {
-        const f32x4_t v = acc[t][b];
-        uint8_t* d = at(16 * b + l16, (16 * t + 4 * q) * (int)sizeof(O));
-        if constexpr (sizeof(O) == 2)
-          *reinterpret_cast<u32x2_t*>(d) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-        else
-          *reinterpret_cast<f32x4_t*>(d) = v;
-      }
-    O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
-    const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
-    auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
-      typedef decltype(unit) V;
-      constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
+    for (int t = 0; t < NA; ++t) {
+      const f32x4_t v = acc[t][b];
+      uint8_t* d = at(16 * b + l16, (16 * t + 4 * q) * (int)sizeof(O));
+      if constexpr (sizeof(O) == 2)
+        *reinterpret_cast<u32x2_t*>(d) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      else
+        *reinterpret_cast<f32x4_t*>(d) = v;
+    }
+  O* Y = static_cast<O*>(a.Y) + (r0 + wm * MB * 16) * a.N + n0 + wn * NA * 16;
+  const int nleft = (int)(a.N - n0) - wn * NA * 16, mleft = rows - wm * MB * 16;
+  auto write = [&](auto unit) {      // rows in pieces of one unit, whole or absent
+    typedef decltype(unit) V;
+    constexpr int PER = sizeof(V) / sizeof(O), UPR = RB / (int)sizeof(V);
 #pragma unroll 8
-      for (int i = lane; i < MB * 16 * UPR; i += 64) {
-        const int r = i / UPR, u = i % UPR;
-        if (r < mleft && u * PER < nleft) {
-          const V v = *reinterpret_cast<const V*>(at(r, u * (int)sizeof(V)));
-          V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
-          if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
-          else *d = v;   // runs that end inside a line are joined in L2
-          if constexpr (sizeof(V) < 4) {
-            seen.take<false>((uint32_t)v << 16);   // (a bf16's bits, as a float32's)
-          } else {
+    for (int i = lane; i < MB * 16 * UPR; i += 64) {
+      const int r = i / UPR, u = i % UPR;
+      if (r < mleft && u * PER < nleft) {
+        const V v = *reinterpret_cast<const V*>(at(r, u * (int)sizeof(V)));
+        V* d = reinterpret_cast<V*>(Y + (int64_t)r * a.N) + u;
+        if constexpr (sizeof(V) == 16) __builtin_nontemporal_store(v, d);
+        else *d = v;   // runs that end inside a line are joined in L2
+        if constexpr (sizeof(V) < 4) {
+          seen.take<false>((uint32_t)v << 16);   // (a bf16's bits, as a float32's)
+        } else {
 #pragma unroll
-            for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
-              if constexpr (sizeof(V) == 4) seen.take<sizeof(O) == 2>(v);
-              else seen.take<sizeof(O) == 2>(v[w]);
-            }
+          for (int w = 0; w < (int)sizeof(V) / 4; ++w) {
+            if constexpr (sizeof(V) == 4) seen.take<sizeof(O) == 2>(v);
+            else seen.take<sizeof(O) == 2>(v[w]);
           }
         }
       }
-    };
-    const int64_t pitch = a.N * (int64_t)sizeof(O);
-    if (pitch % 16 == 0) write(u32x4_t{});
-    else if (pitch % 8 == 0) write(u32x2_t{});
-    else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
-    else write(uint16_t{});
+    }
   };
-  if constexpr (!WIDE) leave(uint16_t{});
-  else if (a.ydt == AR_BF16) leave(uint16_t{});
-  else leave(0.0f);
+  const int64_t pitch = a.N * (int64_t)sizeof(O);
+  if (pitch % 16 == 0) write(u32x4_t{});
+  else if (pitch % 8 == 0) write(u32x2_t{});
+  else if (sizeof(O) == 4 || pitch % 4 == 0) write(uint32_t{});
+  else write(uint16_t{});
   if (seen.odd() && far_scales(a, r0, wm * MB * 16, MB, rows, wsp))
     sum_again<WIDE>(a, e, r0, wm * MB * 16, MB, rows, n0 + wn * NA * 16, NA, wsp, KG, steps, 1,
                     steps);
@@ -765,13 +759,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
 
 }  // namespace
 
-template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE>
+template <int WM, int WN, int MB, int NA, int NS, int KG, bool WIDE, class O>
 static ar_status tile_launch(const Args& a, const ArFp8Shape& g, hipStream_t st) {
   typedef Tile<WM, WN, MB, NA, NS, KG> C;
   const int64_t tilesM = ar_fp8_most_tiles(g, C::TM);
   const int64_t tilesN = (a.N + C::TN - 1) / C::TN;
   if (tilesM * tilesN * C::THREADS >= (int64_t(1) << 32)) return AR_ERR_SHAPE;   // HIP's limit
-  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE>), dim3((unsigned)(tilesM * tilesN)),
+  hipLaunchKernelGGL((k_fp8_tile<WM, WN, MB, NA, NS, KG, WIDE, O>), dim3((unsigned)(tilesM * tilesN)),
                      dim3(C::THREADS), 0, st, a, (int)tilesM, (int)tilesN);
   return last_status();
 }
@@ -785,13 +779,15 @@ static ar_status rows_launch(const Args& a, const ArFp8Shape& g, hipStream_t st)
   return last_status();
 }
 
-template <int WM, int WN, int MB, int NA, int NS1, int NS2>
+template <int WM, int WN, int MB, int NA, int NS, int KG>
+static ar_status tile_sums(const Args& a, const ArFp8Shape& g, hipStream_t st) {
+  if (!g.wide) return tile_launch<WM, WN, MB, NA, NS, KG, false, uint16_t>(a, g, st);
+  return a.ydt == AR_BF16 ? tile_launch<WM, WN, MB, NA, NS, KG, true, uint16_t>(a, g, st)
+                          : tile_launch<WM, WN, MB, NA, NS, KG, true, float>(a, g, st);
+}
+template <int WM, int WN, int MB, int NA, int NS>
 static ar_status tile_pick(const Args& a, const ArFp8Shape& g, bool two, hipStream_t st) {
-  if (g.wide)
-    return two ? tile_launch<WM, WN, MB, NA, NS2, 2, true>(a, g, st)
-               : tile_launch<WM, WN, MB, NA, NS1, 1, true>(a, g, st);
-  return two ? tile_launch<WM, WN, MB, NA, NS2, 2, false>(a, g, st)
-             : tile_launch<WM, WN, MB, NA, NS1, 1, false>(a, g, st);
+  return two ? tile_sums<WM, WN, MB, NA, NS, 2>(a, g, st) : tile_sums<WM, WN, MB, NA, NS, 1>(a, g, st);
 }
 
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
@@ -801,10 +797,10 @@ ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
   const ArFp8Plan p = ar_fp8_plan(shape);
   switch (p.kind) {
     case kRows: return rows_launch(a, shape, st);
-    case k32x64: return tile_pick<2, 2, 1, 2, 4, 4>(a, shape, p.two, st);
-    case k64x64: return tile_pick<2, 2, 2, 2, 4, 4>(a, shape, p.two, st);
-    case k64x128: return tile_pick<2, 2, 2, 4, 3, 3>(a, shape, p.two, st);
-    case k128x128: return tile_pick<2, 2, 4, 4, 2, 2>(a, shape, p.two, st);
-    default: return tile_launch<4, 2, 4, 8, 2, 1, false>(a, shape, st);
+    case k32x64: return tile_pick<2, 2, 1, 2, 4>(a, shape, p.two, st);
+    case k64x64: return tile_pick<2, 2, 2, 2, 4>(a, shape, p.two, st);
+    case k64x128: return tile_pick<2, 2, 2, 4, 3>(a, shape, p.two, st);
+    case k128x128: return tile_pick<2, 2, 4, 4, 2>(a, shape, p.two, st);
+    default: return tile_launch<4, 2, 4, 8, 2, 1, false, uint16_t>(a, shape, st);
   }
 }
