@@ -98,7 +98,8 @@ __device__ __forceinline__ void store_row(float* p, const float (&v)[CH]) {
 // 2^160 lower, and u as mantissa and exponent. 2048 x 11008 bf16 takes 20.9 us.
 template <bool FAR>
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  constexpr float L = -1.44269502f, LREST = -1.92596299e-8f, LN2 = 0.69314718f;   // L + LREST: -log2 e
+  constexpr float L = -1.44269502f, LREST = -1.92596299e-8f;   // their sum is -log2 e
+  constexpr float LN2 = 0.69314718f;
   const float x = FAR ? __builtin_amdgcn_fmed3f(g, -300.0f, 300.0f) : g;
   const float hi = x * L, lo = fmaf(x, LREST, fmaf(x, L, -hi)) * LN2;
   if constexpr (!FAR) {

@@ -20,7 +20,7 @@
 // per operand at 2.41 PFLOP/s (16384 x 4096 x 4096) on the same card:
 //   rows, 1 x 29568 x 8192            44 us, 5.5 TB/s: memory
 //   32x64 tiles, 16 x 29568 x 8192    47 us, 5.1 TB/s: memory
-//   64x128 tiles, 24 tokens, 4 of 64 experts (about 30 used), 2048 x 2048: 28 us, 4.5 TB/s: memory
+//   64x128 tiles, 24 tokens, 4 of 64 experts (30 used), 2048 x 2048: 28 us, 4.5 TB/s: memory
 //   256x256 tiles, 16384 x 4096 x 4096    232 us, 2.37 PFLOP/s; 8192^3 438 us, 2.51
 //   the same by expert, 8192 tokens, 2 of 8, 11008 x 4096: 730 us, 2.02 PFLOP/s
 //   128x128 tiles, float32 Y, 16384 x 4096 x 4096: 475 us, 1.16 PFLOP/s
@@ -220,7 +220,8 @@ struct Seen {
     }
   }
   __device__ __forceinline__ bool odd() const {
-    return __any(f32 >= 0xFF000000u - 2u * 0x17800000u || max(bf16[0], bf16[1]) >= 0xFF00 - 2 * 0x1780);
+    return __any(f32 >= 0xFF000000u - 2u * 0x17800000u ||
+                 max(bf16[0], bf16[1]) >= 0xFF00 - 2 * 0x1780);
   }
 };
 
@@ -669,10 +670,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void k_fp8_tile(Args a, int m
   // The wave's part of Y goes through LDS (the stages are free once everyone is
   // here) so that rows leave as whole runs of 128 or 256 bytes, past the caches:
   // the tiles of all CUs end at about the same time. Measured at 16384 x 4096 x
-  // 4096 against storing from the accumulators: 253 us instead of 267 (and through the
-  // caches 239 instead of 232). Rows of Y
-  // that are not 16-byte aligned leave in smaller units and through the caches
-  // (12468 x 4831 x 256 on 256x256 tiles: 64 us, past them 78).
+  // 4096: 253 us instead of 267 from the accumulators, and 232 instead of 239 through the
+  // caches. Rows of Y that are not 16-byte aligned leave in smaller units and through
+  // the caches (12468 x 4831 x 256 on 256x256 tiles: 64 us, past them 78).
   __syncthreads();
   if constexpr (KG > 1) {
     static_assert((KG - 1) * C::TM * C::TN * 4 <= C::LDS, "the other sets' sums in LDS");
@@ -787,7 +787,8 @@ static ar_status tile_sums(const Args& a, const ArFp8Shape& g, hipStream_t st) {
 }
 template <int WM, int WN, int MB, int NA, int NS>
 static ar_status tile_pick(const Args& a, const ArFp8Shape& g, bool two, hipStream_t st) {
-  return two ? tile_sums<WM, WN, MB, NA, NS, 2>(a, g, st) : tile_sums<WM, WN, MB, NA, NS, 1>(a, g, st);
+  return two ? tile_sums<WM, WN, MB, NA, NS, 2>(a, g, st)
+             : tile_sums<WM, WN, MB, NA, NS, 1>(a, g, st);
 }
 
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st) {
