@@ -9,7 +9,7 @@ A cache is a pair: codes uint8 [pages, 2, heads, page, dim/2] (keys, values) and
 [pages, 2, heads, page, groups]. A group of `dim/groups` channels has one scale whose four lowest
 mantissa bits are its zero-point; a value is scale·(code - zero-point). Two codes share a byte, the
 even channel in its low half. The bytes of a key lie in order. Those of the values lie in octets of
-tokens: byte 16·b + n of token t is at [t/8][n][t%8][b].
+tokens: byte 32·b + 16·c + n of token t is at [t/8][b][n][t%8][c].
 
 `own` selects the package's entry points instead of the plain forms.
 """
@@ -234,9 +234,9 @@ def _grid(x, groups):
 
 
 def _values_view(codes):
-    """The value codes as [pages, heads, octet, n, token, b]."""
+    """The value codes as [pages, heads, octet, b, n, token, c]."""
     pages, _, H, P, half = codes.shape
-    return codes[:, 1].view(pages, H, P // 8, 16, 8, half // 16)
+    return codes[:, 1].view(pages, H, P // 8, half // 32, 16, 8, 2)
 
 
 def _write(x, cache, slots, which):
@@ -253,7 +253,8 @@ def _write(x, cache, slots, which):
         codes[page, 0, :, at] = code
     else:
         T, H, half = code.shape
-        _values_view(codes)[page, :, at // 8, :, at % 8] = code.view(T, H, half // 16, 16).transpose(2, 3)
+        code = code.view(T, H, half // 32, 2, 16).transpose(3, 4)
+        _values_view(codes)[page, :, at // 8, :, :, at % 8] = code
 
 
 def _numbers(code, scale):
@@ -269,7 +270,7 @@ def _read(cache, slots, dtype):
     P = codes.shape[3]
     at = slots.clamp(min=0).long()
     page, at, live = at // P, at % P, (slots >= 0)[:, None, None]
-    v = _values_view(codes)[page, :, at // 8, :, at % 8].transpose(2, 3).flatten(-2)
+    v = _values_view(codes)[page, :, at // 8, :, :, at % 8].transpose(3, 4).flatten(-3)
     k = _numbers(codes[page, 0, :, at], scale[page, 0, :, at])
     v = _numbers(v, scale[page, 1, :, at])
     return (k * live).to(dtype), (v * live).to(dtype)
@@ -279,7 +280,7 @@ def _decode(q, cache, table, lengths):
     codes, scale = cache
     (B, new, H, D), (pages, _, Hk, P, half) = q.shape, codes.shape
     r, L, at = H // Hk, table.shape[1] * P, table.clamp(min=0).long()
-    v = _values_view(codes)[at].permute(0, 2, 1, 3, 5, 6, 4).reshape(B, Hk, L, half)
+    v = _values_view(codes)[at].permute(0, 2, 1, 3, 6, 4, 7, 5).reshape(B, Hk, L, half)
     k = codes[:, 0][at].permute(0, 2, 1, 3, 4).reshape(B, Hk, L, half)
     s = scale[at].permute(0, 2, 3, 1, 4, 5).reshape(B, 2, Hk, L, -1)
     k = _numbers(k, s[:, 0]).view(B * Hk, L, D).transpose(1, 2).contiguous()
@@ -390,8 +391,8 @@ def _cached(cache, pages, which, head):
         if which == 0:
             at = t * (D // 2) + c // 2
         else:
-            b, n = c // 2 // 16, c // 2 % 16
-            at = ((t // 8 * 16 + n) * 8 + t % 8) * (D // 32) + b
+            b, c2, n = c // 64, c // 32 % 2, c // 2 % 16
+            at = (((t // 8 * (D // 64) + b) * 16 + n) * 8 + t % 8) * 2 + c2
         code = flat[:, at].reshape(-1) // (16 if c % 2 else 1) % 16
         x[:, c] = s[:, c * G // D].double() * (code - zp[:, c * G // D])
     return x
