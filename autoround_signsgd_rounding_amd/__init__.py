@@ -32,7 +32,8 @@ EXPORTS = (
     "ar_dequant_gemm_workspace_size", "ar_dequant_gemm", "ar_block_workspace_size",
     "ar_block_forward", "ar_tune_block", "ar_attention", "ar_tune_step_noalloc",
     "ar_fp8_quant_act", "ar_fp8_quant_weight", "ar_rmsnorm_fp8", "ar_fp8_gemm",
-    "ar_fp8_gemm_grouped",
+    "ar_fp8_gemm_grouped", "ar_attention_packed_workspace_size", "ar_attention_packed",
+    "ar_kv4_write", "ar_kv4_read", "ar_kv4_attention_workspace_size", "ar_kv4_attention",
 )
 
 # input channels per scale of the e4m3 operands
@@ -103,6 +104,13 @@ class ArBlockOutputs(ctypes.Structure):
                 ("out_q", ctypes.c_void_p)]
 
 
+class ArKv4Cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("group_size", ctypes.c_int32)]
+
+
 BLOCK_LINEARS = ("q_proj", "k_proj", "v_proj", "o_proj", "gate_proj", "up_proj", "down_proj")
 
 
@@ -113,7 +121,7 @@ def _load():
             "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    cfgp = ctypes.POINTER(ArConfig)
+    cfgp, kvp, fl = ctypes.POINTER(ArConfig), ctypes.POINTER(ArKv4Cache), ctypes.c_float
     sig = {
         "ar_config_default": [cfgp],
         "ar_workspace_size": [cfgp, i64, i64, i32, ctypes.POINTER(sz)],
@@ -153,6 +161,14 @@ def _load():
         "ar_rmsnorm_fp8": [i32, vp, vp, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp],
         "ar_fp8_gemm": [vp, vp, i64, i64, vp, vp, i64, vp, i32, vp],
         "ar_fp8_gemm_grouped": [vp, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i32, vp],
+        "ar_attention_packed_workspace_size": [i64] * 6 + [ctypes.POINTER(sz)],
+        "ar_attention_packed": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64,
+                                fl, vp, vp, vp, sz, vp],
+        "ar_kv4_write": [kvp, i32, vp, i64, vp, i64, vp, i64, vp],
+        "ar_kv4_read": [kvp, vp, i64, i32, vp, vp, vp],
+        "ar_kv4_attention_workspace_size": [kvp, i64, i64, i64, i64, ctypes.POINTER(sz)],
+        "ar_kv4_attention": [kvp, vp, i64, i64, i64, i64, vp, i64, vp, i64, fl, vp, vp, vp, sz,
+                             vp],
         "ar_pack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
         "ar_unpack": [i32, vp, vp, i64, i64, i64, vp, vp, vp],
     }
@@ -782,6 +798,255 @@ def fp8_gemm_grouped(Xq, xs, Wq, ws, offsets, *, row_index=None, out_dtype=None,
     if st:
         _check(st, "ar_fp8_gemm_grouped")
     return out
+
+
+# ------------------------------------------------------------------ attention, 4-bit cache
+class AttentionOutput(NamedTuple):
+    out: object      # as q, bf16
+    lse: object      # [..., heads] float32, or None
+
+
+class KV4Cache(NamedTuple):
+    """A 4-bit key/value cache of one layer; any (codes, scale) pair of these shapes will do."""
+    codes: object    # [pages, 2, heads, page_size, head_dim/2] uint8
+    scale: object    # [pages, 2, heads, page_size, head_dim/group_size] float32
+
+
+def kv4_cache(pages: int, heads: int, head_dim: int, *, page_size: int = 64,
+              group_size: int = -1, device=None) -> KV4Cache:
+    """A cache of zeros for `heads` key heads (ar_kv4_cache): pages of 16, 32, 64, 128 or
+    256 tokens, one scale per 32, 64 or 128 channels of a token's head (-1: per head)."""
+    torch = _torch()
+    if group_size == -1:
+        group_size = head_dim
+    if head_dim not in (64, 128) or group_size not in (32, 64, 128) or group_size > head_dim:
+        raise ValueError("head_dim must be 64 or 128, group_size 32, 64 or 128 and no larger")
+    if page_size not in (16, 32, 64, 128, 256):
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256")
+    if pages < 1 or heads < 1:
+        raise ValueError("pages and heads must be positive")
+    device = torch.device("cuda") if device is None else device
+    lead = (pages, 2, heads, page_size)
+    return KV4Cache(torch.zeros((*lead, head_dim // 2), dtype=torch.uint8, device=device),
+                    torch.zeros((*lead, head_dim // group_size), device=device))
+
+
+def _kv4(cache):
+    """(ArKv4Cache, device index) of a checked (codes, scale) pair."""
+    torch = _torch()
+    if cache is None or len(cache) != 2 or cache[0] is None or cache[1] is None:
+        raise ValueError("cache must be a (codes, scale) pair")
+    codes, scale = cache
+    if codes.dim() != 5 or scale.dim() != 5:
+        raise ValueError("codes must be [pages, 2, heads, page_size, head_dim/2], scale "
+                         "[pages, 2, heads, page_size, head_dim/group_size]")
+    pages, two, heads, page, half = codes.shape
+    groups, dev = scale.shape[4], codes.get_device()
+    if not (dev >= 0 and two == 2 and scale.shape[:4] == codes.shape[:4] and groups > 0 and
+            2 * half % groups == 0 and codes.dtype is torch.uint8 and
+            scale.dtype is torch.float32 and scale.get_device() == dev and
+            codes.is_contiguous() and scale.is_contiguous()):
+        lead = (pages, 2, heads, page)
+        _need(codes, "codes", (*lead, half), torch.uint8)
+        _need(scale, "scale", (*lead, groups), torch.float32)
+        raise ValueError(f"codes {list(codes.shape)} on {codes.device} and scale "
+                         f"{list(scale.shape)} on {scale.device} do not belong together")
+    return ArKv4Cache(codes.data_ptr(), scale.data_ptr(), pages, heads, 2 * half, page,
+                      2 * half // groups), dev
+
+
+def _tokens(t, name, heads, dim, dtypes, dev):
+    """Stride between the tokens of t [tokens, heads, dim], whose tokens may lie apart."""
+    if t is None or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+            t.dtype not in dtypes:
+        want = "/".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{name} must be {want} [tokens, {heads}, {dim}], got " +
+                         ("None" if t is None else f"{t.dtype} {list(t.shape)}"))
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on the other tensors' GPU, got {t.device}")
+    apart, head, one = t.stride()
+    if t.shape[0] <= 1:     # (torch leaves the stride of such a dimension open)
+        apart = heads * dim
+    if t.numel() and ((one != 1 and dim > 1) or (head != dim and heads > 1) or
+                      apart < heads * dim or apart % 8):
+        raise ValueError(f"{name}: a token's heads must be contiguous, its stride a multiple of 8 "
+                         f"no less than they take; got strides {t.stride()}")
+    return apart
+
+
+def _index(t, name, shape, dev):
+    torch = _torch()
+    if t is None or not _is(t, shape, torch.int32, dev):
+        _refuse(t, name, shape, torch.int32)
+    return t.data_ptr()
+
+
+def _heads_of(q, k, v):
+    """(heads, kv_heads, head_dim, device index) of the operands of an attention."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is None or t.dim() != 3:
+            raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
+    H, Hk, D, dev = q.shape[1], k.shape[1], q.shape[2], q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on the GPU")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} query heads cannot share {Hk} key heads")
+    return H, Hk, D, dev
+
+
+def _scratch(need: int, workspace, dev):
+    """(pointer, bytes, tensor) of a workspace of `need` bytes."""
+    torch = _torch()
+    if workspace is not None:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8)
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must live on cuda:{dev}, got {workspace.device}")
+    elif need:
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev)
+    else:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def _attention_outputs(shape, out, want_lse, dev):
+    torch = _torch()
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    elif not _is(out, shape, torch.bfloat16, dev):
+        _refuse(out, "out", shape, torch.bfloat16)
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
+    return out, lse
+
+
+def attention_packed(q, k, v, offsets, *, k_offsets=None, scale=None, want_lse: bool = False,
+                     out=None, workspace=None, stream=None) -> AttentionOutput:
+    """Causal attention within packed sequences (ar_attention_packed): q [Tq, heads,
+    head_dim], k and v [Tk, kv_heads, head_dim] bf16, whose tokens may lie apart (the
+    parts of one q|k|v product); offsets [B + 1] int32 on the GPU: sequence b's tokens of q,
+    and of k and v unless ``k_offsets`` gives theirs (then a query sees the keys up to its
+    own distance from the end). ``scale`` is 1/sqrt(head_dim) by default. Rows of out and
+    lse outside the offsets keep what ``out`` held (without ``out`` they hold nothing
+    meaningful)."""
+    torch = _torch()
+    H, Hk, D, dev = _heads_of(q, k, v)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, q, k, v, offsets, k_offsets, out, workspace):
+            return attention_packed(q, k, v, offsets, k_offsets=k_offsets, scale=scale,
+                                    want_lse=want_lse, out=out, workspace=workspace)
+    bf16 = (torch.bfloat16,)
+    qs, ks = _tokens(q, "q", H, D, bf16, dev), _tokens(k, "k", Hk, D, bf16, dev)
+    vs, Tq, Tk = _tokens(v, "v", Hk, D, bf16, dev), q.shape[0], k.shape[0]
+    if v.shape[0] != Tk:
+        raise ValueError(f"k has {Tk} tokens, v {v.shape[0]}")
+    if offsets is None or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a 1-D [B + 1] tensor")
+    B = offsets.shape[0] - 1
+    off = _index(offsets, "offsets", (B + 1,), dev)
+    koff = None if k_offsets is None else _index(k_offsets, "k_offsets", (B + 1,), dev)
+    if koff is None and Tq != Tk:
+        raise ValueError(f"{Tq} queries and {Tk} keys need k_offsets")
+    out, lse = _attention_outputs((Tq, H, D), out, want_lse, dev)
+    need = ctypes.c_size_t()
+    st = lib.ar_attention_packed_workspace_size(B, Tq, Tk, H, Hk, D, ctypes.byref(need))
+    _check(st, "ar_attention_packed_workspace_size")
+    ws, size, _keep = _scratch(need.value, workspace, dev)
+    st = lib.ar_attention_packed(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, H,
+                                 Hk, D, off, koff, B, D ** -0.5 if scale is None else scale,
+                                 out.data_ptr(), None if lse is None else lse.data_ptr(), ws, size,
+                                 torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_attention_packed")
+    return AttentionOutput(out, lse)
+
+
+def kv4_write(k, v, cache, slots, *, stream=None):
+    """Quantize the tokens k, v [T, heads, head_dim] (float32 / bf16; tokens may lie apart)
+    into slots [T] int32 of the cache (ar_kv4_write); slots outside it, -1 say, are left out."""
+    torch = _torch()
+    c, dev = _kv4(cache)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, *cache, k, v, slots):
+            return kv4_write(k, v, cache, slots)
+    dts = (torch.bfloat16, torch.float32)
+    ks, vs = _tokens(k, "k", c.heads, c.head_dim, dts, dev), \
+        _tokens(v, "v", c.heads, c.head_dim, dts, dev)
+    T = k.shape[0]
+    if v.shape[0] != T or v.dtype is not k.dtype:
+        raise ValueError(f"k is {k.dtype} of {T} tokens, v {v.dtype} of {v.shape[0]}")
+    st = lib.ar_kv4_write(ctypes.byref(c), _dt(k), k.data_ptr(), ks, v.data_ptr(), vs,
+                          _index(slots, "slots", (T,), dev), T,
+                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_kv4_write")
+
+
+def kv4_read(cache, slots, *, out_dtype=None, stream=None):
+    """k and v [T, heads, head_dim] (bf16 unless ``out_dtype`` says float32) held in slots [T]
+    int32 of the cache (ar_kv4_read); zeros for a slot outside it."""
+    torch = _torch()
+    c, dev = _kv4(cache)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, *cache, slots):
+            return kv4_read(cache, slots, out_dtype=out_dtype)
+    if slots is None or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D [T] tensor")
+    T = slots.shape[0]
+    at = _index(slots, "slots", (T,), dev)
+    H, D = c.heads, c.head_dim
+    k = torch.empty_strided((T, H, D), (H * D, D, 1), dtype=out_dtype or torch.bfloat16, device=dev)
+    v = torch.empty_like(k)
+    st = lib.ar_kv4_read(ctypes.byref(c), at, T, _dt(k), k.data_ptr(), v.data_ptr(),
+                         torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_kv4_read")
+    return k, v
+
+
+def kv4_attention(q, cache, table, lengths, *, max_len=None, scale=None, want_lse: bool = False,
+                  out=None, workspace=None, stream=None) -> AttentionOutput:
+    """Attention of each sequence's newest tokens over its cached ones, theirs among them
+    (ar_kv4_attention): q [B, heads, head_dim] (one token each) or [B, n, heads,
+    head_dim] bf16, table [B, width] int32 the pages of each sequence, lengths [B] int32
+    its tokens in the cache, both on the GPU. A length counts up to ``max_len`` (at most, and
+    by default, what the table can hold); naming the longest to come divides the work better.
+    ``workspace``: ar_kv4_attention_workspace_size bytes, not shared by calls that may
+    overlap."""
+    torch = _torch()
+    c, dev = _kv4(cache)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _elsewhere(stream, *cache, q, table, lengths, out, workspace):
+            return kv4_attention(q, cache, table, lengths, max_len=max_len, scale=scale,
+                                 want_lse=want_lse, out=out, workspace=workspace)
+    if q is None or q.dim() not in (3, 4):
+        raise ValueError("q must be a [B, heads, head_dim] or [B, n, heads, head_dim] tensor")
+    B, n, H = q.shape[0], (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    rows = q if q.dim() == 3 else q.flatten(0, 1)
+    if rows.numel() and rows.data_ptr() != q.data_ptr():
+        raise ValueError(f"q: the tokens must lie one stride apart, got strides {q.stride()}")
+    D = c.head_dim
+    qs = _tokens(rows, "q", H, D, (torch.bfloat16,), dev)
+    if H % c.heads:
+        raise ValueError(f"{H} query heads cannot share {c.heads} key heads")
+    if table is None or table.dim() != 2:
+        raise ValueError("table must be a 2-D [B, width] tensor")
+    W = table.shape[1]
+    tab, lens = _index(table, "table", (B, W), dev), _index(lengths, "lengths", (B,), dev)
+    if max_len is None:
+        max_len = W * c.page_size
+    out, lse = _attention_outputs(q.shape, out, want_lse, dev)
+    need = ctypes.c_size_t()
+    st = lib.ar_kv4_attention_workspace_size(ctypes.byref(c), B, n, H, max_len,
+                                             ctypes.byref(need))
+    if st:
+        _check(st, "ar_kv4_attention_workspace_size")
+    ws, size, _keep = _scratch(need.value, workspace, dev)
+    st = lib.ar_kv4_attention(ctypes.byref(c), rows.data_ptr(), qs, B, n, H, tab, W, lens, max_len,
+                              D ** -0.5 if scale is None else scale, out.data_ptr(),
+                              None if lse is None else lse.data_ptr(), ws, size,
+                              torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "ar_kv4_attention")
+    return AttentionOutput(out, lse)
 
 
 # ------------------------------------------------------------------ per-layer config

@@ -1094,6 +1094,154 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
       static_cast<hipStream_t>(stream));
 }
 
+// ------------------------------------------------------------------ attention, 4-bit cache
+namespace {
+
+constexpr int64_t kMaxI32 = int64_t(1) << 31;
+constexpr int64_t kMaxRatio = 256;   // query heads a key head, and new tokens a sequence
+constexpr int64_t kMaxSeqs = 65536;
+
+// heads over kv_heads, and a head's width.
+ar_status check_heads(int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  if (heads < 1 || kv_heads < 1 || kv_heads > 65535 || heads % kv_heads != 0) return AR_ERR_SHAPE;
+  if (heads / kv_heads > kMaxRatio) return AR_ERR_SHAPE;
+  return head_dim == 64 || head_dim == 128 ? AR_OK : AR_ERR_UNSUPPORTED;
+}
+bool stride_ok(int64_t stride, int64_t row) {
+  return stride >= row && stride % 8 == 0 && stride < kMaxLd;
+}
+bool scale_ok(float s) { return finite(s) && s > 0.0f; }
+
+// The sizes of a cache; its arrays where `arrays`.
+ar_status check_cache(const ar_kv4_cache* c, bool arrays) {
+  if (!c) return AR_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return AR_ERR_UNSUPPORTED;
+  if ((c->group_size != 32 && c->group_size != 64 && c->group_size != 128) ||
+      c->group_size > c->head_dim)
+    return AR_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return AR_ERR_UNSUPPORTED;
+  if (c->heads < 1 || c->heads > 65535 || c->pages < 1 ||
+      c->pages >= kMaxI32 / c->page_size)
+    return AR_ERR_SHAPE;
+  if (arrays && (!c->codes || !c->scale || !a16(c->codes) || !a16(c->scale)))
+    return AR_ERR_INVALID_ARG;
+  return AR_OK;
+}
+
+ar_status check_kv4_attention(const ar_kv4_cache* c, int64_t B, int64_t news, int64_t heads,
+                              int64_t max_len) {
+  AR_TRY(check_cache(c, false));
+  AR_TRY(check_heads(heads, c->heads, c->head_dim));
+  if (B < 0 || news < 0 || news > kMaxRatio || max_len < 0 || max_len >= (int64_t(1) << 30))
+    return AR_ERR_SHAPE;
+  return B < kMaxI32 && B * news < kMaxI32 && B * news * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
+}
+
+ar_status check_packed(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads,
+                       int64_t head_dim) {
+  AR_TRY(check_heads(heads, kv_heads, head_dim));
+  if (B < 0 || B > kMaxSeqs || Tq < 0 || Tk < 0 || Tq >= kMaxI32 || Tk >= kMaxI32)
+    return AR_ERR_SHAPE;
+  return Tq * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
+}
+
+}  // namespace
+
+ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,
+                                             int64_t kv_heads, int64_t head_dim, size_t* bytes) {
+  if (!bytes) return AR_ERR_INVALID_ARG;
+  AR_TRY(check_packed(B, Tq, Tk, heads, kv_heads, head_dim));
+  *bytes = (size_t)ar_attention_packed_floats(B, Tq, Tk, heads, kv_heads, head_dim) * sizeof(float);
+  return AR_OK;
+}
+
+ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                              int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                              const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                              float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream) {
+  AR_TRY(check_packed(B, Tq, Tk, heads, kv_heads, head_dim));
+  if (!k_offsets && Tq != Tk) return AR_ERR_SHAPE;
+  if (!scale_ok(scale)) return AR_ERR_INVALID_ARG;
+  if (Tq == 0 || B == 0) return AR_OK;
+  if (!stride_ok(q_stride, heads * head_dim) || !stride_ok(k_stride, kv_heads * head_dim) ||
+      !stride_ok(v_stride, kv_heads * head_dim))
+    return AR_ERR_SHAPE;
+  if (!q || !out || !q_offsets || !a16(q) || !a16(out) || !a4(q_offsets) || !a4(k_offsets) ||
+      !a4(lse))
+    return AR_ERR_INVALID_ARG;
+  if (Tk > 0 && (!k || !v || !a16(k) || !a16(v))) return AR_ERR_INVALID_ARG;
+  const size_t need =
+      (size_t)ar_attention_packed_floats(B, Tq, Tk, heads, kv_heads, head_dim) * sizeof(float);
+  if (ws_bytes < need) return AR_ERR_WORKSPACE;
+  if (need && (!ws || !a16(ws))) return AR_ERR_INVALID_ARG;
+  return ar_launch_attention_packed(
+      ArAttentionPacked{q, k, v, q_stride, k_stride, v_stride, Tq, Tk, heads, kv_heads, head_dim,
+                        q_offsets, k_offsets ? k_offsets : q_offsets, B, scale, out, lse,
+                        static_cast<float*>(ws)},
+      static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                       void* stream) {
+  AR_TRY(check_cache(cache, true));
+  if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
+  if (T < 0 || T >= kMaxI32) return AR_ERR_SHAPE;
+  if (T == 0) return AR_OK;
+  const int64_t row = cache->heads * cache->head_dim;
+  if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return AR_ERR_SHAPE;
+  if (!k || !v || !slots || !a16(k) || !a16(v) || !a4(slots)) return AR_ERR_INVALID_ARG;
+  return ar_launch_kv4_write(*cache, dt, k, k_stride, v, v_stride, slots, T,
+                             static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T, int32_t dt,
+                      void* k, void* v, void* stream) {
+  AR_TRY(check_cache(cache, true));
+  if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
+  if (T < 0 || T >= kMaxI32) return AR_ERR_SHAPE;
+  if (T == 0) return AR_OK;
+  if (!k || !v || !slots || !a16(k) || !a16(v) || !a4(slots)) return AR_ERR_INVALID_ARG;
+  return ar_launch_kv4_read(*cache, slots, T, dt, k, v, static_cast<hipStream_t>(stream));
+}
+
+ar_status ar_kv4_attention_workspace_size(const ar_kv4_cache* cache, int64_t B, int64_t new_tokens,
+                                          int64_t heads, int64_t max_len, size_t* bytes) {
+  if (!bytes) return AR_ERR_INVALID_ARG;
+  AR_TRY(check_kv4_attention(cache, B, new_tokens, heads, max_len));
+  *bytes = B * new_tokens == 0 ? 0
+                               : (size_t)ar_kv4_attention_floats(*cache, B, new_tokens, heads,
+                                                                 max_len) * sizeof(float);
+  return AR_OK;
+}
+
+ar_status ar_kv4_attention(const ar_kv4_cache* cache, const uint16_t* q, int64_t q_stride,
+                           int64_t B, int64_t new_tokens, int64_t heads, const int32_t* table,
+                           int64_t width, const int32_t* lengths, int64_t max_len, float scale,
+                           uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  AR_TRY(check_kv4_attention(cache, B, new_tokens, heads, max_len));
+  AR_TRY(check_cache(cache, true));
+  if (!scale_ok(scale)) return AR_ERR_INVALID_ARG;
+  if (width < 0 || width >= kMaxI32 / cache->page_size || max_len > width * cache->page_size)
+    return AR_ERR_SHAPE;
+  if (B == 0 || new_tokens == 0) return AR_OK;
+  if (!stride_ok(q_stride, heads * cache->head_dim)) return AR_ERR_SHAPE;
+  if (!q || !out || !lengths || !a16(q) || !a16(out) || !a4(lengths) || !a4(lse))
+    return AR_ERR_INVALID_ARG;
+  if (width > 0 && (!table || !a4(table))) return AR_ERR_INVALID_ARG;
+  const size_t need =
+      (size_t)ar_kv4_attention_floats(*cache, B, new_tokens, heads, max_len) * sizeof(float);
+  if (ws_bytes < need) return AR_ERR_WORKSPACE;
+  if (need && (!ws || !a16(ws))) return AR_ERR_INVALID_ARG;
+  return ar_launch_kv4_attention(
+      ArKv4Attention{cache, q, q_stride, B, new_tokens, heads, table, width, lengths, max_len,
+                     scale, out, lse, static_cast<float*>(ws)},
+      static_cast<hipStream_t>(stream));
+}
+
 ar_status ar_pack(int32_t bits, const uint8_t* codes, const uint8_t* zp, int64_t N, int64_t K,
                   int64_t G, int32_t* qweight, int32_t* qzeros, void* stream) {
   if (!(bits == 2 || bits == 3 || bits == 4 || bits == 8)) return AR_ERR_UNSUPPORTED;

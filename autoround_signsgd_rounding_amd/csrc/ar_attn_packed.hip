@@ -1,0 +1,343 @@
+// Causal attention over packed sequences with grouped heads (gfx950):
+//   out = softmax(scale·q·kᵀ)·v,  query i of a sequence of Lq queries and Lk keys seeing
+//   the keys 0 .. i + Lk - Lq.
+//
+// A workgroup takes 128 rows, 32 a wave, of one sequence and key head. Rows are the
+// queries of all the heads that share it, token by token: keys and values are staged once
+// for the group, and a short prompt fills a tile with its heads. Keys and values pass
+// through LDS in tiles of 64 tokens, two stages, loaded straight to LDS.
+//
+// Scores are formed transposed, Sᵀ = K·Qᵀ on v_mfma_f32_32x32x16_bf16, so a lane holds one
+// row's scores of half the tile's tokens. Which token is which row of K is chosen so that
+// the lane's scores 8i .. 8i + 7 are neighbouring tokens, which are the eight that it
+// supplies as the B operand of Oᵀ = Vᵀ·Pᵀ: the weights stay where they are. The A operand
+// there is V transposed, which ds_read_b64_tr_b16 gives out of V as it lies in memory.
+// p = 2^(s - m) with a running reference m that follows the maximum only when that has
+// risen by more than 8; p is rounded to bf16 for the product (2^-9 of each weight, about as
+// much in the output as its own rounding to bf16), the sums of p and all accumulators are
+// float32.
+#include <math.h>
+
+#include "ar_device.h"
+#include "ar_launch.h"
+
+namespace {
+
+constexpr int NT = 256, BM = 128, KT = 64;
+constexpr float NO_MAX = -3.0e38f;
+constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+#define AR_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+
+inline ar_status last_status() { return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP; }
+
+struct Args {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *q_off, *k_off;
+  int64_t Tq, Tk;
+  int B, heads, kv_heads, ratio, tiles;
+  float sl;   // scale·log2 e
+  uint16_t* out;
+  float* lse;
+};
+
+// Sequence b's queries and keys, by offsets that lead nowhere outside the arrays.
+struct Seq {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  s.q0 = min(max(a.q_off[b], 0), (int)a.Tq);
+  s.nq = min(max(a.q_off[b + 1], s.q0), (int)a.Tq) - s.q0;
+  s.k0 = min(max(a.k_off[b], 0), (int)a.Tk);
+  s.nk = min(max(a.k_off[b + 1], s.k0), (int)a.Tk) - s.k0;
+  return s;
+}
+
+// Tile t of the sequences' rows cut into tiles of BM: its sequence and first row; false
+// when there is no such tile. The whole wave calls it.
+__device__ __forceinline__ bool find_tile(const Args& a, int t, int& b, int& r0) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int base = 0; base < a.B; base += 64) {
+    int64_t tiles = 0;
+    if (base + lane < a.B) {
+      const Seq s = seq_of(a, base + lane);
+      tiles = ((int64_t)s.nq * a.ratio + BM - 1) / BM;
+    }
+    int64_t sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t up = __shfl_up((long long)sum, d, 64);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(before + sum > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int64_t first = before + __shfl((long long)(sum - tiles), l, 64);
+      b = __builtin_amdgcn_readfirstlane(base + l);
+      r0 = __builtin_amdgcn_readfirstlane((int)((t - first) * BM));
+      return true;
+    }
+    before += __shfl((long long)sum, 63, 64);
+  }
+  return false;
+}
+
+__device__ __forceinline__ bool finite_bits(uint32_t pair) {
+  return (pair & 0x7F80u) != 0x7F80u && (pair & 0x7F800000u) != 0x7F800000u;
+}
+
+// One row by the definition, by one wave: for a row whose product met an infinity or a NaN
+// of a value hidden from it (0·inf). sees: the keys it sees. o: the wave's lane takes the
+// channels lane, lane + 64.
+template <int DH>
+__device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, const uint16_t* k,
+                                       const uint16_t* v, int sees, uint16_t* out) {
+  const int lane = threadIdx.x & 63;
+  float m = NO_MAX, l = 0.0f, o[DH / 64];
+#pragma unroll
+  for (int d = 0; d < DH / 64; ++d) o[d] = 0.0f;
+  for (int t0 = 0; t0 < sees; t0 += 64) {
+    float s = -INFINITY;
+    if (t0 + lane < sees) {
+      const uint16_t* kr = k + (int64_t)(t0 + lane) * a.k_stride;
+      s = 0.0f;
+      for (int d = 0; d < DH; ++d) s = fmaf(bf16_val(q[d]), bf16_val(kr[d]), s);
+      s *= a.sl;
+    }
+    const float mn = fmaxf(m, group_max<64>(s)), by = exp2f(m - mn);
+    m = mn;
+    const float p = t0 + lane < sees ? exp2f(s - m) : 0.0f;
+    l = l * by + group_sum<64>(p);
+#pragma unroll
+    for (int d = 0; d < DH / 64; ++d) o[d] *= by;
+    for (int j = 0; j < min(64, sees - t0); ++j) {
+      const float w = __shfl(p, j, 64);
+#pragma unroll
+      for (int d = 0; d < DH / 64; ++d)
+        o[d] = fmaf(w, bf16_val(v[(int64_t)(t0 + j) * a.v_stride + lane + 64 * d]), o[d]);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < DH / 64; ++d) out[lane + 64 * d] = (uint16_t)bf16_bits(o[d] / l);
+}
+
+template <int DH>
+__global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
+  constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
+  constexpr int TILE = KT * ROW;                   // bytes of a tile of keys or values
+  constexpr int LD = TILE / (NT * 16), LROWS = NT / C;   // loads a wave, rows between them
+  constexpr int ND = DH / 32, NC = DH / 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][TILE];
+
+  const int kvh = blockIdx.x % a.kv_heads;
+  int b, r0;
+  if (!find_tile(a, a.tiles - 1 - (int)(blockIdx.x / a.kv_heads), b, r0)) return;
+  const Seq sq = seq_of(a, b);
+  const int nk = __builtin_amdgcn_readfirstlane(sq.nk), nq = __builtin_amdgcn_readfirstlane(sq.nq);
+  const int k0 = __builtin_amdgcn_readfirstlane(sq.k0), q0 = __builtin_amdgcn_readfirstlane(sq.q0);
+  const int rows = nq * a.ratio;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l31 = lane & 31, half = lane >> 5;
+
+  // the lane's row: query i of the sequence, seeing keys 0 .. last
+  const int row = r0 + 32 * wave + l31, i = min(row, rows - 1) / a.ratio;
+  const int head = kvh * a.ratio + min(row, rows - 1) - i * a.ratio;
+  const int last = i + nk - nq;
+  const uint16_t* qp = a.q + (int64_t)(q0 + i) * a.q_stride + head * DH;
+  bf16x8_t qf[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) qf[c] = *reinterpret_cast<const bf16x8_t*>(qp + 16 * c + 8 * half);
+
+  // what the workgroup, and what every row of the wave, sees
+  const int wrow0 = r0 + 32 * wave;
+  const int kend = min((min(r0 + BM, rows) - 1) / a.ratio + nk - nq + 1, nk);
+  const int wfirst = min(wrow0, rows - 1) / a.ratio + nk - nq;                    // least of last
+  const int wend = wrow0 < rows ? (min(wrow0 + 32, rows) - 1) / a.ratio + nk - nq + 1 : 0;
+
+  // loads: chunk p of a tile lies at its place with the chunk number turned by the row, so
+  // that the reads below meet 64 different banks
+  const int lrow = threadIdx.x / C, lpos = threadIdx.x % C;
+  const int kswz = C == 16 ? lrow & 15 : (lrow >> 1) & 7;
+  const int vswz = C == 16 ? (lrow & 3) << 2 : ((lrow >> 1) & 1) << 2;
+  const uint32_t kvo = (uint32_t)(lrow * a.k_stride * 2 + ((lpos ^ kswz) << 4));
+  const uint32_t vvo = (uint32_t)(lrow * a.v_stride * 2 + ((lpos ^ vswz) << 4));
+  const uint16_t* kb = a.k + (int64_t)k0 * a.k_stride + kvh * DH;
+  const uint16_t* vb = a.v + (int64_t)k0 * a.v_stride + kvh * DH;
+  auto stage = [&](int t0, int s) {
+    const int n = min(nk - t0, KT);
+    const auto bk = make_rsrc(kb + (int64_t)t0 * a.k_stride,
+                              (uint32_t)(((n - 1) * a.k_stride + DH) * 2));
+    const auto bv = make_rsrc(vb + (int64_t)t0 * a.v_stride,
+                              (uint32_t)(((n - 1) * a.v_stride + DH) * 2));
+#pragma unroll
+    for (int j = 0; j < LD; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bk, AR_LDS(&lds[s][0][(j * 4 + wave) * 1024]), 16,
+                                               kvo + (uint32_t)(j * LROWS * a.k_stride * 2), 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < LD; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bv, AR_LDS(&lds[s][1][(j * 4 + wave) * 1024]), 16,
+                                               vvo + (uint32_t)(j * LROWS * a.v_stride * 2), 0, 0, 0);
+  };
+
+  // reads: key row of the lane (row r of the product is the token that puts neighbouring
+  // tokens side by side in a lane's scores), chunk 2c + half
+  const int kr = 16 * (l31 >> 4) + 8 * ((l31 >> 2) & 1) + 4 * ((l31 >> 3) & 1) + (l31 & 3);
+  const int krs = C == 16 ? kr & 15 : (kr >> 1) & 7;
+  int kat[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) kat[c] = kr * ROW + (((2 * c + half) ^ krs) << 4);
+  // values: 16 lanes take 4 tokens x 16 channels, transposed
+  const int l15 = lane & 15, vk = 8 * half + (l15 >> 2), dh16 = (lane >> 4) & 1;
+  int vat[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    const int chunk = 4 * d + 2 * dh16 + ((l15 & 3) >> 1);
+    const int sw = C == 16 ? (vk & 3) << 2 : ((vk >> 1) & 1) << 2;
+    vat[d] = vk * ROW + ((chunk ^ sw) << 4) + 8 * (l15 & 1);
+  }
+
+  f32x16_t o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+  float m = NO_MAX, l = 0.0f;
+
+  auto work = [&](int t0, const uint8_t* lk, const uint8_t* lv) {
+    f32x16_t s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[j][r] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const bf16x8_t f = *reinterpret_cast<const bf16x8_t*>(lk + kat[c] + j * 32 * ROW);
+        s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[c], s[j], 0, 0, 0);
+      }
+    }
+    if (t0 + KT > wfirst + 1) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (t0 + 32 * j + 16 * (r >> 3) + 8 * half + (r & 7) > last) s[j][r] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[j][r]);
+    top *= a.sl;
+    if (__any(top > m + RISE)) {
+      const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+      const float by = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= by;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= by;
+    }
+    u32x4_t p[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], a.sl, -m));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(s[j][r + 1], a.sl, -m));
+        l += e0 + e1;
+        p[2 * j + (r >> 3)][(r & 7) >> 1] = bf16_pair(e0, e1);
+      }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        typedef __attribute__((address_space(3))) s16x4_t* tr;
+        const uint8_t* at = lv + vat[d] + 16 * kk * ROW;
+        const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr)(at));
+        const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr)(at + 4 * ROW));
+        const auto f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                       __builtin_bit_cast(bf16x8_t, p[kk]), o[d],
+                                                       0, 0, 0);
+      }
+  };
+
+  if (kend > 0) stage(0, 0);
+  int s = 0;
+  for (int t0 = 0; t0 < kend; t0 += KT, s ^= 1) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of the tile (vmcnt 0)
+    __syncthreads();                      // everybody's; and the other stage has been read
+    if (t0 + KT < kend) stage(t0 + KT, s ^ 1);
+    if (t0 < wend) work(t0, lds[s][0], lds[s][1]);
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (row < rows) {
+    const int64_t to = (int64_t)(q0 + i) * a.heads + head;
+    const float inv = last < 0 ? 0.0f : 1.0f / l;   // a row that sees no key is 0
+    uint16_t* op = a.out + to * DH + 4 * half;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<u32x2_t*>(op + 32 * d + 8 * r) =
+            u32x2_t{bf16_pair(o[d][4 * r] * inv, o[d][4 * r + 1] * inv),
+                    bf16_pair(o[d][4 * r + 2] * inv, o[d][4 * r + 3] * inv)};
+    if (a.lse && half == 0) a.lse[to] = last < 0 ? -INFINITY : 0.69314718f * (m + __log2f(l));
+  }
+
+  // An infinity or a NaN among the values of a tile meets weights of 0 in the rows that do
+  // not see it, and makes them NaN: such rows are done again.
+  float big = 0.0f;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      big = __builtin_elementwise_maximum(big, fabsf(o[d][r]));
+  const bool off = row < rows && !(big < INFINITY) && last >= 0;
+  uint64_t redo = __ballot(off);
+  redo = (redo | (redo >> 32)) & 0xFFFFFFFFull;
+  if (redo) {
+    bool found = false;   // (keys beyond the wave's rows, and so hidden from some of them)
+    for (int t = max(wfirst + 1, 0) + lane; t < min(nk, (wend + KT - 1) / KT * KT); t += 64) {
+      const uint16_t* vr = vb + (int64_t)t * a.v_stride;
+      for (int d = 0; d < DH; d += 2)
+        found |= !finite_bits(*reinterpret_cast<const uint32_t*>(vr + d));
+    }
+    if (__any(found))
+      while (redo) {
+        const int r = __ffsll((unsigned long long)redo) - 1;
+        redo &= redo - 1;
+        const int ri = __shfl(i, r, 64), rh = __shfl(head, r, 64);
+        plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, ri + nk - nq + 1,
+                      a.out + ((int64_t)(q0 + ri) * a.heads + rh) * DH);
+      }
+  }
+}
+
+}  // namespace
+
+int64_t ar_attention_packed_floats(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
+  return 0;
+}
+
+ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st) {
+  Args a;
+  a.q = g.q, a.k = g.k, a.v = g.v;
+  a.q_stride = g.q_stride, a.k_stride = g.k_stride, a.v_stride = g.v_stride;
+  a.q_off = g.q_offsets, a.k_off = g.k_offsets;
+  a.Tq = g.Tq, a.Tk = g.Tk;
+  a.B = (int)g.B, a.heads = (int)g.heads, a.kv_heads = (int)g.kv_heads;
+  a.ratio = (int)(g.heads / g.kv_heads);
+  a.tiles = (int)(g.Tq * a.ratio / BM + g.B);   // no less than the sequences' tiles
+  a.sl = (float)((double)g.scale * 1.4426950408889634);
+  a.out = g.out, a.lse = g.lse;
+  const dim3 grid((unsigned)((int64_t)a.tiles * a.kv_heads));
+  if (g.head_dim == 64) hipLaunchKernelGGL((k_attention_packed<64>), grid, dim3(NT), 0, st, a);
+  else hipLaunchKernelGGL((k_attention_packed<128>), grid, dim3(NT), 0, st, a);
+  return last_status();
+}

@@ -229,3 +229,45 @@ struct ArFp8Gemm {
   bool wide;
 };
 ar_status ar_launch_fp8_gemm(const ArFp8Gemm& g, hipStream_t st);
+
+// 4-bit key/value cache (ar_kv4.hip). T > 0; slots outside the cache are left out
+// (written) or give zeros (read).
+ar_status ar_launch_kv4_write(const ar_kv4_cache& c, int dt, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                              hipStream_t st);
+ar_status ar_launch_kv4_read(const ar_kv4_cache& c, const int32_t* slots, int64_t T, int dt,
+                             void* k, void* v, hipStream_t st);
+
+// Attention over that cache (ar_kv4_attn.hip): max_len bounds the lengths; ws holds
+// ar_kv4_attention_floats floats, 16-byte aligned.
+struct ArKv4Attention {
+  const ar_kv4_cache* cache;
+  const uint16_t* q;
+  int64_t q_stride, B, news, heads;
+  const int32_t* table;
+  int64_t width;
+  const int32_t* lengths;
+  int64_t max_len;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* ws;
+};
+int64_t ar_kv4_attention_floats(const ar_kv4_cache& c, int64_t B, int64_t news, int64_t heads,
+                                int64_t max_len);
+ar_status ar_launch_kv4_attention(const ArKv4Attention& g, hipStream_t st);
+
+// Causal attention over packed sequences (ar_attn_packed.hip); strides in elements.
+struct ArAttentionPacked {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride, Tq, Tk, heads, kv_heads, head_dim;
+  const int32_t *q_offsets, *k_offsets;
+  int64_t B;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* ws;
+};
+int64_t ar_attention_packed_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,
+                                   int64_t kv_heads, int64_t head_dim);
+ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st);

@@ -319,6 +319,105 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
                               const int32_t* offsets, const int32_t* row_index, int64_t R, void* Y,
                               int32_t ydt, void* stream);
 
+/* ---- Attention and the 4-bit key/value cache --------------------------------
+   What a decoder layer needs between its q/k/v product and its o product, in serving and
+   on calibration sequences of different lengths: attention over whole prompts beside
+   ar_attention, which takes one length and as many key heads as query heads; a cache that
+   holds keys and values on the integer grid of ar_rtn_quant (asymmetric, 4 bits); and
+   attention of new tokens straight from it. q, k and v come as products of ar_fp8_gemm or
+   ar_dequant_gemm leave them, rotated where the model rotates.
+
+   heads query heads share kv_heads key heads, heads/kv_heads neighbours each (heads must
+   be a multiple, the quotient at most 256). head_dim is 64 or 128. q, k and v are
+   [tokens, heads, head_dim] with a stride in elements between tokens (a multiple of 8, at
+   least heads*head_dim, below 2^22), so they may be parts of one q|k|v product. bf16 unless
+   said otherwise; float32 softmax and sums; outputs bf16, contiguous. scale multiplies
+   q·k and must be positive and finite. lse (nullable): the natural logarithm of the row's
+   sum of exponentials, [tokens, heads] float32. A row that sees no key is 0, its lse
+   minus infinity. What a row does not see may hold anything, NaN too. Index arrays need
+   4-byte alignment, the others 16. */
+
+/* Bytes of device workspace of ar_attention_packed. */
+ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,
+                                             int64_t kv_heads, int64_t head_dim, size_t* bytes);
+
+/* Causal attention within each of B sequences packed one behind the other: sequence b's
+   queries are the tokens q_offsets[b] .. q_offsets[b+1] of q [Tq], its keys and values
+   the tokens k_offsets[b] .. k_offsets[b+1] of k and v [Tk] (k_offsets NULL: q_offsets,
+   and Tq = Tk). Query i of Lq sees the keys 0 .. i + Lk - Lq: all of them at the last
+   query, so a chunk of a prompt takes the keys of what came before it too. Offsets
+   [B+1] int32 on the device, non-decreasing; a sequence may have no queries, or fewer keys
+   than queries. Rows of out [Tq, heads, head_dim] and lse outside [q_offsets[0],
+   q_offsets[B]) keep what they held. Contents of the offsets are not checked on the host:
+   they are clamped to [0, Tq] and [0, Tk], and with decreasing ones rows of out are
+   unspecified, but nothing outside the arrays is read or written. The weights are rounded
+   to bf16 for their product with v. Tq = 0 or B = 0 is a no-op; B <= 65536;
+   Tq*heads < 2^31, Tk < 2^31. No host synchronisation. */
+ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                              int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                              const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                              float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* A cache of pages of page_size tokens (16, 32, 64, 128 or 256). Slot p*page_size + t is
+   token t of page p. Per token, head and group of group_size channels (32, 64 or 128, a
+   divisor of head_dim), for keys and for values, in float32, each step rounded once:
+     lo = min(x, 0), hi = max(x, 0), s = (hi - lo)/15 (1 if 0; never below 2^-100),
+     zp = clamp(rint(-lo/s), 0, 15), s' = s with its four lowest mantissa bits replaced by zp,
+     code = clamp(rint(x/s') + zp, 0, 15); the value held is s'·(code - zp).
+   A NaN or an infinity, or a range beyond float32, makes s' NaN and with it the group.
+   codes [pages, 2, heads, page_size, head_dim/2] uint8, two codes a byte, the even channel
+   in the low half: the keys' (first) bytes in order; of the values, byte 32·b + 16·c + n
+   of token t at [t/8][b][n][t%8][c]. scale [pages, 2, heads, page_size,
+   head_dim/group_size] float32: s'. pages*page_size < 2^31. */
+typedef struct {
+  uint8_t* codes;
+  float* scale;
+  int64_t pages;
+  int64_t heads;        /* key heads */
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t group_size;
+} ar_kv4_cache;
+
+/* Quantize k and v [T, cache heads, head_dim] (dt AR_F32 or AR_BF16; strides as above)
+   into slots [T] int32 on the device; tokens whose slot lies outside the cache (-1, say)
+   are left out. Where two tokens of one call name the same slot, what that slot then
+   holds is unspecified (every other slot is as it should be). T = 0 is a no-op;
+   T < 2^31. */
+ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                       void* stream);
+
+/* The values held in slots [T] int32 (any number of times each), to k and v [T, cache heads,
+   head_dim] of dtype dt, contiguous; zeros for a slot outside the cache. A bf16 output is
+   rounded once. T = 0 is a no-op; T < 2^31. */
+ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T, int32_t dt,
+                      void* k, void* v, void* stream);
+
+/* Bytes of device workspace of ar_kv4_attention (of cache, its sizes only are read). */
+ar_status ar_kv4_attention_workspace_size(const ar_kv4_cache* cache, int64_t B, int64_t new_tokens,
+                                          int64_t heads, int64_t max_len, size_t* bytes);
+
+/* Attention of the newest new_tokens tokens of each of B sequences over its cached tokens,
+   theirs among them: q [B*new_tokens, heads, head_dim]; sequence b's token t lies in page
+   table[b, t / page_size] at t % page_size (table [B, width] int32), and it has
+   lengths[b] (int32) of them, so its new token i sees those before lengths[b] -
+   new_tokens + 1 + i. Both arrays are on the device and not checked on the host: a length
+   is taken as min(max(length, 0), max_len), and tokens of a page that is not of the cache (-1, say)
+   take no part. max_len (the largest length to come; at most width*page_size, below
+   2^30) decides how a long sequence is divided, and with it the workspace. out [B*new_tokens,
+   heads, head_dim], lse [B*new_tokens, heads]. Keys and values enter exactly as they are
+   held, the weights, each with its value's scale, rounded to f16. B*new_tokens = 0 is a no-op;
+   new_tokens <= 256, B*heads*new_tokens < 2^31. No host synchronisation: the call can be captured in a
+   HIP graph and replayed with other lengths and tables. Two calls that may overlap need
+   workspaces of their own. */
+ar_status ar_kv4_attention(const ar_kv4_cache* cache, const uint16_t* q, int64_t q_stride,
+                           int64_t B, int64_t new_tokens, int64_t heads, const int32_t* table,
+                           int64_t width, const int32_t* lengths, int64_t max_len, float scale,
+                           uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- Sequential block-wise tuning with quantized inputs --------------------
    [LLMC] tuning loop (each Linear of a subgraph tuned in turn on its captured
    inputs and targets), parameter table and "enable_quanted_input 모드" (the

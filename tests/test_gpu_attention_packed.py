@@ -1,0 +1,255 @@
+"""attention_packed against the oracle in float64: lengths from one token to several tiles,
+grouped heads, packed sequences, keys longer and shorter than queries, tokens that lie apart,
+rows that see nothing, infinities where nobody looks, offsets that lead nowhere."""
+import numpy as np
+import pytest
+import torch
+
+from attention_common import bf16, check, i32, keys, lse_bound, oracle_heads, out_bound
+from gpu_common import dev, log
+from oracle import kv4_ref as R
+
+pytestmark = pytest.mark.gpu
+ar = pytest.importorskip("autoround_signsgd_rounding_amd")
+
+P_BITS = 2.0 ** -8       # weights are rounded to bf16
+
+
+def offsets(lengths):
+    return np.concatenate([[0], np.cumsum(lengths)]).astype(int)
+
+
+def problem(seed, lq, lk, H, Hk, D):
+    rng = np.random.default_rng(seed)
+    q, k = 1.5 * rng.normal(size=(sum(lq), H, D)), keys(rng, sum(lk), Hk, D)
+    v = rng.normal(size=(sum(lk), Hk, D))
+    return bf16(q), bf16(k), bf16(v)
+
+
+def verify(got, lse, q, k, v, qo, ko, scale, what):
+    for b in range(len(qo) - 1):
+        rows, cols = slice(qo[b], qo[b + 1]), slice(ko[b], ko[b + 1])
+        nq, nk = qo[b + 1] - qo[b], ko[b + 1] - ko[b]
+        if nq == 0:
+            continue
+        out, l, size, mag = oracle_heads(q[rows], k[cols], v[cols], R.causal(nq, nk), scale)
+        D = q.shape[2]
+        check(got[rows], out, out_bound(out, size, mag, D, nk, P_BITS), f"{what}: out {b}")
+        if lse is not None:
+            empty = np.isneginf(l)
+            assert (np.isneginf(lse[rows]) == empty).all(), what
+            check(lse[rows][~empty], l[~empty], lse_bound(l, mag, D, nk)[~empty], f"{what}: lse {b}")
+            assert (got[rows][empty] == 0).all()
+
+
+CASES = [  # queries, keys (None: the same), heads, key heads, head_dim
+    ([1], None, 1, 1, 64),
+    ([1, 1, 2], None, 4, 4, 128),
+    ([37], None, 8, 8, 128),
+    ([64, 63, 65], None, 4, 2, 64),
+    ([130], None, 6, 2, 128),
+    ([16, 1, 200, 3, 77], None, 8, 1, 128),
+    ([129, 0, 31], None, 7, 1, 64),
+    ([300], None, 2, 2, 128),
+    ([700], None, 3, 1, 64),
+    ([5, 17, 90], [5 + 200, 17 + 63, 90 + 64], 8, 2, 128),
+    ([1], [513], 8, 2, 64),
+    ([40, 3, 100], [10, 0, 99], 4, 2, 128),     # fewer keys than queries: rows that see nothing
+    ([2, 2], [0, 0], 2, 1, 64),
+    ([9], [70], 256, 1, 64),                    # the largest group
+]
+
+
+@pytest.mark.parametrize("lq,lk,H,Hk,D", CASES)
+def test_against_the_oracle(lq, lk, H, Hk, D):
+    log(f"packed {lq} {lk} heads {H}/{Hk} x {D}")
+    same, lk = lk is None, lq if lk is None else lk
+    (Q, q), (K, k), (V, v) = problem(sum(lq) + H, lq, lk, H, Hk, D)
+    qo, ko = offsets(lq), offsets(lk)
+    r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=None if same else i32(ko), want_lse=True)
+    torch.cuda.synchronize()
+    got, lse = r.out.double().cpu().numpy(), r.lse.cpu().numpy()
+    verify(got, lse, q, k, v, qo, ko, D ** -0.5, "packed")
+    again = ar.attention_packed(Q, K, V, i32(qo), k_offsets=None if same else i32(ko))
+    assert again.lse is None and torch.equal(again.out, r.out)
+
+
+def test_parts_of_one_product():
+    """q, k and v side by side in one array, another scale, a given output."""
+    log("packed strided")
+    H, Hk, D, T = 4, 2, 64, 150
+    rng = np.random.default_rng(5)
+    qkv, x = bf16(rng.normal(size=(T, H + 2 * Hk, D)))
+    Q, K, V = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    out = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device=dev())
+    r = ar.attention_packed(Q, K, V, i32([3, 60, 140]), scale=0.25, out=out, want_lse=True)
+    torch.cuda.synchronize()
+    assert r.out is out
+    got = out.double().cpu().numpy()
+    assert (got[:3] == 7).all() and (got[140:] == 7).all()      # rows of no sequence
+    q, k, v = x[:, :H], x[:, H:H + Hk], x[:, H + Hk:]
+    verify(got, r.lse.cpu().numpy(), q, k, v, [3, 60, 140], [3, 60, 140], 0.25, "parts")
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_hidden_infinities(bad):
+    """A NaN or an infinity in a key or a value reaches the rows that see it, and no other:
+    not those in front of it, not another sequence's."""
+    log(f"packed hidden {bad}")
+    lq, H, Hk, D = [70, 130, 64], 4, 2, 128
+    rng = np.random.default_rng(9)
+    (Q, q), (K, k), (V, v) = problem(8, lq, lq, H, Hk, D)
+    qo = offsets(lq)
+    want = ar.attention_packed(Q, K, V, i32(qo)).out
+    for t, which in ((qo[1] + 100, "v"), (qo[1] + 3, "k"), (qo[0] + 69, "v"), (qo[2], "k")):
+        X = {"k": K.clone(), "v": V.clone()}
+        X[which][t, 1, 5] = bad
+        r = ar.attention_packed(Q, X["k"], X["v"], i32(qo), want_lse=True)
+        torch.cuda.synchronize()
+        b = int(np.searchsorted(qo, t, side="right")) - 1
+        clean = np.ones((sum(lq), H), bool)
+        clean[t:qo[b + 1], H // Hk:] = False
+        clean = torch.from_numpy(clean).to(dev())
+        d = (r.out.double() - want.double())[clean].abs()
+        # the rows that are done again round their weights less: both are within the bound
+        assert d.max().item() <= 0.05, (t, which)
+        assert torch.isfinite(r.out[clean]).all()
+        hit = r.out[t:qo[b + 1], H // Hk:]
+        if which == "v":
+            assert not torch.isfinite(hit[..., 5]).any()
+            assert torch.isfinite(hit[..., 6]).all()
+            if np.isinf(bad):
+                assert (hit[..., 5] == bad).all()
+        elif np.isnan(bad):
+            assert torch.isnan(hit).all() and torch.isnan(r.lse[t:qo[b + 1], H // Hk:]).all()
+    # exact values of rows done again
+    V2 = V.clone()
+    V2[qo[1] + 129, 0, 0] = bad
+    got = ar.attention_packed(Q, K, V2, i32(qo)).out.double().cpu().numpy()
+    sl = slice(qo[1], qo[1] + 129)
+    out, _, size, mag = oracle_heads(q[sl], k[sl], v[sl], R.causal(129, 129), D ** -0.5)
+    check(got[sl], out, out_bound(out, size, mag, D, 129, P_BITS), "rows done again")
+
+
+def test_extreme_scores():
+    """Rows whose weight is all on one key, scores in the thousands, equal scores."""
+    log("packed extreme scores")
+    H, D, T = 2, 64, 200
+    rng = np.random.default_rng(1)
+    (Q, q), (K, k), (V, v) = problem(2, [T], [T], H, H, D)
+    Q[50:100] *= 64
+    K[::7] *= 16
+    Q[100:120] = 0
+    q, k = Q.double().cpu().numpy(), K.double().cpu().numpy()
+    r = ar.attention_packed(Q, K, V, i32([0, T]), want_lse=True)
+    torch.cuda.synchronize()
+    verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, [0, T], [0, T], D ** -0.5,
+           "extreme")
+
+
+def test_large_values():
+    log("packed large values")
+    (Q, q), (K, k), (V, v) = problem(4, [90], [90], 2, 2, 64)
+    V = V * 1e30
+    v = V.double().cpu().numpy()
+    got = ar.attention_packed(Q, K, V, i32([0, 90])).out.double().cpu().numpy()
+    verify(got, None, q, k, v, [0, 90], [0, 90], 0.125, "large values")
+
+
+@pytest.mark.parametrize("qo", [[0, 500, 100], [-5, 60, 1 << 30], [90, 20, 50, 10], [200, 300, 400],
+                                [-1 << 31, (1 << 31) - 1], [0, 0, 0]])
+def test_offsets_that_lead_nowhere(qo):
+    """Offsets outside the arrays are clamped, decreasing ones give something; nothing
+    outside the output is written."""
+    log(f"packed offsets {qo}")
+    T, H, D = 96, 4, 64
+    (Q, _), (K, _), (V, _) = problem(3, [T], [T], H, 2, D)
+    whole = torch.full((T + 64, H, D), 7.0, dtype=torch.bfloat16, device=dev())
+    ar.attention_packed(Q, K, V, i32(qo), out=whole[32:32 + T])
+    ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(qo[::-1]), out=whole[32:32 + T])
+    torch.cuda.synchronize()
+    assert (whole[:32] == 7).all() and (whole[32 + T:] == 7).all()
+
+
+def test_many_sequences():
+    """More sequences than a wave has lanes, most of them short or empty."""
+    log("packed many sequences")
+    rng = np.random.default_rng(11)
+    lq = [int(x) for x in rng.choice([0, 1, 2, 5, 40], size=300)]
+    (Q, q), (K, k), (V, v) = problem(12, lq, lq, 2, 1, 64)
+    qo = offsets(lq)
+    got = ar.attention_packed(Q, K, V, i32(qo)).out.double().cpu().numpy()
+    verify(got, None, q, k, v, qo, qo, 0.125, "many")
+
+
+@pytest.mark.parametrize("T,H,Hk,D", [(4096, 8, 1, 128), (9000, 2, 2, 64)])
+def test_long_against_float64(T, H, Hk, D):
+    """Long prompts, against float64 on the GPU row by row of heads."""
+    log(f"packed long {T} {H}/{Hk} x {D}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    q, k, v = (torch.randn((T, h, D), generator=g, device="cuda").to(torch.bfloat16)
+               for h in (H, Hk, Hk))
+    r = ar.attention_packed(q, k, v, i32([0, T]), want_lse=True)
+    for h in range(H):
+        x = (q[:, h].double() @ k[:, h // (H // Hk)].double().t()) * D ** -0.5
+        x = x.masked_fill(torch.ones((T, T), dtype=torch.bool, device="cuda").triu(1), -np.inf)
+        lse = torch.logsumexp(x, 1)
+        p = torch.exp(x - lse[:, None])
+        vh = v[:, h // (H // Hk)].double()
+        out, size = p @ vh, p @ vh.abs()
+        mag = D ** -0.5 * (q[:, h].double().abs() @ k[:, h // (H // Hk)].double().abs().t()).amax(1)
+        b = out_bound(out.cpu().numpy(), size.cpu().numpy(), mag.cpu().numpy(), D, T, P_BITS)
+        check(r.out[:, h].double().cpu().numpy(), out.cpu().numpy(), b, "long")
+        check(r.lse[:, h].double().cpu().numpy(), lse.cpu().numpy(),
+              lse_bound(lse.cpu().numpy(), mag.cpu().numpy(), D, T), "long lse")
+
+
+def test_few_queries_behind_a_long_prefix():
+    """A chunk of a few tokens behind thousands: the keys' axis is what there is to divide."""
+    log("packed chunk")
+    lq, lk = [3, 20], [5000, 2777]
+    (Q, q), (K, k), (V, v) = problem(21, lq, lk, 8, 2, 128)
+    qo, ko = offsets(lq), offsets(lk)
+    r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True)
+    verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, qo, ko, 128 ** -0.5, "chunk")
+
+
+def test_equals_the_blocks_attention():
+    """Sequences of one length and a key head for each query head: ar_attention's case."""
+    log("packed beside ar_attention")
+    H, D, S, B = 4, 128, 200, 3
+    (Q, _), (K, _), (V, _) = problem(6, [S] * B, [S] * B, H, H, D)
+    dims = ar.block_dims(H * D, H, 64, S, B)
+    flat = [x.reshape(S * B, H * D).contiguous() for x in (Q, K, V)]
+    want = ar.attention(*flat, dims).view(S * B, H, D).double()
+    got = ar.attention_packed(Q, K, V, i32(offsets([S] * B))).out.double()
+    # both within their roundings of the same values (|v| below 5)
+    assert (got - want).abs().max().item() <= 2.0 ** -8 * 2 * 5
+    assert ((got - want).norm() / want.norm()).item() <= 2.0 ** -8
+
+
+def test_binding_checks():
+    (Q, _), (K, _), (V, _) = problem(6, [8], [8], 4, 2, 64)
+    o = i32([0, 8])
+    ar.attention_packed(Q, K, V, o)
+    bad = [(Q.float(), K, V, o), (Q, K.half(), V, o), (Q[0], K, V, o), (Q, K, V[:4], o),
+           (Q[:, :3], K, V, o), (Q, K, V, o.long()), (Q, K, V, o.cpu()), (Q.cpu(), K, V, o),
+           (Q, K, V, o[None]), (Q[:4], K, V, o), (Q.transpose(0, 1), K, V, o),
+           (Q, K[..., ::2].repeat(1, 1, 2)[..., ::2], V, o), (Q, K, V, i32([]))]
+    for a in bad:
+        with pytest.raises(ValueError):
+            ar.attention_packed(*a)
+    odd = torch.zeros((8, 4 * 64 + 4), dtype=torch.bfloat16, device=dev())[:, :256].view(8, 4, 64)
+    for kw in (dict(out=torch.empty_like(Q)[:4]), dict(out=Q.float()), dict(k_offsets=i32([0])),
+               dict(stream=torch.cuda.Stream(device=0), out=Q.cpu())):
+        with pytest.raises(ValueError):
+            ar.attention_packed(Q, K, V, o, **kw)
+    with pytest.raises(ValueError):
+        ar.attention_packed(odd, K, V, o)
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ar.ArError):
+            ar.attention_packed(Q, K, V, o, scale=s)
+    e = ar.attention_packed(Q[:0], K[:0], V[:0], i32([0, 0]), want_lse=True)
+    assert e.out.shape == (0, 4, 64) and e.lse.shape == (0, 4)
+    assert ar.attention_packed(Q, K, V, i32([0])).out.shape == Q.shape

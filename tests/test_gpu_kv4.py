@@ -1,0 +1,348 @@
+"""The 4-bit cache: written and read back against the oracle bit for bit; attention over it
+against the oracle in float64 on the values that it holds."""
+import numpy as np
+import pytest
+import torch
+
+from attention_common import bf16, check, i32, keys, lse_bound, out_bound
+from gpu_common import dev, log
+from oracle import kv4_ref as R
+
+pytestmark = pytest.mark.gpu
+ar = pytest.importorskip("autoround_signsgd_rounding_amd")
+
+W_BITS = 2.0 ** -11      # weights are rounded to f16
+F32 = np.float32
+
+
+def arrays(pages, heads, D, P, group, fill=0xA5):
+    return (np.full((pages, 2, heads, P, D // 2), fill, np.uint8),
+            np.full((pages, 2, heads, P, D // group), 3.5, F32))
+
+
+def on_gpu(cache):
+    return ar.KV4Cache(*(torch.from_numpy(x).to(dev()) for x in cache))
+
+
+def same(got, want):
+    assert np.array_equal(got[0].cpu().numpy(), want[0])
+    assert np.array_equal(got[1].cpu().numpy().view(np.uint32), want[1].view(np.uint32))
+
+
+# ------------------------------------------------------------------ written and read
+SHAPES = [(1, 1, 64, 16, 64), (5, 2, 128, 32, 128), (77, 3, 64, 16, 32), (300, 2, 128, 64, 64),
+          (130, 1, 128, 128, 32), (33, 5, 64, 256, 32), (600, 8, 128, 64, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,heads,D,P,group", SHAPES)
+def test_write_and_read(T, heads, D, P, group, dtype):
+    """Codes and scales bit for bit, everything else as it was; values read back exactly."""
+    log(f"kv4 write {T} x {heads} x {D} page {P} group {group} {dtype}")
+    rng = np.random.default_rng(T)
+    pages = -(-T // P) + 2
+    k, v = keys(rng, T, heads, D).astype(F32), rng.normal(size=(T, heads, D)).astype(F32)
+    slots = rng.permutation(pages * P)[:T].astype(np.int32)
+    if T > 4:
+        slots[1], slots[3], slots[4] = -1, pages * P, -(1 << 31)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    K, V = (torch.from_numpy(x).to(dev()).to(dt) for x in (k, v))
+    want = arrays(pages, heads, D, P, group)
+    cache = on_gpu(want)
+    R.write(*want, K.float().cpu().numpy(), V.float().cpu().numpy(), slots)
+    assert ar.kv4_write(K, V, cache, i32(slots)) is None
+    same(cache, want)
+    for out in (torch.float32, torch.bfloat16):
+        for x, w in zip(ar.kv4_read(cache, i32(slots), out_dtype=out), R.held(*want, slots)):
+            assert x.dtype is out
+            assert torch.equal(x.cpu(), torch.from_numpy(w.astype(F32)).to(out))
+    # a slot may be read any number of times
+    twice = np.concatenate([slots[:2], slots[:2], slots[-1:]])
+    for x, w in zip(ar.kv4_read(cache, i32(twice), out_dtype=torch.float32), R.held(*want, twice)):
+        assert np.array_equal(x.cpu().numpy(), w.astype(F32))
+
+
+def test_grid_edges():
+    """Groups of zeros, of one sign, of one value, tiny, huge, halfway between codes, with NaN
+    and infinities."""
+    log("kv4 grid edges")
+    rows = []
+    add = lambda x: rows.append(np.resize(np.asarray(x, F32), 64))      # noqa: E731
+    for x in ([0.0], [-0.0], [1.0], [-2.5], [0.0, 15.0], [-15.0, 0.0], np.arange(16) - 7.0,
+              np.arange(32) / 2.0 - 7.5, [-1.0, 1.0], [1e-45], [1e-38, -1e-38], [2e-30, 1e-31],
+              [3.4e38], [1.7e38, -1.7e38], [3e38, -3e38], [np.nan], [1.0, np.nan], [np.inf, 1.0],
+              [-np.inf, 1.0], [np.inf, -np.inf], [2.0 ** -100, 2.0 ** -96], [1e-3, 1e3]):
+        add(x)
+    rng = np.random.default_rng(0)
+    for e in rng.uniform(-30, 37, 200):
+        add(rng.normal(size=64) * 10.0 ** e)
+    for s in 2.0 ** rng.integers(-90, 90, 200) * rng.integers(1, 1 << 20, 200):
+        add((rng.integers(0, 31, 64) / 2.0 - 7.5) * s)                  # halves of a step
+    x = np.stack(rows)[:, None]
+    want = arrays(len(x) // 16 + 1, 1, 64, 16, 32)
+    cache = on_gpu(want)
+    slots = np.arange(len(x), dtype=np.int32)
+    R.write(*want, x, x[::-1], slots)
+    X = torch.from_numpy(x).to(dev())
+    ar.kv4_write(X, X.flip(0).contiguous(), cache, i32(slots))
+    assert np.array_equal(cache.codes.cpu().numpy(), want[0])
+    a, b = cache.scale.cpu().numpy(), want[1]
+    assert np.array_equal(np.isnan(a), np.isnan(b))
+    assert np.array_equal(a[~np.isnan(a)].view(np.uint32), b[~np.isnan(b)].view(np.uint32))
+
+
+def test_strided_tokens_and_repeated_slots():
+    """Parts of one product; a slot named twice spoils itself only."""
+    log("kv4 strided")
+    rng = np.random.default_rng(2)
+    T, heads, D, P = 40, 2, 64, 16
+    qkv = torch.from_numpy(rng.normal(size=(T, 8, D)).astype(F32)).to(dev())
+    K, V = qkv[:, 4:6], qkv[:, 6:]
+    want = arrays(3, heads, D, P, 32)
+    cache = on_gpu(want)
+    slots = rng.permutation(48)[:T].astype(np.int32)
+    slots[9] = slots[7]
+    R.write(*want, K.cpu().numpy(), V.cpu().numpy(), slots)
+    ar.kv4_write(K, V, cache, i32(slots))
+    got = ar.kv4_read(cache, i32([s for s in range(48) if s != slots[7]]), out_dtype=torch.float32)
+    held = R.held(*want, [s for s in range(48) if s != slots[7]])
+    for g, w in zip(got, held):
+        assert np.array_equal(g.cpu().numpy(), w.astype(F32))
+
+
+def test_far_pages():
+    """A cache beyond 4 GiB: offsets of its last pages pass 32 bits."""
+    log("kv4 far pages")
+    pages, heads, D, P = 70000, 8, 128, 64
+    cache = ar.kv4_cache(pages, heads, D, page_size=P)
+    assert cache.codes.numel() > 1 << 32
+    rng = np.random.default_rng(1)
+    T = 100
+    (K, k), (V, v) = bf16(rng.normal(size=(T, heads, D))), bf16(rng.normal(size=(T, heads, D)))
+    last = pages * P - 1
+    slots = np.arange(last, last - T, -1)
+    ar.kv4_write(K, V, cache, i32(slots))
+    for g, x in zip(ar.kv4_read(cache, i32(slots), out_dtype=torch.float32), (k, v)):
+        c, s = R.grid(x, D)
+        w = (c - (s.view(np.uint32) & 15).astype(float)) * s
+        assert np.array_equal(g.cpu().numpy(), w.astype(F32))
+    # the sequence's tokens in order are those of the last pages backwards, token by token
+    order = slots.reshape(-1)[::-1] // P
+    table = i32(np.unique(order)[None])
+    n = int(last - np.unique(order)[0] * P + 1)
+    q, qv = bf16(rng.normal(size=(1, 8, D)))
+    got = ar.kv4_attention(q, cache, table, i32([n]), want_lse=True)
+    first = np.unique(order)[0] * P
+    kk, vv = (x.double().cpu().numpy() for x in
+              ar.kv4_read(cache, i32(np.arange(first, last + 1)), out_dtype=torch.float32))
+    compare(got, qv[:, None], [kk], [vv], 1, "far")
+    del cache
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ attention
+def compare(got, q, ks, vs, new, what, scale=None, gone=None):
+    """kv4_attention's outputs against the oracle's: q [B, new, H, D]; ks, vs [n, heads, D] of
+    each sequence; gone: keys of each sequence that take no part."""
+    B, _, H, D = q.shape
+    out, lse = got.out.double().cpu().numpy().reshape(q.shape), got.lse.cpu().numpy().reshape(B, new, H)
+    for b in range(B):
+        n, r = len(ks[b]), H // ks[b].shape[1]
+        sees = R.causal(new, n)
+        if gone is not None:
+            sees = sees & ~gone[b][None]
+        for h in range(H):
+            o, l, size, mag = R.rows(q[b, :, h], ks[b][:, h // r], vs[b][:, h // r], sees,
+                                     D ** -0.5 if scale is None else scale)
+            empty = np.isneginf(l)
+            assert (np.isneginf(lse[b, :, h]) == empty).all() and (out[b, empty, h] == 0).all()
+            # weights below 2^-32 of the largest may vanish
+            top = np.abs(vs[b][:, h // r]).max() if n else 0.0
+            bound = out_bound(o, size, mag, D, n, W_BITS) + n * 2.0 ** -32 * 2 * top
+            check(out[b, :, h], o, bound, f"{what}: out {b} {h}")
+            check(lse[b, ~empty, h], l[~empty], lse_bound(l, mag, D, n)[~empty], f"{what}: lse {b} {h}")
+
+
+def filled(rng, lengths, heads, D, P, group, spare=2):
+    """A cache in which the sequences' pages lie anywhere, every other place holding NaN
+    scales, and what it holds for each."""
+    per = [-(-n // P) for n in lengths]
+    pages = sum(per) + spare
+    order = rng.permutation(pages)
+    width = max(max(per), 1) + 1
+    table = np.full((len(lengths), width), -1, np.int32)
+    cache = ar.kv4_cache(pages, heads, D, page_size=P, group_size=group, device=dev())
+    cache.codes.fill_(0x3C)
+    cache.scale.fill_(float("nan"))
+    ks, vs, at = [], [], 0
+    for b, n in enumerate(lengths):
+        mine = order[at:at + per[b]]
+        at += per[b]
+        table[b, :per[b]] = mine
+        t = np.arange(n)
+        slots = mine[t // P] * P + t % P if n else np.zeros(0, int)
+        K, V = bf16(keys(rng, n, heads, D))[0], bf16(rng.normal(size=(n, heads, D)))[0]
+        ar.kv4_write(K, V, cache, i32(slots))
+        k, v = ar.kv4_read(cache, i32(slots), out_dtype=torch.float32)
+        ks.append(k.double().cpu().numpy())
+        vs.append(v.double().cpu().numpy())
+    return cache, i32(table), ks, vs
+
+
+CASES = [  # lengths, new, heads, key heads, head_dim, page, group
+    ([1], 1, 1, 1, 64, 16, 64),
+    ([1, 15, 16, 17, 31, 32, 33], 1, 4, 2, 128, 16, 128),
+    ([100], 1, 8, 8, 128, 64, 128),
+    ([129, 500, 7], 1, 16, 2, 64, 32, 32),
+    ([1000], 1, 8, 1, 128, 128, 64),
+    ([257, 1300], 1, 6, 2, 128, 16, 32),
+    ([90, 40], 5, 14, 2, 64, 16, 32),
+    ([300, 3, 65], 4, 8, 1, 128, 64, 128),          # 32 rows; a sequence shorter than the draft
+    ([600], 8, 8, 1, 128, 32, 64),                  # 64 rows
+    ([77, 0, 5], 1, 4, 1, 64, 16, 64),              # a sequence without tokens
+    ([2, 0], 3, 2, 2, 128, 64, 32),
+    ([50], 1, 256, 1, 64, 16, 32),                  # the largest group
+    ([260], 3, 17, 1, 128, 256, 128),
+]
+
+
+@pytest.mark.parametrize("lengths,new,H,heads,D,P,group", CASES)
+def test_attention(lengths, new, H, heads, D, P, group):
+    log(f"kv4 attention {lengths} new {new} heads {H}/{heads} x {D} page {P} group {group}")
+    rng = np.random.default_rng(sum(lengths) + H)
+    cache, table, ks, vs = filled(rng, lengths, heads, D, P, group)
+    Q, q = bf16(1.5 * rng.normal(size=(len(lengths), new, H, D)))
+    got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+    torch.cuda.synchronize()
+    compare(got, q, ks, vs, new, "kv4")
+    bare = ar.kv4_attention(Q, cache, table, i32(lengths))
+    assert bare.lse is None and torch.equal(bare.out, got.out)
+    if new == 1:
+        flat = ar.kv4_attention(Q[:, 0], cache, table, i32(lengths))
+        assert flat.out.shape == (len(lengths), H, D) and torch.equal(flat.out, got.out[:, 0])
+
+
+@pytest.mark.parametrize("H,heads,new,group", [(8, 1, 1, 128), (32, 8, 1, 64), (4, 2, 3, 32)])
+def test_long_sequences(H, heads, new, group):
+    """Several workgroups share a sequence; neighbours are short."""
+    log(f"kv4 long {H}/{heads} new {new} group {group}")
+    rng = np.random.default_rng(H)
+    lengths = [9001, 3, 4096, 700]
+    cache, table, ks, vs = filled(rng, lengths, heads, 128, 64, group)
+    Q, q = bf16(1.5 * rng.normal(size=(4, new, H, 128)))
+    got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+    compare(got, q, ks, vs, new, "long")
+    # a bound on the lengths divides the work otherwise; a longer one is cut to it
+    tight = ar.kv4_attention(Q, cache, table, i32(lengths), max_len=9001, want_lse=True)
+    compare(tight, q, ks, vs, new, "bounded")
+    cut = ar.kv4_attention(Q, cache, table, i32(lengths), max_len=1000, want_lse=True)
+    compare(cut, q, [k[:1000] for k in ks], [v[:1000] for v in vs], new, "cut")
+
+
+def test_pages_that_are_not_there():
+    """Pages outside the cache take no part: -1, beyond it, all of a sequence's."""
+    log("kv4 pages that are not there")
+    rng = np.random.default_rng(4)
+    for P in (16, 32):
+        lengths, H, heads, D = [300, 200, 90], 4, 2, 64
+        cache, table, ks, vs = filled(rng, lengths, heads, D, P, 32)
+        table[0, 3], table[0, 4], table[0, 0] = -1, cache.codes.shape[0], 1 << 30
+        table[2] = -(1 << 31)
+        gone = [np.isin(np.arange(300) // P, [0, 3, 4]), np.zeros(200, bool), np.ones(90, bool)]
+        Q, q = bf16(rng.normal(size=(3, 2, H, D)))
+        got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+        compare(got, q, ks, vs, 2, f"gone {P}", gone=gone)
+        # lengths outside the table
+        Q1 = Q[:, :1]
+        a = ar.kv4_attention(Q1, cache, table, i32([-5, 1 << 30, -(1 << 31)]), want_lse=True)
+        assert (a.out[0] == 0).all() and torch.isneginf(a.lse[0]).all()
+        n = table.shape[1] * P
+        there = table[1].cpu().numpy()[np.arange(n) // P] >= 0
+        if there[200:].any():       # the tail of its last page holds NaN
+            assert torch.isnan(a.out[1]).all()
+
+
+def test_hidden_nan_and_seen_nan():
+    """A cached NaN makes the rows that see it NaN; the draft's earlier rows do not see it."""
+    log("kv4 nan")
+    rng = np.random.default_rng(6)
+    H, heads, D, P, n = 4, 2, 128, 16, 70
+    cache, table, ks, vs = filled(rng, [n], heads, D, P, 64)
+    slot = int(table[0, (n - 1) // P]) * P + (n - 1) % P
+    K = torch.ones((1, heads, D), device=dev())
+    for which in (0, 1):
+        kv = [K.clone(), K.clone()]
+        kv[which][0, 1, 70] = float("nan")
+        ar.kv4_write(*kv, cache, i32([slot]))
+        Q, q = bf16(rng.normal(size=(1, 3, H, D)))
+        got = ar.kv4_attention(Q, cache, table, i32([n]), want_lse=True)
+        assert torch.isfinite(got.out[0, :2]).all() and torch.isfinite(got.out[0, 2, :2]).all()
+        hit = got.out[0, 2, 2:]
+        assert torch.isnan(hit[..., 64:]).all()
+        assert torch.isnan(hit[..., :64]).all() == (which == 0)
+
+
+def test_extremes():
+    """Queries and values at the ends of bf16's range, sharp and flat rows, tiny values."""
+    log("kv4 extremes")
+    rng = np.random.default_rng(8)
+    H, heads, D, P, n = 8, 2, 64, 32, 150
+    for qs, ks_, vs_ in ((1e30, 1e-30, 1e30), (1e-36, 1.0, 1e-25), (40.0, 4.0, 1e-6), (0.0, 1.0, 1e6)):
+        cache = ar.kv4_cache(8, heads, D, page_size=P, group_size=32)
+        slots = i32(np.arange(n))
+        K, V = bf16(ks_ * keys(rng, n, heads, D))[0], bf16(vs_ * rng.normal(size=(n, heads, D)))[0]
+        V[5] *= 100
+        ar.kv4_write(K, V, cache, slots)
+        k, v = (x.double().cpu().numpy() for x in ar.kv4_read(cache, slots, out_dtype=torch.float32))
+        Q, q = bf16(qs * rng.normal(size=(1, 1, H, D)))
+        got = ar.kv4_attention(Q, cache, i32(np.arange(8)[None]), i32([n]), want_lse=True)
+        compare(got, q, [k], [v], 1, f"extremes {qs}")
+        got = ar.kv4_attention(Q, cache, i32(np.arange(8)[None]), i32([n]), want_lse=True, scale=0.02)
+        compare(got, q, [k], [v], 1, f"extremes {qs}, scale", scale=0.02)
+
+
+def test_given_outputs_and_workspace():
+    log("kv4 given outputs")
+    rng = np.random.default_rng(3)
+    cache, table, ks, vs = filled(rng, [3000, 50], 2, 128, 64, 128)
+    qkv, x = bf16(rng.normal(size=(2, 12, 128)))      # q beside k and v
+    Q, out = qkv[:, :8], torch.empty((2, 8, 128), dtype=torch.bfloat16, device=dev())
+    ws = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=dev())     # NaN all over
+    got = ar.kv4_attention(Q, cache, table, i32([3000, 50]), out=out, workspace=ws, want_lse=True)
+    assert got.out is out
+    compare(got, x[:, None, :8], ks, vs, 1, "given")
+    with pytest.raises(ar.ArError, match="WORKSPACE"):
+        ar.kv4_attention(Q, cache, table, i32([3000, 50]), workspace=ws[:1024])
+
+
+def test_binding_checks():
+    cache = ar.kv4_cache(4, 2, 64, page_size=16, group_size=32)
+    K, s = torch.zeros((5, 2, 64), dtype=torch.bfloat16, device=dev()), i32(range(5))
+    ar.kv4_write(K, K, cache, s)
+    for a in ((K[..., :32], K, s), (K, K.float(), s), (K, K[:4], s), (K, K, s.long()), (K, K, s[:3]),
+              (K, K, s.cpu()), (K.half(), K.half(), s), (K[:, :1], K[:, :1], s), (None, K, s)):
+        with pytest.raises(ValueError):
+            ar.kv4_write(a[0], a[1], cache, a[2])
+    for bad in ((cache.codes, cache.scale[:2]), (cache.codes.int(), cache.scale),
+                (cache.codes, cache.scale.double()), (cache.codes, cache.scale.cpu()),
+                (cache.codes[:, :, :1], cache.scale[:, :, :1]), (cache.codes[:, :1], cache.scale[:, :1])):
+        with pytest.raises(ValueError):
+            ar.kv4_read(bad, s)
+    with pytest.raises(TypeError):
+        ar.kv4_read(cache, s, out_dtype=torch.float16)
+    Q, t, n = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=dev()), i32([[0, 1], [2, 3]]), i32([3, 9])
+    ar.kv4_attention(Q, cache, t, n)
+    for a in ((Q.float(), t, n), (Q[:, :3], t, n), (Q, t[:1], n), (Q, t, n[:1]), (Q, t.long(), n),
+              (Q, t, n.float()), (Q[..., :32], t, n), (Q.transpose(0, 1), t, n), (Q[None, None], t, n),
+              (torch.zeros((4, 2, 4, 64), dtype=torch.bfloat16, device=dev()).transpose(0, 1), t, n)):
+        with pytest.raises(ValueError):
+            ar.kv4_attention(a[0], cache, a[1], a[2])
+    for kw in (dict(max_len=33), dict(max_len=-1), dict(scale=0.0), dict(scale=float("nan"))):
+        with pytest.raises(ar.ArError):
+            ar.kv4_attention(Q, cache, t, n, **kw)
+    # nothing to do
+    assert ar.kv4_attention(Q[:0], cache, t[:0], n[:0]).out.shape == (0, 4, 64)
+    ar.kv4_write(K[:0], K[:0], cache, s[:0])
+    assert ar.kv4_read(cache, s[:0])[0].shape == (0, 2, 64)
+    none = ar.kv4_attention(Q, cache, t[:, :0].contiguous(), n, want_lse=True)
+    assert (none.out == 0).all() and torch.isneginf(none.lse).all()

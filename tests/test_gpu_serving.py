@@ -1,0 +1,191 @@
+"""The attention operators together as a decoder layer uses them: a prompt taken whole and in
+chunks, its tokens written to the 4-bit cache, then token by token from there; the same under
+graph capture, on streams of their own, and beside the e4m3 product."""
+import numpy as np
+import pytest
+import torch
+
+from attention_common import bf16, check, i32, keys, out_bound
+from gpu_common import dev, log
+from oracle import kv4_ref as R
+
+pytestmark = pytest.mark.gpu
+ar = pytest.importorskip("autoround_signsgd_rounding_amd")
+
+H, HK, D, P = 8, 2, 128, 32
+
+
+def qkv(rng, T):
+    x = np.concatenate([1.5 * rng.normal(size=(T, H, D)), keys(rng, T, HK, D),
+                        rng.normal(size=(T, HK, D))], 1)
+    return bf16(x)
+
+
+def parts(x):
+    return x[:, :H], x[:, H:H + HK], x[:, H + HK:]
+
+
+def test_prompt_chunks_and_tokens():
+    """Prefill of two prompts, the second in chunks whose prefix is read back from the cache;
+    then five tokens each, all against the oracle on the values that each step sees."""
+    log("serving chain")
+    rng = np.random.default_rng(0)
+    lens, cache = [70, 45], ar.kv4_cache(12, HK, D, page_size=P)
+    table = i32([[3, 7, 1, 9], [0, 11, 4, 2]])
+    place = lambda b, t: [int(table[b, i // P]) * P + i % P for i in t]        # noqa: E731
+    X, x = qkv(rng, sum(lens))
+    q, k, v = parts(X)
+    r = ar.attention_packed(q, k, v, i32([0, 70, 115]))
+    ar.kv4_write(k, v, cache, i32(place(0, range(70)) + place(1, range(45))))
+    # the second prompt again, its last 20 tokens behind what the cache holds of the first 25
+    pk, pv = ar.kv4_read(cache, i32(place(1, range(25))))
+    kk, vv = torch.cat([pk, k[95:]]), torch.cat([pv, v[95:]])
+    chunk = ar.attention_packed(q[95:], kk, vv, i32([0, 20]), k_offsets=i32([0, 45]))
+    for got, rows, K, V in ((r.out[:70], slice(0, 70), x[:70, H:H + HK], x[:70, H + HK:]),
+                            (r.out[70:], slice(70, 115), x[70:, H:H + HK], x[70:, H + HK:]),
+                            (chunk.out, slice(95, 115), kk.double().cpu().numpy(),
+                             vv.double().cpu().numpy())):
+        nq = rows.stop - rows.start
+        for h in range(H):
+            o, _, size, mag = R.rows(x[rows, h], K[:, h // 4], V[:, h // 4], R.causal(nq, len(K)),
+                                     D ** -0.5)
+            check(got[:, h].double().cpu().numpy(), o, out_bound(o, size, mag, D, len(K), 2.0 ** -8),
+                  "prompt")
+    lengths = i32(lens)
+    for step in range(5):
+        X, x = qkv(rng, 2)
+        q, k, v = parts(X)
+        ar.kv4_write(k, v, cache, i32(place(0, [lens[0] + step]) + place(1, [lens[1] + step])))
+        lengths += 1
+        got = ar.kv4_attention(q, cache, table, lengths)
+        for b in range(2):
+            K, V = (t.double().cpu().numpy() for t in
+                    ar.kv4_read(cache, i32(place(b, range(lens[b] + step + 1))),
+                                out_dtype=torch.float32))
+            for h in range(H):
+                o, _, size, mag = R.rows(x[b:b + 1, h], K[:, h // 4], V[:, h // 4],
+                                         np.ones((1, len(K)), bool), D ** -0.5)
+                check(got.out[b:b + 1, h].double().cpu().numpy(), o,
+                      out_bound(o, size, mag, D, len(K), 2.0 ** -11) + 1e-6, f"step {step}")
+
+
+def test_layer_between_products():
+    """Between a q|k|v product and an o product in e4m3."""
+    log("serving layer")
+    rng = np.random.default_rng(1)
+    T, hidden = 33, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    w = 0.05 * torch.randn(((H + 2 * HK) * D, hidden), generator=g, device=dev())
+    wo = 0.05 * torch.randn((hidden, H * D), generator=g, device=dev())
+    h = torch.randn((T, hidden), generator=g, device=dev()).to(torch.bfloat16)
+    X = ar.fp8_gemm(*ar.fp8_quant_act(h), *ar.fp8_quant_weight(w)).view(T, H + 2 * HK, D)
+    q, k, v = parts(X)
+    cache, slots = ar.kv4_cache(2, HK, D, page_size=P), torch.arange(T, dtype=torch.int32, device=dev())
+    a = ar.attention_packed(q, k, v, i32([0, T])).out
+    ar.kv4_write(k, v, cache, slots)
+    last = ar.kv4_attention(q[-1:], cache, i32([[0, 1]]), i32([T])).out
+    y = ar.fp8_gemm(*ar.fp8_quant_act(a.view(T, H * D)), *ar.fp8_quant_weight(wo))
+    assert torch.isfinite(y).all()
+    # the last token from the cache: 4 bits of each key and value away from the prompt's
+    a, last = a[-1].double(), last[0].double()
+    assert ((a - last).norm() / a.norm()).item() < 0.5
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_graph(long):
+    """Write, attend and attend again in one graph, replayed with other tokens, lengths and
+    pages, with eager calls between the replays."""
+    log(f"serving graph long={long}")
+    rng = np.random.default_rng(2)
+    B, width = 3, 64 if long else 2
+    cache = ar.kv4_cache(B * width + 1, HK, D, page_size=P)
+    fill = i32(np.arange((B * width + 1) * P))
+    X, _ = qkv(rng, (B * width + 1) * P)
+    ar.kv4_write(*parts(X)[1:], cache, fill)
+    X, slots, lengths = qkv(rng, B)[0], i32([1, 2, 3]), i32([1, 1, 1])
+    table = i32(np.zeros((B, width)))
+    po, ko = i32([0, 1, 2, 3]), i32([0, 0, 0, 0])
+
+    def step():
+        q, k, v = parts(X)
+        ar.kv4_write(k, v, cache, slots)
+        a = ar.kv4_attention(q, cache, table, lengths, want_lse=True)
+        b = ar.attention_packed(q, k, v, po, want_lse=True)
+        return [*a, *b, *ar.kv4_read(cache, slots)]
+
+    step()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        with torch.cuda.graph(graph, stream=s):
+            captured = step()
+    torch.cuda.current_stream().wait_stream(s)
+    for i in range(4):
+        X.copy_(qkv(rng, B)[0])
+        order = rng.permutation(B * width + 1)[:B * width].reshape(B, width)
+        table.copy_(i32(order))
+        n = rng.integers(1, width * P, B)
+        lengths.copy_(i32(n))
+        slots.copy_(i32([order[b, (n[b] - 1) // P] * P + (n[b] - 1) % P for b in range(B)]))
+        po.copy_(i32([[0, 1, 2, 3], [0, 3, 3, 3], [0, 0, 1, 3], [0, 1, 1, 2]][i]))
+        for t in captured[2:4]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        want = step()
+        last = int(po[-1])
+        want[2], got[2], want[3], got[3] = want[2][:last], got[2][:last], want[3][:last], got[3][:last]
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_streams():
+    """The same calls on two streams at once, each with outputs and workspace of its own, and
+    on a stream that is not the current one."""
+    log("serving streams")
+    rng = np.random.default_rng(3)
+    pages = 200
+    cache = ar.kv4_cache(pages, HK, D, page_size=P)
+    X, _ = qkv(rng, pages * P)
+    q, k, v = parts(X)
+    ar.kv4_write(k, v, cache, i32(np.arange(pages * P)))
+    tables = [i32(rng.permutation(pages)[None]) for _ in range(2)]
+    n = i32([pages * P - 5])
+    want = [ar.kv4_attention(q[i:i + 1], cache, tables[i], n).out for i in range(2)]
+    prompt = ar.attention_packed(q, k, v, i32([0, 1000, pages * P])).out
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    off = i32([0, 1000, pages * P])
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(ar.kv4_attention(q[i:i + 1], cache, tables[i], n, stream=s).out)
+            if i:
+                with torch.cuda.stream(s):
+                    got[i].append(ar.attention_packed(q, k, v, off).out)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o, want[i] if o.shape == want[i].shape else prompt)
+
+
+def test_same_bits_every_time():
+    log("serving same bits")
+    rng = np.random.default_rng(4)
+    cache = ar.kv4_cache(300, HK, D, page_size=P)
+    X, _ = qkv(rng, 300 * P)
+    q, k, v = parts(X)
+    ar.kv4_write(k, v, cache, i32(np.arange(300 * P)))
+    table, n = i32(np.arange(300)[None]), i32([300 * P])
+    first = ar.kv4_attention(q[:1], cache, table, n, want_lse=True)
+    chunk = ar.attention_packed(q[:40], k, v, i32([0, 40]), k_offsets=i32([0, 300 * P]))
+    for _ in range(5):
+        again = ar.kv4_attention(q[:1], cache, table, n, want_lse=True)
+        assert torch.equal(first.out, again.out) and torch.equal(first.lse, again.lse)
+        c = ar.attention_packed(q[:40], k, v, i32([0, 40]), k_offsets=i32([0, 300 * P]))
+        assert torch.equal(chunk.out, c.out)
