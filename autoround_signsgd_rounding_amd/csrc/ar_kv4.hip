@@ -3,7 +3,7 @@
 //
 // A group of g channels of a token's head (g = 32, 64 or 128) has the asymmetric integer
 // grid of the weights' quantizer at alpha = beta = 1, in float32, each step rounded once:
-//   lo = min(x, 0), hi = max(x, 0);   s = (hi - lo)/15, 1 where that is 0, never below 2^-100
+//   lo = min(x, 0), hi = max(x, 0);   s = max((hi - lo)/15, 2^-100)
 //   zp = clamp(rint(-lo/s), 0, 15);   s' = s with its four lowest bits replaced by zp
 //   code = clamp(rint(x/s') + zp, 0, 15);   value s'·(code - zp)
 // s' is off s by 15·2^-23 at most, 1/70000 of the half step that a code is rounded by,
@@ -24,8 +24,7 @@ struct Grid4 {
 };
 __device__ __forceinline__ Grid4 grid_of(float lo, float hi) {
   const float d = hi - lo;
-  float s = d / 15.0f;
-  s = d == 0.0f ? 1.0f : fmaxf(s, 0x1p-100f);
+  const float s = fmaxf(d / 15.0f, 0x1p-100f);
   const float zp = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
   Grid4 g;
   g.zp = zp;

@@ -13,7 +13,7 @@ def grid(x, group):
         lo = np.minimum(g.min(-1), F32(0))
         hi = np.maximum(g.max(-1), F32(0))
         d = hi - lo
-        s = np.where(d == 0, F32(1), np.maximum(d / F32(15), F32(2.0 ** -100)))
+        s = np.maximum(d / F32(15), F32(2.0 ** -100))
         zp = np.clip(np.rint(-lo / s), 0, 15)
         ok = np.isfinite(d)
         bits = (s.astype(F32).view(np.uint32) & ~np.uint32(15)) | np.where(ok, zp, 0).astype(np.uint32)

@@ -156,11 +156,23 @@ def compare(got, q, ks, vs, new, what, scale=None, gone=None):
                                      D ** -0.5 if scale is None else scale)
             empty = np.isneginf(l)
             assert (np.isneginf(lse[b, :, h]) == empty).all() and (out[b, empty, h] == 0).all()
-            # weights below 2^-32 of the largest may vanish
-            top = np.abs(vs[b][:, h // r]).max() if n else 0.0
-            bound = out_bound(o, size, mag, D, n, W_BITS) + n * 2.0 ** -32 * 2 * top
+            if n == 0:
+                continue
+            # what the matrix unit cuts off, with scales of a token's keys or values of at most a
+            # seventh of their largest: of a score, 2^-17 of scale times max |q| a channel; of
+            # a value's product and its zero-point's, 2^-14 of the largest of 8 weights each
+            ktop = np.abs(ks[b][:, h // r]).max(1) / 7
+            vtop = np.abs(vs[b][:, h // r]).max(1) / 7
+            sc = D ** -0.5 if scale is None else scale
+            cut = D * 2.0 ** -17 * np.abs(q[b, :, h]).max(1) * sc * ktop.max()
+            weight = np.stack([R.rows(q[b, i:i + 1, h], ks[b][:, h // r], vtop[:, None],
+                                      sees[i:i + 1], sc)[0][0] for i in range(new)])
+            # weights below 2^-30 of the largest may vanish
+            bound = out_bound(o, size, mag, D, n, W_BITS) + size * 2 * np.expm1(cut)[:, None] + \
+                2.0 ** -10 * weight + n * 2.0 ** -30 * 8 * vtop.max()
             check(out[b, :, h], o, bound, f"{what}: out {b} {h}")
-            check(lse[b, ~empty, h], l[~empty], lse_bound(l, mag, D, n)[~empty], f"{what}: lse {b} {h}")
+            bound = lse_bound(l, mag, D, n) + cut
+            check(lse[b, ~empty, h], l[~empty], bound[~empty], f"{what}: lse {b} {h}")
 
 
 def filled(rng, lengths, heads, D, P, group, spare=2):

@@ -20,7 +20,7 @@ def test_grid_by_hand():
     c, s = R.grid(np.linspace(5, 20, 32, dtype=F32)[None], 32)
     assert (s.view(np.uint32) & 15).item() == 0 and c.min() == 4 and c.max() == 15
     # zeros, tiny values
-    assert R.grid(np.zeros((1, 32)), 32)[1].item() == 1.0
+    assert R.grid(np.zeros((1, 32)), 32)[1].item() == 2.0 ** -100
     c, s = R.grid(np.full((1, 32), 1e-40), 32)
     assert s.item() == 2.0 ** -100 and c.max() == 0
 
