@@ -87,64 +87,34 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
-// 32 tokens' keys and values as they lie in memory: a lane takes its channels of one key
-// token in each half j of the tile, and the values of its octet.
+// 32 tokens of a key head in LDS, as they lie in memory: codes of the keys, of the values,
+// scales of the keys, of the values.
 template <int DH, int GS>
-struct Keys {
-  static constexpr int G = DH / GS, KW = GS / 32;
-  uint32_t k[2][G][KW];
-  float zero[2][G];   // that token's scales, for their zero-points
-  float s[8][G];      // scales of the octet
+struct Tile {
+  static constexpr int G = DH / GS, CODES = 16 * DH, SCALES = 128 * G;
+  static constexpr int BYTES = 2 * (CODES + SCALES), LOADS = 2 * (CODES / 1024) + G;
 };
-template <int DH, int GS>
-struct Values {
-  static constexpr int G = DH / GS, NB = DH / 64;
-  u32x4_t v[NB];
-  float s[8][G];
-};
-template <int G>
-__device__ __forceinline__ void load_scales(const float* p, float (&s)[8][G]) {
+// Scales of groups g .. g + N - 1 of an octet (p: those of its first token).
+template <int G, int N>
+__device__ __forceinline__ void octet_scales(const float* p, int g, float (&s)[N][8]) {
+  if constexpr (N == G) {
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
-    const f32x4_t w = reinterpret_cast<const f32x4_t*>(p)[i];
+    for (int i = 0; i < 2 * G; ++i) {
+      const f32x4_t w = reinterpret_cast<const f32x4_t*>(p)[i];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[(4 * i + e) / G][(4 * i + e) % G] = w[e];
-  }
-}
-// p + at: the lane's codes of its token in half 0 of the tile, which is four tokens before
-// that in half 1; s + az that token's scales, s + as those of the octet.
-template <int DH, int GS>
-__device__ __forceinline__ void load_keys(Keys<DH, GS>& x, const uint8_t* p, uint32_t at,
-                                          const float* s, uint32_t az, uint32_t as) {
-  constexpr int G = DH / GS, KW = GS / 32;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint8_t* w = p + (at + (uint32_t)(j * 4 * (DH / 2) + g * (GS / 2)));
-      if constexpr (KW == 4) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.k[j][g][i] = v[i];
-      } else if constexpr (KW == 2) {
-        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(w);
-        x.k[j][g][0] = v[0];
-        x.k[j][g][1] = v[1];
-      } else {
-        x.k[j][g][0] = *reinterpret_cast<const uint32_t*>(w);
-      }
-      x.zero[j][g] = s[az + (uint32_t)(j * 4 * G + g)];
+      for (int e = 0; e < 4; ++e) s[(4 * i + e) % G][(4 * i + e) / G] = w[e];
     }
-  }
-  load_scales<G>(s + as, x.s);
-}
-template <int DH, int GS>
-__device__ __forceinline__ void load_values(Values<DH, GS>& x, const uint8_t* p, uint32_t at,
-                                            const float* s, uint32_t as) {
+  } else {
 #pragma unroll
-  for (int b = 0; b < DH / 64; ++b)
-    x.v[b] = *reinterpret_cast<const u32x4_t*>(p + (at + (uint32_t)(b * 256)));
-  load_scales<DH / GS>(s + as, x.s);
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i][e] = p[e * G + g + i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  asm volatile("" ::: "memory");
 }
 
 // Sum over a wave, inclusive of the lane's own and from lane 0 on.
@@ -240,12 +210,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int a
 // Waves a SIMD that the registers are held to. (From two on, products stay out of the
 // accumulation registers, which the softmax would have to copy from.)
 constexpr int occupancy(int DH, int G, int RT, int WAVES) {
-  return WAVES == 8 || DH + RT * G == 130 ? 2
-         : DH == 64                         ? (RT == 2 ? 2 : G == 1 ? 4 : 3)
-                                            : (G * RT == 1 ? 3 : 1);
+  return WAVES == 8 || RT == 2 ? 2 : DH == 64 ? 4 : G == 4 ? 2 : 3;
 }
 
-template <int DH, int GS, int RT, int WAVES>
+template <int DH, int GS, int RT, int WAVES, int STAGES>
 __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void k_kv4_attention(AttnArgs a) {
   constexpr int G = DH / GS, KW = GS / 32, NB = DH / 64, NO = DH / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -266,29 +234,88 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     last = min(len, first + d.chunk);
   }
 
-  // the lane's row of each of the RT products, its queries and what it sees
-  f16x8_t qf[RT][G][KW], qz[RT][G];
-  float qs[RT];        // takes a sum of products to the exponent of 2
+  // the lane's row of each of the RT products and its queries
+  u32x4_t qraw[RT][G][KW];
   int sees[RT];        // keys before this one
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int row = (tile * RT + t) * 16 + n, i = row / a.ratio;
-    const bool live = row < a.rows;
     const uint16_t* p = a.q + ((int64_t)b * a.news + i) * a.q_stride +
                         (h * a.ratio + row - i * a.ratio) * DH;
-    sees[t] = live ? len - a.news + 1 + i : 0;
+    sees[t] = row < a.rows ? len - a.news + 1 + i : 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        qraw[t][g][k] = u32x4_t{0u, 0u, 0u, 0u};
+        if (row < a.rows)
+          qraw[t][g][k] = *reinterpret_cast<const u32x4_t*>(p + g * GS + g4 * (GS / 4) + 8 * k);
+      }
+  }
+
+  // (read through the scalar cache: a wait for an entry is then none for the loads before it)
+  typedef __attribute__((address_space(4))) const int32_t* table_t;
+  const table_t tab = (table_t)(a.table + (int64_t)b * a.width);
+  const int npages = (int)a.c.pages;
+  auto page_of = [&](int t) {   // page of token t, -1 where there is none
+    const int e = t >> a.c.shift;
+    const int p = e < a.width ? tab[e] : -1;
+    return (uint32_t)p < (uint32_t)npages ? p : -1;
+  };
+  const int ktok = 8 * (n >> 2) + (n & 3), vtok = 8 * g4;   // the lane's tokens in a tile
+  using Tl = Tile<DH, GS>;
+  constexpr int R = 16 * RT, LD = DH + 4, RING = STAGES * Tl::BYTES;
+  constexpr int JOIN = WAVES * R * (LD + 2) * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * RING > JOIN ? WAVES * RING : JOIN];
+  uint8_t* const ring = lds + wave * RING;
+
+  // the tile at token t, whose halves lie in pages p0 and p1 (any page stands in for none),
+  // straight to LDS: each load 1 KiB of codes or 256 bytes of scales
+  const int64_t page_rows = (int64_t)2 * Hk * a.c.page, head_row = (int64_t)h * a.c.page;
+  const int64_t to_values = (int64_t)Hk * a.c.page;
+  auto fetch = [&](int t, int p0, int p1, uint8_t* to) {
+    typedef __attribute__((address_space(1))) const void* from_t;
+    typedef __attribute__((address_space(3))) void* to_t;
+    const int in = t & (a.c.page - 1);
+    const int64_t row0 = max(p0, 0) * page_rows + head_row + in;
+    // (with pages of 16 the second half begins a page of its own)
+    const int64_t more = a.c.page == 16 ? (max(p1, 0) - max(p0, 0)) * page_rows - 16 : 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < Tl::CODES / 1024; ++i) {
+        const int at = i * 1024 + lane * 16;
+        const uint8_t* p = a.c.codes + (row0 + w * to_values) * (DH / 2);
+        if (a.c.page == 16 && at >= 8 * DH) p += more * (DH / 2);
+        __builtin_amdgcn_global_load_lds((from_t)(p + (uint32_t)at),
+                                         (to_t)(to + w * Tl::CODES + i * 1024), 16, 0, 0);
+      }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int at = i * 64 + lane, w = at / (32 * G), k = at - w * 32 * G;
+      const float* p = a.c.scale + row0 * G;
+      if (G == 1 ? w != 0 : 2 * i >= G) p += to_values * G;
+      if (a.c.page == 16 && k >= 16 * G) p += more * G;
+      __builtin_amdgcn_global_load_lds((from_t)(p + (uint32_t)k), (to_t)(to + 2 * Tl::CODES + i * 256),
+                                       4, 0, 0);
+    }
+  };
+  f16x8_t qf[RT][G][KW], qz[RT][G];
+  float qs[RT];        // takes a sum of products to the exponent of 2
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
     float x[G][KW][8];
     uint32_t top = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int k = 0; k < KW; ++k) {
+      for (int k = 0; k < KW; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[g][k][e] = 0.0f;
-        if (live) load8(p + g * GS + g4 * (GS / 4) + 8 * k, x[g][k]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[g][k][e]) & 0x7FFFFFFFu);
-      }
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = qraw[t][g][k][e / 2], f = e & 1 ? w & 0xFFFF0000u : w << 16;
+          x[g][k][e] = __uint_as_float(f);
+          top = max(top, f & 0x7FFFFFFFu);
+        }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     const float big = __uint_as_float(top);
@@ -319,6 +346,17 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     }
   }
 
+  // STAGES tiles on their way, and the pages of those that are not yet worked on
+  constexpr int STEP = 32 * WAVES, LOADS = Tl::LOADS;
+  const int t0 = first + 32 * wave;
+  int p0[STAGES], p1[STAGES];
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) {
+    const int t = t0 + i * STEP;
+    p0[i] = page_of(t), p1[i] = page_of(t + 16);
+    if (t < last) fetch(t, p0[i], p1[i], ring + i * Tl::BYTES);
+  }
+
   f32x4_t o[RT][NO];
   // what the values' zero-points take off, in every element (a group's own, so that a NaN
   // stays within it)
@@ -336,53 +374,20 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
   for (int g = 0; g < G; ++g) sv[g] = 0x1p-120f, wk[g] = W_TOP * 0x1p120f;
 
-  // (read through the scalar cache: a wait for an entry is then none for the loads before it)
-  typedef __attribute__((address_space(4))) const int32_t* table_t;
-  const table_t tab = (table_t)(a.table + (int64_t)b * a.width);
-  const int npages = (int)a.c.pages;
-  auto page_of = [&](int t) {   // page of token t, -1 where there is none
-    const int e = t >> a.c.shift;
-    const int p = e < a.width ? tab[e] : -1;
-    return (uint32_t)p < (uint32_t)npages ? p : -1;
-  };
-  const int ktok = 8 * (n >> 2) + (n & 3), vtok = 8 * g4;   // the lane's tokens in a tile
-  const int64_t page_rows = (int64_t)2 * Hk * a.c.page, head_row = (int64_t)h * a.c.page;
-  const int64_t to_values = (int64_t)Hk * a.c.page;
-  Keys<DH, GS> x;
-  Values<DH, GS> y;
-  // the tile at token t, whose halves lie in pages p0 and p1 (any page stands in for none)
-  auto keys = [&](int t, int p0, int p1) {
-    if (a.c.page > 16) {   // one page: the lanes' places in it are always the same
-      const int64_t row = max(p0, 0) * page_rows + head_row + (t & (a.c.page - 1));
-      load_keys<DH, GS>(x, a.c.codes + row * (DH / 2), ktok * (DH / 2) + g4 * (GS / 8),
-                        a.c.scale + row * G, ktok * G, vtok * G);
-    } else {
-      const int64_t rk = max(ktok >= 16 ? p1 : p0, 0) * page_rows + head_row + (ktok & 15);
-      const int64_t rv = max(vtok >= 16 ? p1 : p0, 0) * page_rows + head_row + (vtok & 15);
-      load_keys<DH, GS>(x, a.c.codes + rk * (DH / 2), g4 * (GS / 8), a.c.scale + rk * G, 0,
-                        (uint32_t)0);
-      load_scales<G>(a.c.scale + rv * G, x.s);
-    }
-  };
-  auto values = [&](int t, int p0, int p1) {
-    if (a.c.page > 16) {
-      const int in = t & (a.c.page - 1);
-      const int64_t row = max(p0, 0) * page_rows + head_row + to_values;
-      load_values<DH, GS>(y, a.c.codes + row * (DH / 2) + kv4_value_at(in, 0, 0, 0, NB),
-                          kv4_value_at(vtok, 0, n, 0, NB), a.c.scale + (row + in) * G, vtok * G);
-    } else {
-      const int64_t row = max(vtok >= 16 ? p1 : p0, 0) * page_rows + head_row + to_values;
-      load_values<DH, GS>(y, a.c.codes + row * (DH / 2), kv4_value_at(vtok & 15, 0, n, 0, NB),
-                          a.c.scale + row * G, (vtok & 15) * G);
-    }
-  };
+  // Groups whose scales are held at once: all of four would take 64 registers; with fewer a
+  // tile looks once whether any reference has to follow (two long sequences, two groups: 63 us
+  // instead of 76).
+  constexpr int AT = G <= 2 && (DH == 64 || G * RT < 4) ? G : 1;
   float s[RT][8];   // of token t0 + 8·g4 + e
-  auto scores = [&]() {
+  auto scores = [&](const uint8_t* tile) {
+    const float* scale = reinterpret_cast<const float*>(tile + 2 * Tl::CODES);
+    float ks[AT][8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int g = 0; g < G; ++g) {
+      if (g % AT == 0) octet_scales<G, AT>(scale + vtok * G, g, ks);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t z = kv4_zero(x.zero[j][g]) * 0x00800080u;   // 128·zp, twice
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t z = kv4_zero(scale[(ktok + 4 * j) * G + g]) * 0x00800080u;   // 128·zp, twice
         // (of the same shape as the products that it is chained to: behind a 16x16x16 one they
         // took half of its result too early)
         const f16x8_t zf = __builtin_bit_cast(f16x8_t, u32x4_t{z, z, z, z});
@@ -391,9 +396,22 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
         for (int t = 0; t < RT; ++t)
           acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(zf, qz[t][g],
                                                           f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+        uint32_t words[KW];   // the lane's token's codes of GS/4 channels
+        const uint8_t* from = tile + (ktok + 4 * j) * (DH / 2) + g * (GS / 2) + g4 * (GS / 8);
+        if constexpr (KW == 4) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(from);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) words[i] = v[i];
+        } else if constexpr (KW == 2) {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(from);
+          words[0] = v[0];
+          words[1] = v[1];
+        } else {
+          words[0] = *reinterpret_cast<const uint32_t*>(from);
+        }
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
-          const f16x8_t f = keys_of(x.k[j][g][k]);
+          const f16x8_t f = keys_of(words[k]);
 #pragma unroll
           for (int t = 0; t < RT; ++t)
             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, qf[t][g][k], acc[t], 0, 0, 0);
@@ -402,71 +420,91 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            s[t][4 * j + r] = g == 0 ? acc[t][r] * x.s[4 * j + r][g]
-                                     : fmaf(acc[t][r], x.s[4 * j + r][g], s[t][4 * j + r]);
+            s[t][4 * j + r] = g == 0 ? acc[t][r] * ks[g % AT][4 * j + r]
+                                     : fmaf(acc[t][r], ks[g % AT][4 * j + r], s[t][4 * j + r]);
       }
+    }
   };
-  auto weigh = [&](int t0, int p0, int p1) {
-    float vs[8][G];
+  auto weigh = [&](const uint8_t* tile, int t0, int p0, int p1) {
+    u32x4_t yv[NB];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int g = 0; g < G; ++g) vs[e][g] = y.s[e][g];
+    for (int i = 0; i < NB; ++i)
+      yv[i] = *reinterpret_cast<const u32x4_t*>(tile + Tl::CODES + kv4_value_at(vtok, i, n, 0, NB));
     const bool bad = p0 < 0 || p1 < 0;
     const bool tail = bad || t0 + 32 > len - a.news + 1;
+    const bool gone = (vtok >= 16 ? p1 : p0) < 0;
+    const float* vscale =
+        reinterpret_cast<const float*>(tile + 2 * Tl::CODES + Tl::SCALES) + vtok * G;
+    float ys[AT][8], vs[AT][8];
+    auto value_scales = [&](int g) {
+      octet_scales<G, AT>(vscale, g, ys);
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vs[i][e] = ys[i][e];
+    };
+    auto hide_scales = [&]() {
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vs[i][e] = gone || t0 + vtok + e >= len ? 0.0f : vs[i][e];
+    };
+    if constexpr (AT == G) value_scales(0);
     if (tail) {   // some token is hidden from some row
-      const bool gone = (vtok >= 16 ? p1 : p0) < 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int tok = t0 + vtok + e;
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           s[t][e] = gone || tok >= sees[t] ? -INFINITY : s[t][e];
-#pragma unroll
-        for (int g = 0; g < G; ++g) vs[e][g] = gone || tok >= len ? 0.0f : vs[e][g];
       }
+      if constexpr (AT == G) hide_scales();
     }
-    bool rises = false;
-    float top[RT], vtop[G];
+    auto largest = [&](const float (&x)[8]) {
+      float m = x[0];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      top[t] = s[t][0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], s[t][e]);
-      top[t] *= qs[t];
-      rises |= top[t] > m[t] + RISE;
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      vtop[g] = vs[0][g];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) vtop[g] = fmaxf(vtop[g], vs[e][g]);
-      rises |= vtop[g] > 2.0f * sv[g];
-    }
-    if (__any(rises)) {
-      float by[RT], vby[G];
+      for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
+      return m;
+    };
+    auto follow = [&](int g, float top) {   // sv of group g
+      const float sn = fmaxf(sv[g], group_max<64>(top)), by = sv[g] / sn;
+      sv[g] = sn;
+      wk[g] = W_TOP / sn;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const float mn = fmaxf(m[t], row_max(top[t]));
-        by[t] = __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        l[t] *= by[t];
+#pragma unroll
+        for (int d = g * GS / 16; d < (g + 1) * GS / 16; ++d) o[t][d] *= by;
+        oz[t][g] *= by;
       }
+    };
+    bool rises = false;
+    float top[RT], vtop[AT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      top[t] = largest(s[t]) * qs[t];
+      rises |= top[t] > m[t] + RISE;
+    }
+    if constexpr (AT == G) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float sn = fmaxf(sv[g], group_max<64>(vtop[g]));
-        vby[g] = sv[g] / sn;
-        sv[g] = sn;
-        wk[g] = W_TOP / sn;
+        vtop[g] = largest(vs[g]);
+        rises |= vtop[g] > 2.0f * sv[g];
       }
+    }
+    if (__any(rises)) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+      for (int t = 0; t < RT; ++t) {
+        const float mn = fmaxf(m[t], row_max(top[t])), by = __builtin_amdgcn_exp2f(m[t] - mn);
+        m[t] = mn;
+        l[t] *= by;
 #pragma unroll
-        for (int d = 0; d < NO; ++d) o[t][d] *= by[t] * vby[16 * d / GS];
+        for (int d = 0; d < NO; ++d) o[t][d] *= by;
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+        for (int g = 0; g < G; ++g) oz[t][g] *= by;
+      }
+      if constexpr (AT == G)
 #pragma unroll
-        for (int g = 0; g < G; ++g) oz[t][g] *= by[t] * vby[g];
+        for (int g = 0; g < G; ++g) follow(g, vtop[g]);
     }
     float p[RT][8];
 #pragma unroll
@@ -478,15 +516,20 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
       }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      if constexpr (AT < G) {
+        value_scales(g);
+        if (tail) hide_scales();
+        vtop[0] = largest(vs[0]);
+        if (__any(vtop[0] > 2.0f * sv[g])) follow(g, vtop[0]);
+      }
       // weights p·vs, eight tokens of the lane's row
       f16x8_t w[RT];
-      float k[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) k[e] = vs[e][g] * wk[g];
+      for (int e = 0; e < 8; ++e) vs[g % AT][e] *= wk[g];
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[t][e] = (_Float16)(p[t][e] * k[e]);
+        for (int e = 0; e < 8; ++e) w[t][e] = (_Float16)(p[t][e] * vs[g % AT][e]);
       if (tail)   // hidden tokens weigh nothing, whatever they hold
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -495,7 +538,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
             if (s[t][e] == -INFINITY) w[t][e] = (_Float16)0.0f;
       u32x4_t z;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = zeros_of(y.s[2 * i][g], y.s[2 * i + 1][g]);
+      for (int i = 0; i < 4; ++i) z[i] = zeros_of(ys[g % AT][2 * i], ys[g % AT][2 * i + 1]);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
         oz[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, z), w[t],
@@ -505,7 +548,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
         u32x4_t lo, hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t u = q & 1 ? y.v[q / 2][i] >> 8 : y.v[q / 2][i];
+          const uint32_t u = q & 1 ? yv[q / 2][i] >> 8 : yv[q / 2][i];
           lo[i] = low_codes(u);
           hi[i] = high_codes(u);
         }
@@ -521,53 +564,60 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     }
   };
 
-  constexpr int STEP = 32 * WAVES;
-  int t = first + 32 * wave;
-  if (t < last) {
-    // keys and values of the next tile are asked for as soon as the registers are free
-    int p0 = page_of(t), p1 = page_of(t + 16);
-    keys(t, p0, p1);
-    values(t, p0, p1);
-    for (; t < last; t += STEP) {
-      const bool more = t + STEP < last;
-      const int n0 = page_of(t + STEP), n1 = page_of(t + STEP + 16);
-      scores();
-      if (more) keys(t + STEP, n0, n1);
-      weigh(t, p0, p1);
-      if (more) values(t + STEP, n0, n1);
-      p0 = n0, p1 = n1;
+  for (int base = t0; base < last; base += STAGES * STEP)
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      const int t = base + i * STEP;
+      if (t >= last) break;
+      // the loads of this tile have come once no more than the others' are left
+      if (t + (STAGES - 1) * STEP < last) wait_loads<(STAGES - 1) * LOADS>();
+      else wait_loads<0>();
+      const int n0 = page_of(t + STAGES * STEP), n1 = page_of(t + STAGES * STEP + 16);
+      scores(ring + i * Tl::BYTES);
+      weigh(ring + i * Tl::BYTES, t, p0[i], p1[i]);
+      asm volatile("" ::: "memory");
+      if (t + STAGES * STEP < last) fetch(t + STAGES * STEP, n0, n1, ring + i * Tl::BYTES);
+      p0[i] = n0, p1[i] = n1;
     }
-  }
 
   // join the waves: rows x channels in LDS, each wave's relative to its own m
-  constexpr int R = 16 * RT, LD = DH + 4;
-  __shared__ float sm[WAVES][R], sl[WAVES][R], so[WAVES][R][LD];
+  float(&so)[WAVES][R][LD] = *reinterpret_cast<float(*)[WAVES][R][LD]>(lds);
+  float(&sm)[WAVES][R] = *reinterpret_cast<float(*)[WAVES][R]>(lds + sizeof(so));
+  float(&sl)[WAVES][R] = *reinterpret_cast<float(*)[WAVES][R]>(lds + sizeof(so) + sizeof(sm));
+  const int waves = max(1, min(WAVES, (last - first + 31) / 32));   // those that had tokens
+  __syncthreads();   // the tiles have been read
+  if (wave < waves)
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int row = 16 * t + n;
-    const float sum = row_sum(l[t]);
-    if (g4 == 0) sm[wave][row] = m[t], sl[wave][row] = sum;
+    for (int t = 0; t < RT; ++t) {
+      const int row = 16 * t + n;
+      const float sum = row_sum(l[t]);
+      if (tile * R + row >= a.rows) continue;
+      if (g4 == 0) sm[wave][row] = m[t], sl[wave][row] = sum;
 #pragma unroll
-    for (int d = 0; d < NO; ++d) {
-      // (codes are 2^-24 of themselves, those of odd d 2^-20)
-      const float k = sv[16 * d / GS] * (0x1p24f / W_TOP), odd = d & 1 ? 0.0625f : 1.0f;
+      for (int q = 0; q < NO / 2; ++q) {
+        // (codes are 2^-24 of themselves, those of odd channels 2^-20)
+        const float k = sv[32 * q / GS] * (0x1p24f / W_TOP);
+        const f32x4_t z = oz[t][32 * q / GS], x = o[t][2 * q], y = o[t][2 * q + 1];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)   // channel 32·(d/2) + 2·(4·g4 + r) + d%2
-        so[wave][row][32 * (d >> 1) + 2 * (4 * g4 + r) + (d & 1)] =
-            (o[t][d][r] * odd - oz[t][16 * d / GS][r]) * k;
+        for (int r = 0; r < 4; r += 2)   // channels 32·q + 8·g4 + 2·r ..
+          *reinterpret_cast<f32x4_t*>(&so[wave][row][32 * q + 8 * g4 + 2 * r]) =
+              f32x4_t{(x[r] - z[r]) * k, (y[r] * 0.0625f - z[r]) * k, (x[r + 1] - z[r + 1]) * k,
+                      (y[r + 1] * 0.0625f - z[r + 1]) * k};
+      }
     }
-  }
   __syncthreads();
   for (int e = threadIdx.x; e < R * (DH / 4); e += 64 * WAVES) {
     const int row = e / (DH / 4), c = 4 * (e % (DH / 4)), at = tile * R + row;
-    if (at >= a.rows) continue;
+    if (at >= a.rows) break;
     float mm = sm[0][row];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) mm = fmaxf(mm, sm[w][row]);
+    for (int w = 1; w < WAVES; ++w)
+      if (w < waves) mm = fmaxf(mm, sm[w][row]);
     float sum = 0.0f;
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
+      if (w >= waves) break;
       const float f = __builtin_amdgcn_exp2f(sm[w][row] - mm);
       sum += f * sl[w][row];
       v += f * *reinterpret_cast<const f32x4_t*>(&so[w][row][c]);
@@ -641,12 +691,12 @@ struct Plan {
 };
 Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max_len) {
   Plan p;
-  p.RT = rows > 16 && DH / GS < 4 ? 2 : 1;   // (four groups of scales for two rows do not fit)
+  p.RT = rows > 16 && DH / GS < 4 ? 2 : 1;   // (two rows of four groups do not fit)
   p.tiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.least = 256;
   p.target = 9;
   const int64_t per = heads * p.tiles;
-  p.wide = p.RT == 1 && DH / GS < 4 && max_len > 256 && max_len <= 1024;
+  p.wide = p.RT == 1 && B * per <= 512 && max_len > 256 && max_len <= 1024;
   p.whole = p.wide || max_len <= p.least || B * per >= int64_t(4) << p.target;
   p.groups = (B + (p.whole ? 0 : ((int64_t(1) << p.target) + per - 1) / per)) * per;
   return p;
@@ -655,17 +705,15 @@ Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max
 template <int DH, int GS>
 void launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
   const dim3 grid((unsigned)p.groups);
-  if constexpr (DH / GS < 4) {
+  if constexpr (DH / GS < 4)
     if (p.RT == 2) {
-      hipLaunchKernelGGL((k_kv4_attention<DH, GS, 2, 4>), grid, dim3(256), 0, st, a);
+      hipLaunchKernelGGL((k_kv4_attention<DH, GS, 2, 4, 2>), grid, dim3(256), 0, st, a);
       return;
     }
-    if (p.wide) {
-      hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 8>), grid, dim3(512), 0, st, a);
-      return;
-    }
-  }
-  hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 4>), grid, dim3(256), 0, st, a);
+  if (p.wide)
+    hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 8, 2>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 4, 2>), grid, dim3(256), 0, st, a);
 }
 template <int DH>
 void join(const AttnArgs& a, const Plan& p, hipStream_t st) {
