@@ -1141,9 +1141,9 @@ ar_status check_kv4_attention(const ar_kv4_cache* c, int64_t B, int64_t news, in
 ar_status check_packed(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads,
                        int64_t head_dim) {
   AR_TRY(check_heads(heads, kv_heads, head_dim));
-  if (B < 0 || B > kMaxSeqs || Tq < 0 || Tk < 0 || Tq >= kMaxI32 || Tk >= kMaxI32)
+  if (B < 0 || B > kMaxSeqs || Tq < 0 || Tk < 0 || Tk >= kMaxI32 / 2)
     return AR_ERR_SHAPE;
-  return Tq * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
+  return Tq < kMaxI32 / 2 && Tq * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
 }
 
 }  // namespace

@@ -18,12 +18,15 @@
 // float32.
 #include <math.h>
 
+#include <type_traits>
+
 #include "ar_device.h"
 #include "ar_launch.h"
 
 namespace {
 
 constexpr int NT = 256, BM = 128, KT = 64;
+constexpr int TARGET = 512, LEAST = 256;   // workgroups wanted of few tiles, keys of one at least
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
 
@@ -39,9 +42,11 @@ struct Args {
   const int32_t *q_off, *k_off;
   int64_t Tq, Tk;
   int B, heads, kv_heads, ratio, tiles;
-  float sl;   // scale·log2 e
+  float sl;       // scale·log2 e
   uint16_t* out;
   float* lse;
+  float *po, *pm; // partial sums [workgroup][row][Dh] and (m, l) of each row
+  int64_t groups; // of those
 };
 
 // Sequence b's queries and keys, by offsets that lead nowhere outside the arrays.
@@ -57,32 +62,79 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   return s;
 }
 
-// Tile t of the sequences' rows cut into tiles of BM: its sequence and first row; false
-// when there is no such tile. The whole wave calls it.
-__device__ __forceinline__ bool find_tile(const Args& a, int t, int& b, int& r0) {
+// Sum over a wave, from lane 0 to the lane's own.
+template <class T>
+__device__ __forceinline__ T wave_scan(T x) {
+  auto add = [&](auto ctrl, auto rows) {
+    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                              decltype(rows)::value, 0xF, false);
+    x += __builtin_bit_cast(T, o);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>(), integral_constant<int, 0xF>());   // from 1, 2, 4, 8 lanes
+  add(integral_constant<int, 0x112>(), integral_constant<int, 0xF>());   // before in the row
+  add(integral_constant<int, 0x114>(), integral_constant<int, 0xF>());
+  add(integral_constant<int, 0x118>(), integral_constant<int, 0xF>());
+  add(integral_constant<int, 0x142>(), integral_constant<int, 0xA>());   // from the rows before
+  add(integral_constant<int, 0x143>(), integral_constant<int, 0xC>());
+  return x;
+}
+template <class T>
+__device__ __forceinline__ T wave_last(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
+__device__ __forceinline__ int tiles_of(const Args& a, const Seq& s) {
+  return (int)(((int64_t)s.nq * a.ratio + BM - 1) / BM);
+}
+// Tokens of the parts into which the keys are divided where there are few tiles: TARGET
+// parts over all tiles and key heads, the same for every workgroup.
+__device__ __forceinline__ int chunk_of(const Args& a) {
+  float work = 0.0f;   // (rounded alike everywhere)
+  for (int b = threadIdx.x & 63; b < a.B; b += 64) {
+    const Seq s = seq_of(a, b);
+    work += (float)tiles_of(a, s) * (float)s.nk;
+  }
+  // (above the quotient, so that there are no more parts than workgroups)
+  const float each = wave_last(wave_scan(work)) * (float)a.kv_heads * (1.0f / TARGET) + 1.0f;
+  const int c = (int)fminf(fmaxf(each, (float)LEAST), 0x1p30f);
+  return __builtin_amdgcn_readfirstlane((c + KT - 1) / KT * KT);
+}
+// Unit `at` of the sequences' rows cut into tiles of BM and these (chunk > 0) into parts of
+// the keys: its sequence, first row, part, and the units before its tile. `whole`: the
+// count goes over tiles. False when there is no such unit.
+struct Unit {
+  int b, r0, part;
+  int64_t before;
+};
+__device__ __forceinline__ bool find_unit(const Args& a, int chunk, int at, bool whole, Unit& u) {
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;
+  int before = 0;
+  int64_t units = 0;
   for (int base = 0; base < a.B; base += 64) {
-    int64_t tiles = 0;
+    int tiles = 0, parts = 1;
     if (base + lane < a.B) {
       const Seq s = seq_of(a, base + lane);
-      tiles = ((int64_t)s.nq * a.ratio + BM - 1) / BM;
+      tiles = tiles_of(a, s);
+      if (chunk) parts = max(1, (int)(((uint32_t)s.nk + (uint32_t)chunk - 1) / (uint32_t)chunk));
     }
-    int64_t sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t up = __shfl_up((long long)sum, d, 64);
-      if (lane >= d) sum += up;
-    }
-    const uint64_t past = __ballot(before + sum > t);
+    // (overlapping sequences may count more than there can be: bounded, so that 64 fit an int)
+    const int n = (int)min((int64_t)tiles * (whole ? 1 : parts), (int64_t)1 << 24);
+    const int m = (int)min((int64_t)tiles * parts, (int64_t)1 << 24);
+    const int sum = wave_scan(n), all = whole && chunk ? wave_scan(m) : sum;
+    const uint64_t past = __ballot(before + sum > at);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      const int64_t first = before + __shfl((long long)(sum - tiles), l, 64);
-      b = __builtin_amdgcn_readfirstlane(base + l);
-      r0 = __builtin_amdgcn_readfirstlane((int)((t - first) * BM));
+      const int local = at - before - __builtin_amdgcn_readlane(sum - n, l);
+      const int p = __builtin_amdgcn_readlane(parts, l), tile = whole ? local : local / p;
+      u.b = base + l;
+      u.r0 = tile * BM;
+      u.part = whole ? 0 : local - tile * p;
+      u.before = units + __builtin_amdgcn_readlane(all - m, l) + (int64_t)tile * p;
       return true;
     }
-    before += __shfl((long long)sum, 63, 64);
+    before += wave_last(sum);
+    units += wave_last(all);
   }
   return false;
 }
@@ -91,19 +143,20 @@ __device__ __forceinline__ bool finite_bits(uint32_t pair) {
   return (pair & 0x7F80u) != 0x7F80u && (pair & 0x7F800000u) != 0x7F800000u;
 }
 
-// One row by the definition, by one wave: for a row whose product met an infinity or a NaN
-// of a value hidden from it (0·inf). sees: the keys it sees. o: the wave's lane takes the
-// channels lane, lane + 64.
+// One row by the definition over the keys first .. last, by one wave: for a row whose product
+// met an infinity or a NaN of a value hidden from it (0·inf). The lane takes the channels
+// lane, lane + 64 of o.
 template <int DH>
 __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, const uint16_t* k,
-                                       const uint16_t* v, int sees, uint16_t* out) {
+                                          const uint16_t* v, int first, int last, float& m, float& l,
+                                          float (&o)[DH / 64]) {
   const int lane = threadIdx.x & 63;
-  float m = NO_MAX, l = 0.0f, o[DH / 64];
+  m = NO_MAX, l = 0.0f;
 #pragma unroll
   for (int d = 0; d < DH / 64; ++d) o[d] = 0.0f;
-  for (int t0 = 0; t0 < sees; t0 += 64) {
+  for (int t0 = first; t0 <= last; t0 += 64) {
     float s = -INFINITY;
-    if (t0 + lane < sees) {
+    if (t0 + lane <= last) {
       const uint16_t* kr = k + (int64_t)(t0 + lane) * a.k_stride;
       s = 0.0f;
       for (int d = 0; d < DH; ++d) s = fmaf(bf16_val(q[d]), bf16_val(kr[d]), s);
@@ -111,22 +164,20 @@ __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, cons
     }
     const float mn = fmaxf(m, group_max<64>(s)), by = exp2f(m - mn);
     m = mn;
-    const float p = t0 + lane < sees ? exp2f(s - m) : 0.0f;
+    const float p = t0 + lane <= last ? exp2f(s - m) : 0.0f;
     l = l * by + group_sum<64>(p);
 #pragma unroll
     for (int d = 0; d < DH / 64; ++d) o[d] *= by;
-    for (int j = 0; j < min(64, sees - t0); ++j) {
+    for (int j = 0; j < min(64, last + 1 - t0); ++j) {
       const float w = __shfl(p, j, 64);
 #pragma unroll
       for (int d = 0; d < DH / 64; ++d)
         o[d] = fmaf(w, bf16_val(v[(int64_t)(t0 + j) * a.v_stride + lane + 64 * d]), o[d]);
     }
   }
-#pragma unroll
-  for (int d = 0; d < DH / 64; ++d) out[lane + 64 * d] = (uint16_t)bf16_bits(o[d] / l);
 }
 
-template <int DH>
+template <int DH, bool PARTS>
 __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
   constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
   constexpr int TILE = KT * ROW;                   // bytes of a tile of keys or values
@@ -134,9 +185,12 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
   constexpr int ND = DH / 32, NC = DH / 16;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][TILE];
 
-  const int kvh = blockIdx.x % a.kv_heads;
-  int b, r0;
-  if (!find_tile(a, a.tiles - 1 - (int)(blockIdx.x / a.kv_heads), b, r0)) return;
+  // the longest tiles, the last of a sequence, come first
+  const int kvh = blockIdx.x % a.kv_heads, at = blockIdx.x / a.kv_heads;
+  const int chunk = PARTS ? chunk_of(a) : 0;
+  Unit un;
+  if (!find_unit(a, chunk, PARTS ? at : a.tiles - 1 - at, !PARTS, un)) return;
+  const int b = un.b, r0 = un.r0;
   const Seq sq = seq_of(a, b);
   const int nk = __builtin_amdgcn_readfirstlane(sq.nk), nq = __builtin_amdgcn_readfirstlane(sq.nq);
   const int k0 = __builtin_amdgcn_readfirstlane(sq.k0), q0 = __builtin_amdgcn_readfirstlane(sq.q0);
@@ -148,14 +202,13 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
   const int row = r0 + 32 * wave + l31, i = min(row, rows - 1) / a.ratio;
   const int head = kvh * a.ratio + min(row, rows - 1) - i * a.ratio;
   const int last = i + nk - nq;
-  const uint16_t* qp = a.q + (int64_t)(q0 + i) * a.q_stride + head * DH;
-  bf16x8_t qf[NC];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) qf[c] = *reinterpret_cast<const bf16x8_t*>(qp + 16 * c + 8 * half);
-
   // what the workgroup, and what every row of the wave, sees
   const int wrow0 = r0 + 32 * wave;
-  const int kend = min((min(r0 + BM, rows) - 1) / a.ratio + nk - nq + 1, nk);
+  const int kall = min((min(r0 + BM, rows) - 1) / a.ratio + nk - nq + 1, nk);
+  const int kfirst = PARTS ? un.part * chunk : 0;
+  if (kfirst > 0 && kfirst >= kall) return;   // (the join leaves it out too)
+  const int kend = PARTS ? min(kall, kfirst + chunk) : kall;
+  const bool joined = PARTS && kall > chunk;
   const int wfirst = min(wrow0, rows - 1) / a.ratio + nk - nq;                    // least of last
   const int wend = wrow0 < rows ? (min(wrow0 + 32, rows) - 1) / a.ratio + nk - nq + 1 : 0;
 
@@ -184,6 +237,13 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
                                                vvo + (uint32_t)(j * LROWS * a.v_stride * 2), 0, 0, 0);
   };
 
+  if (kend > kfirst) stage(kfirst, 0);
+
+  const uint16_t* qp = a.q + (int64_t)(q0 + i) * a.q_stride + head * DH;
+  bf16x8_t qf[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) qf[c] = *reinterpret_cast<const bf16x8_t*>(qp + 16 * c + 8 * half);
+
   // reads: key row of the lane (row r of the product is the token that puts neighbouring
   // tokens side by side in a lane's scores), chunk 2c + half
   const int kr = 16 * (l31 >> 4) + 8 * ((l31 >> 2) & 1) + 4 * ((l31 >> 3) & 1) + (l31 & 3);
@@ -208,7 +268,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
     for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   float m = NO_MAX, l = 0.0f;
 
-  auto work = [&](int t0, const uint8_t* lk, const uint8_t* lv) {
+  auto work = [&](auto masked, int t0, const uint8_t* lk, const uint8_t* lv) {
     f32x16_t s[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -220,7 +280,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
         s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[c], s[j], 0, 0, 0);
       }
     }
-    if (t0 + KT > wfirst + 1) {
+    if constexpr (decltype(masked)::value) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -266,18 +326,32 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
       }
   };
 
-  if (kend > 0) stage(0, 0);
-  int s = 0;
-  for (int t0 = 0; t0 < kend; t0 += KT, s ^= 1) {
+  int t0 = kfirst, s = 0;
+  auto step = [&](auto masked) {
     __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of the tile (vmcnt 0)
     __syncthreads();                      // everybody's; and the other stage has been read
     if (t0 + KT < kend) stage(t0 + KT, s ^ 1);
-    if (t0 < wend) work(t0, lds[s][0], lds[s][1]);
-  }
+    if (!decltype(masked)::value || t0 < wend) work(masked, t0, lds[s][0], lds[s][1]);
+    t0 += KT;
+    s ^= 1;
+  };
+  // tiles that every row of the workgroup sees whole, then the others
+  const int kfull = r0 / a.ratio + nk - nq + 1;
+  while (t0 + KT <= min(kfull, kend)) step(std::false_type());
+  while (t0 < kend) step(std::true_type());
 
   l += __shfl_xor(l, 32, 64);
-  if (row < rows) {
-    const int64_t to = (int64_t)(q0 + i) * a.heads + head;
+  const int64_t to = (int64_t)(q0 + i) * a.heads + head;
+  const int64_t pto = (int64_t)blockIdx.x * BM + 32 * wave + l31;
+  if (row < rows && joined) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<f32x4_t*>(a.po + pto * DH + 32 * d + 8 * r + 4 * half) =
+            f32x4_t{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
+    if (half == 0) a.pm[2 * pto] = m, a.pm[2 * pto + 1] = l;
+  } else if (row < rows) {
     const float inv = last < 0 ? 0.0f : 1.0f / l;   // a row that sees no key is 0
     uint16_t* op = a.out + to * DH + 4 * half;
 #pragma unroll
@@ -303,7 +377,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
   redo = (redo | (redo >> 32)) & 0xFFFFFFFFull;
   if (redo) {
     bool found = false;   // (keys beyond the wave's rows, and so hidden from some of them)
-    for (int t = max(wfirst + 1, 0) + lane; t < min(nk, (wend + KT - 1) / KT * KT); t += 64) {
+    for (int t = max(wfirst + 1, kfirst) + lane; t < min(nk, (kend + KT - 1) / KT * KT); t += 64) {
       const uint16_t* vr = vb + (int64_t)t * a.v_stride;
       for (int d = 0; d < DH; d += 2)
         found |= !finite_bits(*reinterpret_cast<const uint32_t*>(vr + d));
@@ -313,19 +387,92 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
         const int r = __ffsll((unsigned long long)redo) - 1;
         redo &= redo - 1;
         const int ri = __shfl(i, r, 64), rh = __shfl(head, r, 64);
-        plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, ri + nk - nq + 1,
-                      a.out + ((int64_t)(q0 + ri) * a.heads + rh) * DH);
+        float rm, rl, ro[DH / 64];
+        plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, kfirst,
+                      min(ri + nk - nq, kend - 1), rm, rl, ro);
+        const int64_t rto = (int64_t)(q0 + ri) * a.heads + rh;
+        const int64_t rpto = (int64_t)blockIdx.x * BM + 32 * wave + r;
+#pragma unroll
+        for (int d = 0; d < DH / 64; ++d)
+          if (joined) a.po[rpto * DH + lane + 64 * d] = ro[d];
+          else a.out[rto * DH + lane + 64 * d] = (uint16_t)bf16_bits(ro[d] / rl);
+        if (joined && lane == 0) a.pm[2 * rpto] = rm, a.pm[2 * rpto + 1] = rl;
       }
   }
 }
 
+// Joins the parts of a tile's rows, where there are several: Dh/4 lanes a row, four channels
+// each, the parts in order.
+template <int DH>
+__global__ __launch_bounds__(NT) void k_attention_join(Args a) {
+  constexpr int LPR = DH / 4, ROWS = NT / LPR, PER = BM / ROWS;   // workgroups a tile
+  const int tile = blockIdx.x / PER, kvh = tile % a.kv_heads;
+  const int chunk = chunk_of(a);
+  Unit un;
+  if (!find_unit(a, chunk, tile / a.kv_heads, true, un)) return;
+  const Seq s = seq_of(a, un.b);
+  const int rows = s.nq * a.ratio, in = (blockIdx.x - tile * PER) * ROWS + threadIdx.x / LPR;
+  const int row = un.r0 + in, c = threadIdx.x % LPR;
+  const int kall = min((min(un.r0 + BM, rows) - 1) / a.ratio + s.nk - s.nq + 1, s.nk);
+  if (kall <= chunk || row >= rows) return;   // a single part has written its rows
+  const int parts = (kall + chunk - 1) / chunk;
+  if ((un.before + parts) * a.kv_heads > a.groups) return;   // (overlapping sequences)
+  auto at = [&](int p) { return ((int64_t)(un.before + p) * a.kv_heads + kvh) * BM + in; };
+  float m = NO_MAX, sum = 0.0f;
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.pm[2 * at(p)]);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float f = __builtin_amdgcn_exp2f(a.pm[2 * at(p)] - m);
+    sum += f * a.pm[2 * at(p) + 1];
+    v += f * *reinterpret_cast<const f32x4_t*>(a.po + at(p) * DH + 4 * c);
+  }
+  const int i = row / a.ratio;
+  const int64_t to = (int64_t)(s.q0 + i) * a.heads + kvh * a.ratio + row - i * a.ratio;
+  const bool none = i + s.nk - s.nq < 0;
+  const float inv = none ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x2_t*>(a.out + to * DH + 4 * c) =
+      u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
+  if (a.lse && c == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(sum));
+}
+
+// The keys are divided where there are too few tiles for the GPU.
+struct Plan {
+  int64_t tiles, groups;   // tiles and workgroups at most, both times key heads
+  bool parts;
+};
+Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads) {
+  Plan p;
+  const int64_t rows = Tq * (heads / kv_heads);
+  p.tiles = (rows / BM + B) * kv_heads;   // no fewer than the sequences'
+  p.parts = (rows + BM - 1) / BM * kv_heads < TARGET && Tk > LEAST;
+  p.groups = p.tiles + (p.parts ? (TARGET + kv_heads - 1) / kv_heads * kv_heads : 0);
+  return p;
+}
+
+template <int DH>
+void launch(const Args& a, const Plan& p, hipStream_t st) {
+  if (!p.parts) {
+    hipLaunchKernelGGL((k_attention_packed<DH, false>), dim3((unsigned)p.groups), dim3(NT), 0, st, a);
+    return;
+  }
+  hipLaunchKernelGGL((k_attention_packed<DH, true>), dim3((unsigned)p.groups), dim3(NT), 0, st, a);
+  constexpr int PER = BM / (NT / (DH / 4));
+  hipLaunchKernelGGL((k_attention_join<DH>), dim3((unsigned)(p.tiles * PER)), dim3(NT), 0, st, a);
+}
+
 }  // namespace
 
-int64_t ar_attention_packed_floats(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
-  return 0;
+// Floats of the workspace: partial sums and (m, l) of every row of every workgroup.
+int64_t ar_attention_packed_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,
+                                   int64_t kv_heads, int64_t head_dim) {
+  if (Tq == 0 || B == 0) return 0;
+  const Plan p = plan_of(B, Tq, Tk, heads, kv_heads);
+  return p.parts ? p.groups * BM * (head_dim + 2) : 0;
 }
 
 ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st) {
+  const Plan p = plan_of(g.B, g.Tq, g.Tk, g.heads, g.kv_heads);
   Args a;
   a.q = g.q, a.k = g.k, a.v = g.v;
   a.q_stride = g.q_stride, a.k_stride = g.k_stride, a.v_stride = g.v_stride;
@@ -333,11 +480,13 @@ ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st)
   a.Tq = g.Tq, a.Tk = g.Tk;
   a.B = (int)g.B, a.heads = (int)g.heads, a.kv_heads = (int)g.kv_heads;
   a.ratio = (int)(g.heads / g.kv_heads);
-  a.tiles = (int)(g.Tq * a.ratio / BM + g.B);   // no less than the sequences' tiles
+  a.tiles = (int)(p.tiles / g.kv_heads);
   a.sl = (float)((double)g.scale * 1.4426950408889634);
   a.out = g.out, a.lse = g.lse;
-  const dim3 grid((unsigned)((int64_t)a.tiles * a.kv_heads));
-  if (g.head_dim == 64) hipLaunchKernelGGL((k_attention_packed<64>), grid, dim3(NT), 0, st, a);
-  else hipLaunchKernelGGL((k_attention_packed<128>), grid, dim3(NT), 0, st, a);
+  a.po = g.ws;
+  a.groups = p.groups;
+  a.pm = g.ws + p.groups * BM * g.head_dim;
+  if (g.head_dim == 64) launch<64>(a, p, st);
+  else launch<128>(a, p, st);
   return last_status();
 }

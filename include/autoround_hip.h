@@ -352,7 +352,8 @@ ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, 
    they are clamped to [0, Tq] and [0, Tk], and with decreasing ones rows of out are
    unspecified, but nothing outside the arrays is read or written. The weights are rounded
    to bf16 for their product with v. Tq = 0 or B = 0 is a no-op; B <= 65536;
-   Tq*heads < 2^31, Tk < 2^31. No host synchronisation. */
+   Tq*heads < 2^31, Tq and Tk < 2^30. No host synchronisation. Two calls that may overlap need
+   workspaces of their own. */
 ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                               int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
                               int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
@@ -407,7 +408,7 @@ ar_status ar_kv4_attention_workspace_size(const ar_kv4_cache* cache, int64_t B, 
    new_tokens + 1 + i. Both arrays are on the device and not checked on the host: a length
    is taken as min(max(length, 0), max_len), and tokens of a page that is not of the cache (-1, say)
    take no part. max_len (the largest length to come; at most width*page_size, below
-   2^30) decides how a long sequence is divided, and with it the workspace. out [B*new_tokens,
+   2^30) decides whether long sequences are divided, and with it the workspace. out [B*new_tokens,
    heads, head_dim], lse [B*new_tokens, heads]. The weights, each with its value's
    scale, are rounded to f16, and the matrix unit cuts products off: a score is off by up to
    2^-17 of a key's scale times the largest |q| for each channel, an output by 2^-13 of the

@@ -114,7 +114,7 @@ def test_packed_validation():
     assert packed(D=96, qs=768) == packed(D=256, qs=2048) == UNSUP
     for kw in (dict(H=7), dict(Hk=0), dict(H=0), dict(H=1024, qs=1024 * 128), dict(B=-1),
                dict(B=65537), dict(Tq=-1), dict(Tk=-1), dict(Tk=5), dict(Tq=1 << 31),
-               dict(Tq=1 << 28, Tk=1 << 28), dict(qs=1016), dict(ks=252), dict(vs=128),
+               dict(Tq=1 << 28, Tk=1 << 28), dict(Tk=1 << 30, ko=P), dict(qs=1016), dict(ks=252), dict(vs=128),
                dict(ks=1 << 22)):
         assert packed(**kw) == SHAPE, kw
     for kw in (dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(qo=NULL), dict(out=NULL), dict(q=P4),
