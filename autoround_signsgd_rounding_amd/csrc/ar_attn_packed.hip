@@ -25,8 +25,12 @@
 
 namespace {
 
-constexpr int NT = 256, BM = 128, KT = 64;
-constexpr int TARGET = 512, LEAST = 256;   // workgroups wanted of few tiles, keys of one at least
+constexpr int NT = 256, BM = 128;
+constexpr int GRAIN = 64;   // parts of the keys are a multiple of that
+// With few tiles the keys are divided: workgroups wanted, keys of one at least. (A part
+// costs its rows in float32, written and read, as much as 256 keys and values at 128 channels.)
+constexpr int TARGET = 512, LEAST = 1024;
+constexpr int MANY = 1536;   // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
 
@@ -41,7 +45,7 @@ struct Args {
   int64_t q_stride, k_stride, v_stride;
   const int32_t *q_off, *k_off;
   int64_t Tq, Tk;
-  int B, heads, kv_heads, ratio, tiles;
+  int B, heads, kv_heads, ratio;
   float sl;       // scale·log2 e
   uint16_t* out;
   float* lse;
@@ -98,11 +102,11 @@ __device__ __forceinline__ int chunk_of(const Args& a) {
   // (above the quotient, so that there are no more parts than workgroups)
   const float each = wave_last(wave_scan(work)) * (float)a.kv_heads * (1.0f / TARGET) + 1.0f;
   const int c = (int)fminf(fmaxf(each, (float)LEAST), 0x1p30f);
-  return __builtin_amdgcn_readfirstlane((c + KT - 1) / KT * KT);
+  return __builtin_amdgcn_readfirstlane((c + GRAIN - 1) / GRAIN * GRAIN);
 }
-// Unit `at` of the sequences' rows cut into tiles of BM and these (chunk > 0) into parts of
-// the keys: its sequence, first row, part, and the units before its tile. `whole`: the
-// count goes over tiles. False when there is no such unit.
+// Unit `at` of the sequences' rows cut into tiles of BM (a sequence's last tile, the longest,
+// first) and these (chunk > 0) into parts of the keys: its sequence, first row, part, and the
+// units before its tile. `whole`: the count goes over tiles. False when there is no such unit.
 struct Unit {
   int b, r0, part;
   int64_t before;
@@ -128,7 +132,7 @@ __device__ __forceinline__ bool find_unit(const Args& a, int chunk, int at, bool
       const int local = at - before - __builtin_amdgcn_readlane(sum - n, l);
       const int p = __builtin_amdgcn_readlane(parts, l), tile = whole ? local : local / p;
       u.b = base + l;
-      u.r0 = tile * BM;
+      u.r0 = (__builtin_amdgcn_readlane(tiles, l) - 1 - tile) * BM;
       u.part = whole ? 0 : local - tile * p;
       u.before = units + __builtin_amdgcn_readlane(all - m, l) + (int64_t)tile * p;
       return true;
@@ -177,19 +181,21 @@ __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, cons
   }
 }
 
-template <int DH, bool PARTS>
-__global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
+// KT keys a tile. 64 wait less often; 32 leave registers and LDS for a third workgroup on a
+// CU, which pays where there are more of them than run at once (16384 tokens, 64 heads of 128 over
+// 8: 3832 us instead of 3976; 1000 tokens, 32 over 8: 26.6 instead of 24.2).
+template <int DH, bool PARTS, int KT>
+__global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args a) {
   constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
   constexpr int TILE = KT * ROW;                   // bytes of a tile of keys or values
   constexpr int LD = TILE / (NT * 16), LROWS = NT / C;   // loads a wave, rows between them
   constexpr int ND = DH / 32, NC = DH / 16;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][TILE];
 
-  // the longest tiles, the last of a sequence, come first
   const int kvh = blockIdx.x % a.kv_heads, at = blockIdx.x / a.kv_heads;
   const int chunk = PARTS ? chunk_of(a) : 0;
   Unit un;
-  if (!find_unit(a, chunk, PARTS ? at : a.tiles - 1 - at, !PARTS, un)) return;
+  if (!find_unit(a, chunk, at, !PARTS, un)) return;
   const int b = un.b, r0 = un.r0;
   const Seq sq = seq_of(a, b);
   const int nk = __builtin_amdgcn_readfirstlane(sq.nk), nq = __builtin_amdgcn_readfirstlane(sq.nq);
@@ -269,9 +275,9 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
   float m = NO_MAX, l = 0.0f;
 
   auto work = [&](auto masked, int t0, const uint8_t* lk, const uint8_t* lv) {
-    f32x16_t s[2];
+    f32x16_t s[KT / 32];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < KT / 32; ++j) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[j][r] = 0.0f;
 #pragma unroll
@@ -282,14 +288,14 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
     }
     if constexpr (decltype(masked)::value) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (t0 + 32 * j + 16 * (r >> 3) + 8 * half + (r & 7) > last) s[j][r] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[j][r]);
     top *= a.sl;
@@ -301,9 +307,9 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[d] *= by;
     }
-    u32x4_t p[4];
+    u32x4_t p[KT / 16];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
         const float e0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], a.sl, -m));
@@ -312,7 +318,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
         p[2 * j + (r >> 3)][(r & 7) >> 1] = bf16_pair(e0, e1);
       }
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < KT / 16; ++kk)
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         typedef __attribute__((address_space(3))) s16x4_t* tr;
@@ -342,7 +348,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
 
   l += __shfl_xor(l, 32, 64);
   const int64_t to = (int64_t)(q0 + i) * a.heads + head;
-  const int64_t pto = (int64_t)blockIdx.x * BM + 32 * wave + l31;
+  const int64_t slot = ((int64_t)at * a.kv_heads + kvh) * BM, pto = slot + 32 * wave + l31;
   if (row < rows && joined) {
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -382,6 +388,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
       for (int d = 0; d < DH; d += 2)
         found |= !finite_bits(*reinterpret_cast<const uint32_t*>(vr + d));
     }
+    __threadfence();   // behind the stores above
     if (__any(found))
       while (redo) {
         const int r = __ffsll((unsigned long long)redo) - 1;
@@ -391,7 +398,7 @@ __global__ __launch_bounds__(NT, 2) void k_attention_packed(Args a) {
         plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, kfirst,
                       min(ri + nk - nq, kend - 1), rm, rl, ro);
         const int64_t rto = (int64_t)(q0 + ri) * a.heads + rh;
-        const int64_t rpto = (int64_t)blockIdx.x * BM + 32 * wave + r;
+        const int64_t rpto = slot + 32 * wave + r;
 #pragma unroll
         for (int d = 0; d < DH / 64; ++d)
           if (joined) a.po[rpto * DH + lane + 64 * d] = ro[d];
@@ -452,11 +459,17 @@ Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads)
 
 template <int DH>
 void launch(const Args& a, const Plan& p, hipStream_t st) {
+  const dim3 grid((unsigned)p.groups), block(NT);
   if (!p.parts) {
-    hipLaunchKernelGGL((k_attention_packed<DH, false>), dim3((unsigned)p.groups), dim3(NT), 0, st, a);
+    if constexpr (DH == 128)
+      if (p.groups >= MANY) {
+        hipLaunchKernelGGL((k_attention_packed<DH, false, 32>), grid, block, 0, st, a);
+        return;
+      }
+    hipLaunchKernelGGL((k_attention_packed<DH, false, 64>), grid, block, 0, st, a);
     return;
   }
-  hipLaunchKernelGGL((k_attention_packed<DH, true>), dim3((unsigned)p.groups), dim3(NT), 0, st, a);
+  hipLaunchKernelGGL((k_attention_packed<DH, true, 64>), grid, block, 0, st, a);
   constexpr int PER = BM / (NT / (DH / 4));
   hipLaunchKernelGGL((k_attention_join<DH>), dim3((unsigned)(p.tiles * PER)), dim3(NT), 0, st, a);
 }
@@ -480,7 +493,6 @@ ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st)
   a.Tq = g.Tq, a.Tk = g.Tk;
   a.B = (int)g.B, a.heads = (int)g.heads, a.kv_heads = (int)g.kv_heads;
   a.ratio = (int)(g.heads / g.kv_heads);
-  a.tiles = (int)(p.tiles / g.kv_heads);
   a.sl = (float)((double)g.scale * 1.4426950408889634);
   a.out = g.out, a.lse = g.lse;
   a.po = g.ws;
