@@ -842,8 +842,8 @@ def _kv4(cache):
                          "[pages, 2, heads, page_size, head_dim/group_size]")
     pages, two, heads, page, half = codes.shape
     groups, dev = scale.shape[4], codes.get_device()
-    if not (dev >= 0 and two == 2 and scale.shape[:4] == codes.shape[:4] and groups > 0 and
-            2 * half % groups == 0 and codes.dtype is torch.uint8 and
+    if not (dev >= 0 and scale.shape == (pages, 2, heads, page, groups) and two == 2 and
+            groups > 0 and 2 * half % groups == 0 and codes.dtype is torch.uint8 and
             scale.dtype is torch.float32 and scale.get_device() == dev and
             codes.is_contiguous() and scale.is_contiguous()):
         lead = (pages, 2, heads, page)
@@ -856,19 +856,27 @@ def _kv4(cache):
 
 
 def _tokens(t, name, heads, dim, dtypes, dev):
-    """Stride between the tokens of t [tokens, heads, dim], whose tokens may lie apart."""
-    if t is None or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+    """Stride between the tokens of t [tokens, heads, dim], whose tokens may lie apart, or of
+    t [B, n, heads, dim], all of whose tokens lie one stride apart."""
+    if t is None or t.dim() < 3 or t.shape[-2] != heads or t.shape[-1] != dim or \
             t.dtype not in dtypes:
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be {want} [tokens, {heads}, {dim}], got " +
                          ("None" if t is None else f"{t.dtype} {list(t.shape)}"))
     if t.get_device() != dev:
         raise ValueError(f"{name} must live on the other tensors' GPU, got {t.device}")
-    apart, head, one = t.stride()
-    if t.shape[0] <= 1:     # (torch leaves the stride of such a dimension open)
+    if t.is_contiguous():
+        return heads * dim
+    *lead, apart, head, one = t.stride()
+    if lead and t.shape[0] > 1:
+        if t.shape[1] <= 1:     # (torch leaves the stride of such a dimension open)
+            apart = lead[0]
+        elif lead[0] != t.shape[1] * apart:
+            raise ValueError(f"{name}: the tokens must lie one stride apart, got strides "
+                             f"{t.stride()}")
+    elif t.shape[-3] <= 1:
         apart = heads * dim
-    if t.numel() and ((one != 1 and dim > 1) or (head != dim and heads > 1) or
-                      apart < heads * dim or apart % 8):
+    if (one != 1 and dim > 1) or (head != dim and heads > 1) or apart < heads * dim or apart % 8:
         raise ValueError(f"{name}: a token's heads must be contiguous, its stride a multiple of 8 "
                          f"no less than they take; got strides {t.stride()}")
     return apart
@@ -908,10 +916,11 @@ def _scratch(need: int, workspace, dev):
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
-def _attention_outputs(shape, out, want_lse, dev):
+def _attention_outputs(q, out, want_lse, dev):
     torch = _torch()
+    shape = q.shape
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif not _is(out, shape, torch.bfloat16, dev):
         _refuse(out, "out", shape, torch.bfloat16)
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
@@ -945,10 +954,11 @@ def attention_packed(q, k, v, offsets, *, k_offsets=None, scale=None, want_lse: 
     koff = None if k_offsets is None else _index(k_offsets, "k_offsets", (B + 1,), dev)
     if koff is None and Tq != Tk:
         raise ValueError(f"{Tq} queries and {Tk} keys need k_offsets")
-    out, lse = _attention_outputs((Tq, H, D), out, want_lse, dev)
+    out, lse = _attention_outputs(q, out, want_lse, dev)
     need = ctypes.c_size_t()
     st = lib.ar_attention_packed_workspace_size(B, Tq, Tk, H, Hk, D, ctypes.byref(need))
-    _check(st, "ar_attention_packed_workspace_size")
+    if st:
+        _check(st, "ar_attention_packed_workspace_size")
     ws, size, _keep = _scratch(need.value, workspace, dev)
     st = lib.ar_attention_packed(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, H,
                                  Hk, D, off, koff, B, D ** -0.5 if scale is None else scale,
@@ -968,11 +978,12 @@ def kv4_write(k, v, cache, slots, *, stream=None):
         with _elsewhere(stream, *cache, k, v, slots):
             return kv4_write(k, v, cache, slots)
     dts = (torch.bfloat16, torch.float32)
-    ks, vs = _tokens(k, "k", c.heads, c.head_dim, dts, dev), \
-        _tokens(v, "v", c.heads, c.head_dim, dts, dev)
+    H, D = c.heads, c.head_dim
+    ks, vs = _tokens(k, "k", H, D, dts, dev), _tokens(v, "v", H, D, dts, dev)
     T = k.shape[0]
-    if v.shape[0] != T or v.dtype is not k.dtype:
-        raise ValueError(f"k is {k.dtype} of {T} tokens, v {v.dtype} of {v.shape[0]}")
+    if k.dim() != 3 or v.shape != k.shape or v.dtype is not k.dtype:
+        raise ValueError(f"k and v must be alike [tokens, {H}, {D}], got {k.dtype} "
+                         f"{list(k.shape)} and {v.dtype} {list(v.shape)}")
     st = lib.ar_kv4_write(ctypes.byref(c), _dt(k), k.data_ptr(), ks, v.data_ptr(), vs,
                           _index(slots, "slots", (T,), dev), T,
                           torch._C._cuda_getCurrentRawStream(dev))
@@ -1020,11 +1031,8 @@ def kv4_attention(q, cache, table, lengths, *, max_len=None, scale=None, want_ls
     if q is None or q.dim() not in (3, 4):
         raise ValueError("q must be a [B, heads, head_dim] or [B, n, heads, head_dim] tensor")
     B, n, H = q.shape[0], (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
-    rows = q if q.dim() == 3 else q.flatten(0, 1)
-    if rows.numel() and rows.data_ptr() != q.data_ptr():
-        raise ValueError(f"q: the tokens must lie one stride apart, got strides {q.stride()}")
     D = c.head_dim
-    qs = _tokens(rows, "q", H, D, (torch.bfloat16,), dev)
+    qs = _tokens(q, "q", H, D, (torch.bfloat16,), dev)
     if H % c.heads:
         raise ValueError(f"{H} query heads cannot share {c.heads} key heads")
     if table is None or table.dim() != 2:
@@ -1033,14 +1041,14 @@ def kv4_attention(q, cache, table, lengths, *, max_len=None, scale=None, want_ls
     tab, lens = _index(table, "table", (B, W), dev), _index(lengths, "lengths", (B,), dev)
     if max_len is None:
         max_len = W * c.page_size
-    out, lse = _attention_outputs(q.shape, out, want_lse, dev)
+    out, lse = _attention_outputs(q, out, want_lse, dev)
     need = ctypes.c_size_t()
     st = lib.ar_kv4_attention_workspace_size(ctypes.byref(c), B, n, H, max_len,
                                              ctypes.byref(need))
     if st:
         _check(st, "ar_kv4_attention_workspace_size")
     ws, size, _keep = _scratch(need.value, workspace, dev)
-    st = lib.ar_kv4_attention(ctypes.byref(c), rows.data_ptr(), qs, B, n, H, tab, W, lens, max_len,
+    st = lib.ar_kv4_attention(ctypes.byref(c), q.data_ptr(), qs, B, n, H, tab, W, lens, max_len,
                               D ** -0.5 if scale is None else scale, out.data_ptr(),
                               None if lse is None else lse.data_ptr(), ws, size,
                               torch._C._cuda_getCurrentRawStream(dev))

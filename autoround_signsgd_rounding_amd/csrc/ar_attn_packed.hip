@@ -30,6 +30,7 @@ constexpr int GRAIN = 64;   // parts of the keys are a multiple of that
 // With few tiles the keys are divided: workgroups wanted, keys of one at least. (A part
 // costs its rows in float32, written and read, as much as 256 keys and values at 128 channels.)
 constexpr int TARGET = 512, LEAST = 1024;
+constexpr int PER = 8;       // workgroups that join the parts of a tile
 constexpr int MANY = 1536;   // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
@@ -412,35 +413,38 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 // each, the parts in order.
 template <int DH>
 __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
-  constexpr int LPR = DH / 4, ROWS = NT / LPR, PER = BM / ROWS;   // workgroups a tile
+  constexpr int LPR = DH / 4, ROWS = NT / LPR;
   const int tile = blockIdx.x / PER, kvh = tile % a.kv_heads;
   const int chunk = chunk_of(a);
   Unit un;
   if (!find_unit(a, chunk, tile / a.kv_heads, true, un)) return;
   const Seq s = seq_of(a, un.b);
-  const int rows = s.nq * a.ratio, in = (blockIdx.x - tile * PER) * ROWS + threadIdx.x / LPR;
-  const int row = un.r0 + in, c = threadIdx.x % LPR;
+  const int rows = s.nq * a.ratio, c = threadIdx.x % LPR;
   const int kall = min((min(un.r0 + BM, rows) - 1) / a.ratio + s.nk - s.nq + 1, s.nk);
-  if (kall <= chunk || row >= rows) return;   // a single part has written its rows
+  if (kall <= chunk) return;   // a single part has written its rows
   const int parts = (kall + chunk - 1) / chunk;
   if ((un.before + parts) * a.kv_heads > a.groups) return;   // (overlapping sequences)
-  auto at = [&](int p) { return ((int64_t)(un.before + p) * a.kv_heads + kvh) * BM + in; };
-  float m = NO_MAX, sum = 0.0f;
-  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.pm[2 * at(p)]);
+  const int first = (blockIdx.x - tile * PER) * (BM / PER) + threadIdx.x / LPR;
+  for (int in = first; in < first + BM / PER && un.r0 + in < rows; in += ROWS) {
+    const int row = un.r0 + in;
+    auto at = [&](int p) { return ((int64_t)(un.before + p) * a.kv_heads + kvh) * BM + in; };
+    float m = NO_MAX, sum = 0.0f;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, a.pm[2 * at(p)]);
 #pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float f = __builtin_amdgcn_exp2f(a.pm[2 * at(p)] - m);
-    sum += f * a.pm[2 * at(p) + 1];
-    v += f * *reinterpret_cast<const f32x4_t*>(a.po + at(p) * DH + 4 * c);
+    for (int p = 0; p < parts; ++p) {
+      const float f = __builtin_amdgcn_exp2f(a.pm[2 * at(p)] - m);
+      sum += f * a.pm[2 * at(p) + 1];
+      v += f * *reinterpret_cast<const f32x4_t*>(a.po + at(p) * DH + 4 * c);
+    }
+    const int i = row / a.ratio;
+    const int64_t to = (int64_t)(s.q0 + i) * a.heads + kvh * a.ratio + row - i * a.ratio;
+    const bool none = i + s.nk - s.nq < 0;
+    const float inv = none ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<u32x2_t*>(a.out + to * DH + 4 * c) =
+        u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
+    if (a.lse && c == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(sum));
   }
-  const int i = row / a.ratio;
-  const int64_t to = (int64_t)(s.q0 + i) * a.heads + kvh * a.ratio + row - i * a.ratio;
-  const bool none = i + s.nk - s.nq < 0;
-  const float inv = none ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<u32x2_t*>(a.out + to * DH + 4 * c) =
-      u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
-  if (a.lse && c == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(sum));
 }
 
 // The keys are divided where there are too few tiles for the GPU.
@@ -470,7 +474,6 @@ void launch(const Args& a, const Plan& p, hipStream_t st) {
     return;
   }
   hipLaunchKernelGGL((k_attention_packed<DH, true, 64>), grid, block, 0, st, a);
-  constexpr int PER = BM / (NT / (DH / 4));
   hipLaunchKernelGGL((k_attention_join<DH>), dim3((unsigned)(p.tiles * PER)), dim3(NT), 0, st, a);
 }
 
