@@ -1100,6 +1100,8 @@ namespace {
 constexpr int64_t kMaxI32 = int64_t(1) << 31;
 constexpr int64_t kMaxRatio = 256;   // query heads a key head, and new tokens a sequence
 constexpr int64_t kMaxSeqs = 65536;
+constexpr int64_t kMaxTokens = int64_t(1) << 28;   // written or read in one call
+constexpr int64_t kMaxGroups = int64_t(1) << 23;   // workgroups of a launch (below 2^32 threads)
 
 // heads over kv_heads, and a head's width.
 ar_status check_heads(int64_t heads, int64_t kv_heads, int64_t head_dim) {
@@ -1135,7 +1137,9 @@ ar_status check_kv4_attention(const ar_kv4_cache* c, int64_t B, int64_t news, in
   AR_TRY(check_heads(heads, c->heads, c->head_dim));
   if (B < 0 || news < 0 || news > kMaxRatio || max_len < 0 || max_len >= (int64_t(1) << 30))
     return AR_ERR_SHAPE;
-  return B < kMaxI32 && B * news < kMaxI32 && B * news * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
+  if (B >= kMaxI32 || B * news >= kMaxI32 || B * news * heads >= kMaxI32) return AR_ERR_SHAPE;
+  const int64_t tiles = (news * (heads / c->heads) + 15) / 16;
+  return B * c->heads * tiles < kMaxGroups ? AR_OK : AR_ERR_SHAPE;
 }
 
 ar_status check_packed(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads,
@@ -1143,7 +1147,8 @@ ar_status check_packed(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t
   AR_TRY(check_heads(heads, kv_heads, head_dim));
   if (B < 0 || B > kMaxSeqs || Tq < 0 || Tk < 0 || Tk >= kMaxI32 / 2)
     return AR_ERR_SHAPE;
-  return Tq < kMaxI32 / 2 && Tq * heads < kMaxI32 ? AR_OK : AR_ERR_SHAPE;
+  if (Tq >= kMaxI32 / 2 || Tq * heads >= kMaxI32 / 2) return AR_ERR_SHAPE;
+  return (B < Tq ? B : Tq) * kv_heads < kMaxGroups / 2 ? AR_OK : AR_ERR_SHAPE;
 }
 
 }  // namespace
@@ -1189,7 +1194,7 @@ ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int
                        void* stream) {
   AR_TRY(check_cache(cache, true));
   if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
-  if (T < 0 || T >= kMaxI32) return AR_ERR_SHAPE;
+  if (T < 0 || T >= kMaxTokens) return AR_ERR_SHAPE;
   if (T == 0) return AR_OK;
   const int64_t row = cache->heads * cache->head_dim;
   if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return AR_ERR_SHAPE;
@@ -1202,7 +1207,7 @@ ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T
                       void* k, void* v, void* stream) {
   AR_TRY(check_cache(cache, true));
   if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
-  if (T < 0 || T >= kMaxI32) return AR_ERR_SHAPE;
+  if (T < 0 || T >= kMaxTokens) return AR_ERR_SHAPE;
   if (T == 0) return AR_OK;
   if (!k || !v || !slots || !a16(k) || !a16(v) || !a4(slots)) return AR_ERR_INVALID_ARG;
   return ar_launch_kv4_read(*cache, slots, T, dt, k, v, static_cast<hipStream_t>(stream));

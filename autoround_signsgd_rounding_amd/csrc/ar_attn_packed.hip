@@ -455,8 +455,9 @@ struct Plan {
 Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads) {
   Plan p;
   const int64_t rows = Tq * (heads / kv_heads);
-  p.tiles = (rows / BM + B) * kv_heads;   // no fewer than the sequences'
-  p.parts = (rows + BM - 1) / BM * kv_heads < TARGET && Tk > LEAST;
+  // no fewer than the sequences': each of at most min(B, Tq) ends within a tile
+  p.tiles = (rows + (B < Tq ? B : Tq) * (BM - 1)) / BM * kv_heads;
+  p.parts = p.tiles < TARGET && Tk > LEAST;
   p.groups = p.tiles + (p.parts ? (TARGET + kv_heads - 1) / kv_heads * kv_heads : 0);
   return p;
 }

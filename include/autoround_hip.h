@@ -351,8 +351,9 @@ ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, 
    q_offsets[B]) keep what they held. Contents of the offsets are not checked on the host:
    they are clamped to [0, Tq] and [0, Tk], and with decreasing ones rows of out are
    unspecified, but nothing outside the arrays is read or written. The weights are rounded
-   to bf16 for their product with v. Tq = 0 or B = 0 is a no-op; B <= 65536;
-   Tq*heads < 2^31, Tq and Tk < 2^30. No host synchronisation. Two calls that may overlap need
+   to bf16 for their product with v. Tq = 0 or B = 0 is a no-op; B <= 65536, Tq and
+   Tk < 2^30, Tq*heads < 2^30, min(B, Tq)*kv_heads < 2^22. No host synchronisation: the call can
+   be captured in a HIP graph and replayed with other offsets. Two calls that may overlap need
    workspaces of their own. */
 ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                               int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
@@ -364,7 +365,7 @@ ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_
 /* A cache of pages of page_size tokens (16, 32, 64, 128 or 256). Slot p*page_size + t is
    token t of page p. Per token, head and group of group_size channels (32, 64 or 128, a
    divisor of head_dim), for keys and for values, in float32, each step rounded once:
-     lo = min(x, 0), hi = max(x, 0), s = (hi - lo)/15 (1 if 0; never below 2^-100),
+     lo = min(x, 0), hi = max(x, 0), s = max((hi - lo)/15, 2^-100),
      zp = clamp(rint(-lo/s), 0, 15), s' = s with its four lowest mantissa bits replaced by zp,
      code = clamp(rint(x/s') + zp, 0, 15); the value held is s'·(code - zp).
    A NaN or an infinity, or a range beyond float32, makes s' NaN and with it the group.
@@ -386,14 +387,14 @@ typedef struct {
    into slots [T] int32 on the device; tokens whose slot lies outside the cache (-1, say)
    are left out. Where two tokens of one call name the same slot, what that slot then
    holds is unspecified (every other slot is as it should be). T = 0 is a no-op;
-   T < 2^31. */
+   T < 2^28. */
 ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int64_t k_stride,
                        const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
                        void* stream);
 
 /* The values held in slots [T] int32 (any number of times each), to k and v [T, cache heads,
    head_dim] of dtype dt, contiguous; zeros for a slot outside the cache. A bf16 output is
-   rounded once. T = 0 is a no-op; T < 2^31. */
+   rounded once. T = 0 is a no-op; T < 2^28. */
 ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T, int32_t dt,
                       void* k, void* v, void* stream);
 
@@ -413,9 +414,10 @@ ar_status ar_kv4_attention_workspace_size(const ar_kv4_cache* cache, int64_t B, 
    scale, are rounded to f16, and the matrix unit cuts products off: a score is off by up to
    2^-17 of a key's scale times the largest |q| for each channel, an output by 2^-13 of the
    largest weight times scale of 8 neighbouring tokens for each token. B*new_tokens = 0 is a no-op;
-   new_tokens <= 256, B*heads*new_tokens < 2^31. No host synchronisation: the call can be captured in a
-   HIP graph and replayed with other lengths and tables. Two calls that may overlap need
-   workspaces of their own. */
+   new_tokens <= 256, B*heads*new_tokens < 2^31, and B*(cache heads)*ceil(rows/16) < 2^23 for
+   the new_tokens*heads/(cache heads) rows of a key head. No host synchronisation: the call can
+   be captured in a HIP graph and replayed with other lengths and tables. Two calls that may
+   overlap need workspaces of their own. */
 ar_status ar_kv4_attention(const ar_kv4_cache* cache, const uint16_t* q, int64_t q_stride,
                            int64_t B, int64_t new_tokens, int64_t heads, const int32_t* table,
                            int64_t width, const int32_t* lengths, int64_t max_len, float scale,

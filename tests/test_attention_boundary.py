@@ -50,7 +50,7 @@ def test_cache_validation(f):
         assert f(c=cache(**kw)) == INV, kw
     assert f(c=ctypes.POINTER(ar.ArKv4Cache)()) == INV
     assert f(dt=2) == UNSUP
-    assert f(T=-1) == f(T=1 << 31) == SHAPE
+    assert f(T=-1) == f(T=1 << 31) == f(T=1 << 28) == SHAPE     # (a launch holds 2^32 threads)
     for kw in (dict(k=NULL), dict(v=NULL), dict(slots=NULL), dict(k=P4), dict(v=P4), dict(slots=P2)):
         assert f(**kw) == INV
     assert f(T=0) == f(T=0, k=NULL, v=NULL, slots=NULL) == OK
@@ -74,7 +74,7 @@ def test_kv4_attention_validation():
     for kw in BAD_ARRAYS:
         assert attention(c=cache(**kw)) == INV, kw
     for kw in (dict(H=7), dict(H=0), dict(H=1024, qs=1024 * 128), dict(n=-1), dict(n=257),
-               dict(B=-1), dict(B=1 << 31), dict(B=1 << 28), dict(max_len=-1), dict(max_len=257),
+               dict(B=-1), dict(B=1 << 31), dict(B=1 << 28), dict(B=1 << 22), dict(max_len=-1), dict(max_len=257),
                dict(width=1 << 25), dict(width=-1), dict(qs=1016), dict(qs=1028),
                dict(max_len=1 << 30, width=1 << 24)):
         assert attention(**kw) == SHAPE, kw
@@ -115,7 +115,8 @@ def test_packed_validation():
     for kw in (dict(H=7), dict(Hk=0), dict(H=0), dict(H=1024, qs=1024 * 128), dict(B=-1),
                dict(B=65537), dict(Tq=-1), dict(Tk=-1), dict(Tk=5), dict(Tq=1 << 31),
                dict(Tq=1 << 28, Tk=1 << 28), dict(Tk=1 << 30, ko=P), dict(qs=1016), dict(ks=252), dict(vs=128),
-               dict(ks=1 << 22)):
+               dict(ks=1 << 22), dict(Tq=1 << 27, Tk=1 << 27),
+               dict(B=65536, Tq=65536, Tk=65536, H=64, Hk=64, qs=8192, ks=8192, vs=8192)):
         assert packed(**kw) == SHAPE, kw
     for kw in (dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(qo=NULL), dict(out=NULL), dict(q=P4),
                dict(k=P4), dict(v=P4), dict(out=P4), dict(qo=P2), dict(ko=P2), dict(lse=P2),
