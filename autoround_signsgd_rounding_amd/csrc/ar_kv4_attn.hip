@@ -691,12 +691,22 @@ struct Plan {
 };
 Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max_len) {
   Plan p;
-  p.RT = rows > 16 && DH / GS < 4 ? 2 : 1;   // (two rows of four groups do not fit)
-  p.tiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
+  // 512 workgroups run at once (2 x 131072 tokens: 63.2 us; 256 wanted 80.5, 1024 70.9), of
+  // 256 tokens at least (1 x 2000: 10.3; of 512 11.8, of 128 10.0)
   p.least = 256;
   p.target = 9;
+  // Up to 1024 tokens, eight waves of four tiles each are done before a join would be, unless
+  // there are many (8 x 900 tokens, 8 key heads: 9.8 us, divided 10.7; 1 x 2000: 13.7, divided
+  // 10.3; 64 x 900: 17.5 and 18.8).
+  p.wide = B * heads * ((rows + 15) / 16) <= 512 && max_len > 256 && max_len <= 1024;
+  // Two tiles of rows halve what each token's codes cost, where there is enough of that (8 key
+  // heads, 32 rows; 8 x 8192 tokens: 29.9 us instead of 33.2; 64 x 1200: 36.0 and 43.1), and the
+  // time of a single workgroup counts where there is not (2 x 8192: 22.1 instead of 18.0;
+  // 32 x 1500: 15.8 and 15.6). Those of four groups do not fit.
+  p.RT = !p.wide && rows > 16 && DH / GS < 4 && B * heads * max_len >= 3 << 17 ? 2 : 1;
+  p.tiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   const int64_t per = heads * p.tiles;
-  p.wide = p.RT == 1 && B * per <= 512 && max_len > 256 && max_len <= 1024;
+  // (300 x up to 4000 tokens, 8 key heads: 72.3 us, divided 85.4; 150 of them: 46.5 either way)
   p.whole = p.wide || max_len <= p.least || B * per >= int64_t(4) << p.target;
   p.groups = (B + (p.whole ? 0 : ((int64_t(1) << p.target) + per - 1) / per)) * per;
   return p;
@@ -718,6 +728,9 @@ void launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
 template <int DH>
 void join(const AttnArgs& a, const Plan& p, hipStream_t st) {
   constexpr int ALL = NT / (DH / 4);
+  // one group a row where there are many rows (32 x up to 8192 tokens, 64 rows: 38.9 us and
+  // 41.0 by all groups; 150 x up to 4000: 46.5 and 55.6), all of them for the many parts of
+  // few rows (2 x 30000 tokens: 24.2 us and 27.2 by one)
   const int64_t units = (int64_t)a.B * a.c.heads;
   if (units * a.rows >= 2048)
     hipLaunchKernelGGL((k_kv4_join<DH, 1>), dim3((unsigned)(units * ((a.rows + ALL - 1) / ALL))),

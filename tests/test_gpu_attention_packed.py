@@ -57,6 +57,7 @@ CASES = [  # queries, keys (None: the same), heads, key heads, head_dim
     ([40, 3, 100], [10, 0, 99], 4, 2, 128),     # fewer keys than queries: rows that see nothing
     ([2, 2], [0, 0], 2, 1, 64),
     ([9], [70], 256, 1, 64),                    # the largest group
+    ([3], [5], 300, 300, 64),                   # many key heads
 ]
 
 
@@ -213,6 +214,79 @@ def test_few_queries_behind_a_long_prefix():
     qo, ko = offsets(lq), offsets(lk)
     r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True)
     verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, qo, ko, 128 ** -0.5, "chunk")
+
+
+def test_many_sequences_of_which_few_are_long():
+    """More sequences than a wave has lanes, the keys of two divided."""
+    log("packed few long ones of many")
+    rng = np.random.default_rng(13)
+    lq = [int(x) for x in rng.integers(0, 3, 100)]
+    lk = [int(x) for x in rng.integers(0, 60, 100)]
+    lq[5], lk[5], lq[80], lk[80] = 2, 3100, 1, 2600
+    (Q, q), (K, k), (V, v) = problem(14, lq, lk, 4, 1, 128)
+    qo, ko = offsets(lq), offsets(lk)
+    r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True)
+    verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, qo, ko, 128 ** -0.5, "few")
+
+
+def test_divided_keys_and_hidden_infinities():
+    """The last part of the keys holds an infinity that only the later queries see."""
+    log("packed divided, hidden infinity")
+    lq, lk, H, Hk, D = [40], [5000], 4, 2, 64
+    (Q, q), (K, k), (V, v) = problem(22, lq, lk, H, Hk, D)
+    V[4990, 0, 5] = np.inf
+    r = ar.attention_packed(Q, K, V, i32([0, 40]), k_offsets=i32([0, 5000]), want_lse=True)
+    got, lse = r.out.double().cpu().numpy(), r.lse.cpu().numpy()
+    out, l, size, mag = oracle_heads(q, k, v, R.causal(40, 5000), D ** -0.5)
+    bound = out_bound(out, size, mag, D, 5000, P_BITS)
+    check(got[:30], out[:30], bound[:30], "in front of it")
+    check(got[30:, 2:], out[30:, 2:], bound[30:, 2:], "the other key head's")
+    check(lse, l, lse_bound(l, mag, D, 5000), "lse")
+    assert (got[30:, :2, 5] == np.inf).all()
+
+
+@pytest.mark.parametrize("bad", [None, np.nan])
+def test_many_tiles(bad):
+    """More workgroups than run at once: prompts of very different lengths, 64 heads; rows in
+    front of a NaN among the values."""
+    log(f"packed many tiles {bad}")
+    lq, H, Hk, D = [1000, 1, 0, 700, 31, 32, 33, 1200, 64, 200], 64, 8, 128
+    (Q, q), (K, k), (V, v) = problem(23, lq, lq, H, Hk, D)
+    qo = offsets(lq)
+    if bad is not None:
+        V[qo[1] - 1, 1] = bad                  # the last token of the first sequence
+    r = ar.attention_packed(Q, K, V, i32(qo), want_lse=True)
+    got, lse = r.out.double().cpu().numpy(), r.lse.cpu().numpy()
+    hit = got[qo[1] - 1, 8:16].copy()
+    assert np.isnan(hit).all() == (bad is not None)
+    for h in (0, 13, 63):
+        if bad is not None and h // 8 == 1:
+            got[qo[1] - 1, h] = 0
+            o = oracle_heads(q[:1000, h:h + 1], k[:1000, 1:2], v[:1000, 1:2], R.causal(1000, 1000),
+                             D ** -0.5)
+            check(got[:999, h:h + 1], o[0][:999],
+                  out_bound(o[0], o[2], o[3], D, 1000, P_BITS)[:999], "in front of it")
+            continue
+        one = lambda x, i: x[:, i:i + 1]        # noqa: E731
+        verify(one(got, h), one(lse, h), one(q, h), one(k, h // 8), one(v, h // 8), qo, qo,
+               D ** -0.5, f"many tiles {h}")
+
+
+def test_tokens_far_apart():
+    """Tokens at the largest stride: offsets pass 2^32 elements."""
+    log("packed far apart")
+    H, Hk, D, T, S = 4, 2, 128, 1100, (1 << 22) - 8
+    rng = np.random.default_rng(24)
+    base = torch.empty(T * S, dtype=torch.bfloat16, device=dev())
+    x = base.view(T, S)[:, :(H + 2 * Hk) * D].unflatten(1, (H + 2 * Hk, D))
+    X, f = bf16(rng.normal(size=x.shape))
+    x.copy_(X)
+    qo = offsets([1060, 40])
+    r = ar.attention_packed(x[:, :H], x[:, H:H + Hk], x[:, H + Hk:], i32(qo), want_lse=True)
+    verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), f[:, :H], f[:, H:H + Hk],
+           f[:, H + Hk:], qo, qo, D ** -0.5, "far apart")
+    del base, x
+    torch.cuda.empty_cache()
 
 
 def test_equals_the_blocks_attention():

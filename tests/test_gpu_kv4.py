@@ -215,6 +215,8 @@ CASES = [  # lengths, new, heads, key heads, head_dim, page, group
     ([2, 0], 3, 2, 2, 128, 64, 32),
     ([50], 1, 256, 1, 64, 16, 32),                  # the largest group
     ([260], 3, 17, 1, 128, 256, 128),
+    ([40, 300], 256, 2, 1, 64, 32, 64),             # the most new tokens, more than there are
+    ([20], 2, 300, 300, 64, 16, 32),                # many key heads
 ]
 
 
@@ -249,6 +251,54 @@ def test_long_sequences(H, heads, new, group):
     compare(tight, q, ks, vs, new, "bounded")
     cut = ar.kv4_attention(Q, cache, table, i32(lengths), max_len=1000, want_lse=True)
     compare(cut, q, [k[:1000] for k in ks], [v[:1000] for v in vs], new, "cut")
+
+
+@pytest.mark.parametrize("lengths,new,H,heads,D,P,group", [
+    ([300, 3, 65], 4, 8, 1, 128, 64, 128), ([600], 8, 8, 1, 128, 32, 64), ([90, 2000], 5, 14, 2, 64, 16, 32),
+    ([1500, 700, 5], 3, 24, 3, 64, 128, 64), ([700], 17, 4, 2, 128, 16, 32)])
+def test_room_for_long_sequences(lengths, new, H, heads, D, P, group):
+    """Many rows a key head, under a table that has room for a great deal more."""
+    log(f"kv4 room {lengths} new {new} heads {H}/{heads} x {D} page {P} group {group}")
+    rng = np.random.default_rng(sum(lengths))
+    cache, table, ks, vs = filled(rng, lengths, heads, D, P, group)
+    width = -(-400000 // (len(lengths) * heads * P))
+    wide = torch.full((len(lengths), width), -1, dtype=torch.int32, device=dev())
+    wide[:, :table.shape[1]] = table
+    Q, q = bf16(1.5 * rng.normal(size=(len(lengths), new, H, D)))
+    got = ar.kv4_attention(Q, cache, wide, i32(lengths), want_lse=True)
+    compare(got, q, ks, vs, new, "room")
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_many_short_sequences(new):
+    """More sequences than a wave has lanes, 8 query heads a key head."""
+    log(f"kv4 many short sequences, new {new}")
+    rng = np.random.default_rng(31)
+    lengths = [int(x) for x in rng.integers(0, 40, 400)]
+    lengths[350] = 230
+    cache, table, ks, vs = filled(rng, lengths, 4, 64, 16, 64)
+    Q, q = bf16(1.5 * rng.normal(size=(400, new, 32, 64)))
+    got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+    compare(got, q, ks, vs, new, "many")
+
+
+def test_strided_queries():
+    """Queries [B, n] within a larger array, all of whose tokens lie one stride apart; what
+    does not is refused."""
+    log("kv4 strided queries")
+    rng = np.random.default_rng(32)
+    cache, table, ks, vs = filled(rng, [50, 20], 2, 64, 32, 64)
+    n = i32([50, 20])
+    X, x = bf16(rng.normal(size=(2, 3, 8, 64)))
+    got = ar.kv4_attention(X[:, :, 2:6], cache, table, n, want_lse=True)
+    assert got.out.is_contiguous()
+    compare(got, x[:, :, 2:6], ks, vs, 3, "strided")
+    got = ar.kv4_attention(X[:, 1:2, 2:6], cache, table, n, want_lse=True)
+    compare(got, x[:, 1:2, 2:6], ks, vs, 1, "one of three")
+    got = ar.kv4_attention(X[1:, 1:, 2:6], cache, table[1:], n[1:], want_lse=True)
+    compare(got, x[1:, 1:, 2:6], ks[1:], vs[1:], 2, "one sequence")
+    with pytest.raises(ValueError, match="one stride apart"):
+        ar.kv4_attention(X[:, 1:, 2:6], cache, table, n)
 
 
 def test_pages_that_are_not_there():
