@@ -5,7 +5,9 @@
 // A workgroup takes 128 rows, 32 a wave, of one sequence and key head. Rows are the
 // queries of all the heads that share it, token by token: keys and values are staged once
 // for the group, and a short prompt fills a tile with its heads. Keys and values pass
-// through LDS in tiles of 64 tokens, two stages, loaded straight to LDS.
+// through LDS in tiles of 64 or 32 tokens, two stages, loaded straight to LDS, their 16-byte
+// chunks turned by the row so that no read meets a bank twice. Tiles that every row sees whole
+// go through a loop without masks. A sequence's last rows, which see the most keys, come first.
 //
 // Scores are formed transposed, Sᵀ = K·Qᵀ on v_mfma_f32_32x32x16_bf16, so a lane holds one
 // row's scores of half the tile's tokens. Which token is which row of K is chosen so that
@@ -16,6 +18,13 @@
 // risen by more than 8; p is rounded to bf16 for the product (2^-9 of each weight, about as
 // much in the output as its own rounding to bf16), the sums of p and all accumulators are
 // float32.
+//
+// The matrix unit and what feeds it bound long prompts. Measured, counting the causal half:
+// 16384 tokens, 64 heads of 128 over 8: 3748 us, 1.17 PFLOP/s (a large library product: 1.23),
+// the unit busy 67% of the cycles at 1.63 GHz; 8 x 2048 tokens, 32 heads of 128: 311 us, 0.88
+// PFLOP/s, where 4096 workgroups go in 5.3 rounds and each has 17 tiles of 64 keys in the mean;
+// 16384 tokens, 32 heads of 64 over 8: 1100 us, 1.0 PFLOP/s, half as much product for each
+// exponential; 37 tokens: 5 us, a launch and four tiles one after the other.
 #include <math.h>
 
 #include <type_traits>
@@ -27,10 +36,13 @@ namespace {
 
 constexpr int NT = 256, BM = 128;
 constexpr int GRAIN = 64;   // parts of the keys are a multiple of that
-// With few tiles the keys are divided: workgroups wanted, keys of one at least. (A part
-// costs its rows in float32, written and read, as much as 256 keys and values at 128 channels.)
+// With few tiles the keys are divided: workgroups wanted (as many as run at once), keys of one at
+// least. A part costs its rows in float32, written and read, as much as 256 keys and values at
+// 128 channels. (32 heads of 128 over 8; 2048 tokens: 48.8 us, 768 or 1024 wanted 69; 64 tokens
+// behind 16000: 38.5, parts of 512 keys 49.2; 1000 tokens: 24.2 and 31.)
 constexpr int TARGET = 512, LEAST = 1024;
-constexpr int PER = 8;       // workgroups that join the parts of a tile
+constexpr int PER = 8;       // workgroups that join the parts of a tile (64 tokens behind 16000:
+                             // 38.6 us; 4 of them 48.7)
 constexpr int MANY = 1536;   // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
@@ -184,7 +196,8 @@ __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, cons
 
 // KT keys a tile. 64 wait less often; 32 leave registers and LDS for a third workgroup on a
 // CU, which pays where there are more of them than run at once (16384 tokens, 64 heads of 128 over
-// 8: 3832 us instead of 3976; 1000 tokens, 32 over 8: 26.6 instead of 24.2).
+// 8: 3832 us instead of 3976; 1000 tokens, 32 over 8: 26.6 instead of 24.2). With 64 channels
+// four workgroups fit anyway (16384 tokens, 32 heads over 8: 1127 us instead of 1100).
 template <int DH, bool PARTS, int KT>
 __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args a) {
   constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
@@ -447,7 +460,9 @@ __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
   }
 }
 
-// The keys are divided where there are too few tiles for the GPU.
+// The keys are divided where there are too few tiles for the GPU, so far as the host can tell
+// (256 x up to 20 tokens, 8 heads over 2: 5.7 us, divided 19.1; 150 x 8 tokens behind 3000, 32
+// over 8: 294 and 317; 64 tokens behind 16000: see above).
 struct Plan {
   int64_t tiles, groups;   // tiles and workgroups at most, both times key heads
   bool parts;

@@ -6,8 +6,9 @@
 // The cache is read once and nothing else is large, so memory bounds it; what the codes
 // cost on the way is kept below that. The products run on v_mfma_f32_16x16x32_f16 with the
 // codes themselves on the cache's side: masked out of a word, (word & 0x000F000F) is two f16
-// subnormals, code·2^-24, which the matrix unit takes; one instruction for two codes. What the zero-points take off, Σ q·zp and Σ p·vs·zp, is one more such product each,
-// and the scales stay outside: ks multiplies the finished score, vs the weight.
+// subnormals, code·2^-24, which the matrix unit takes; one instruction for two codes. What the
+// zero-points take off, Σ q·zp and Σ p·vs·zp, is one more such product each, and the scales
+// stay outside: ks multiplies the finished score, vs the weight.
 //
 // q goes to f16 as q·2^k, its row's largest magnitude in [2^11, 2^12): exact but for what
 // lies 2^-31 below that. A row is one query head of one new token; up to 16·RT rows share a
@@ -21,9 +22,16 @@
 // the maximum only when that has risen by more than 8 (p <= 256); the sums of p and all
 // accumulators are float32.
 //
-// Each wave goes through its tokens alone, 32 at a time, and asks for the next keys once the
-// scores are formed, for the next values once the product is; the waves of a workgroup are joined in LDS, and the workgroups that
-// share a long sequence through the workspace, in order.
+// Each wave goes through its tokens alone, 32 at a time. A tile goes straight to one of two
+// LDS stages of the wave, and the one after next is asked for as soon as it has been used; no
+// wave waits for another until all are joined in LDS, and the workgroups that share a long
+// sequence are joined through the workspace, in order. How the sequences are divided follows
+// from their lengths, on the device: every workgroup makes the same plan.
+//
+// Measured: 2 x 131072 tokens, 64 heads over 8 of 128, groups of 64 (302 MB) 63 us, 4.8 TB/s;
+// 64 x 8192, groups of 128 (570 MB) 103 us, 5.5 TB/s; 64 x up to 8192 (123 MB) 39 us, 3.2 TB/s,
+// where plan, joins and the last workgroups' ends are a third; one sequence of 1000 tokens,
+// 32 heads, 10 us, a chain of launch, lengths, table, tiles and joins with nothing to hide it under.
 #include <math.h>
 
 #include <type_traits>
