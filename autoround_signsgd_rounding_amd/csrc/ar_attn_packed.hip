@@ -79,28 +79,6 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   return s;
 }
 
-// Sum over a wave, from lane 0 to the lane's own.
-template <class T>
-__device__ __forceinline__ T wave_scan(T x) {
-  auto add = [&](auto ctrl, auto rows) {
-    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
-                                              decltype(rows)::value, 0xF, false);
-    x += __builtin_bit_cast(T, o);
-  };
-  using std::integral_constant;
-  add(integral_constant<int, 0x111>(), integral_constant<int, 0xF>());   // from 1, 2, 4, 8 lanes
-  add(integral_constant<int, 0x112>(), integral_constant<int, 0xF>());   // before in the row
-  add(integral_constant<int, 0x114>(), integral_constant<int, 0xF>());
-  add(integral_constant<int, 0x118>(), integral_constant<int, 0xF>());
-  add(integral_constant<int, 0x142>(), integral_constant<int, 0xA>());   // from the rows before
-  add(integral_constant<int, 0x143>(), integral_constant<int, 0xC>());
-  return x;
-}
-template <class T>
-__device__ __forceinline__ T wave_last(T x) {
-  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-}
-
 __device__ __forceinline__ int tiles_of(const Args& a, const Seq& s) {
   return (int)(((int64_t)s.nq * a.ratio + BM - 1) / BM);
 }
@@ -112,8 +90,8 @@ __device__ __forceinline__ int chunk_of(const Args& a) {
     const Seq s = seq_of(a, b);
     work += (float)tiles_of(a, s) * (float)s.nk;
   }
-  // (above the quotient, so that there are no more parts than workgroups)
-  const float each = wave_last(wave_scan(work)) * (float)a.kv_heads * (1.0f / TARGET) + 1.0f;
+  // (above the quotient whatever the roundings, so that there are no more parts than workgroups)
+  const float each = wave_total(wave_scan(work)) * (float)a.kv_heads * (1.001f / TARGET) + 1.0f;
   const int c = (int)fminf(fmaxf(each, (float)LEAST), 0x1p30f);
   return __builtin_amdgcn_readfirstlane((c + GRAIN - 1) / GRAIN * GRAIN);
 }
@@ -150,8 +128,8 @@ __device__ __forceinline__ bool find_unit(const Args& a, int chunk, int at, bool
       u.before = units + __builtin_amdgcn_readlane(all - m, l) + (int64_t)tile * p;
       return true;
     }
-    before += wave_last(sum);
-    units += wave_last(all);
+    before += wave_total(sum);
+    units += wave_total(all);
   }
   return false;
 }
@@ -172,7 +150,7 @@ __device__ __forceinline__ bool find_tile(const Args& a, int at, Unit& u) {
   }
   const int cut = (int)group_max<64>((float)top) / 4;
   const int early = min(max(top - cut, 0), tiles);
-  const int sum = wave_scan(early), all = wave_last(sum);
+  const int sum = wave_scan(early), all = wave_total(sum);
   const bool late = at >= all;
   const int n = late ? tiles - early : early, upto = late ? wave_scan(n) : sum;
   const int in = late ? at - all : at;

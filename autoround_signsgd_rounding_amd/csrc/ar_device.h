@@ -101,6 +101,25 @@ __device__ __forceinline__ float group_max(float x) {
   for (int o = LPG / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
   return x;
 }
+// Sum over a wave from lane 0 to the lane's own; of all lanes, from such sums.
+template <int CTRL, int ROWS, class T>
+__device__ __forceinline__ T scan_step(T x) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false);
+  return x + __builtin_bit_cast(T, o);
+}
+template <class T>
+__device__ __forceinline__ T wave_scan(T x) {
+  x = scan_step<0x111, 0xF>(x);   // from 1, 2, 4, 8 lanes before in the row
+  x = scan_step<0x112, 0xF>(x);
+  x = scan_step<0x114, 0xF>(x);
+  x = scan_step<0x118, 0xF>(x);
+  x = scan_step<0x142, 0xA>(x);   // from the rows before
+  return scan_step<0x143, 0xC>(x);
+}
+template <class T>
+__device__ __forceinline__ T wave_total(T scanned) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scanned), 63));
+}
 
 // ---------------------------------------------------------------- quantizer
 // Static description of the integer grid.

@@ -34,8 +34,6 @@
 // 32 heads, 10 us, a chain of launch, lengths, table, tiles and joins with nothing to hide it under.
 #include <math.h>
 
-#include <type_traits>
-
 #include "ar_kv4.h"
 #include "ar_launch.h"
 
@@ -125,28 +123,6 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
-// Sum over a wave, inclusive of the lane's own and from lane 0 on.
-template <class T>
-__device__ __forceinline__ T wave_scan(T x) {
-  auto add = [&](auto ctrl, auto rows) {
-    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
-                                              decltype(rows)::value, 0xF, false);
-    x += __builtin_bit_cast(T, o);
-  };
-  using std::integral_constant;
-  add(integral_constant<int, 0x111>(), integral_constant<int, 0xF>());   // from 1, 2, 4, 8 lanes
-  add(integral_constant<int, 0x112>(), integral_constant<int, 0xF>());   // before in the row
-  add(integral_constant<int, 0x114>(), integral_constant<int, 0xF>());
-  add(integral_constant<int, 0x118>(), integral_constant<int, 0xF>());
-  add(integral_constant<int, 0x142>(), integral_constant<int, 0xA>());   // from the rows before
-  add(integral_constant<int, 0x143>(), integral_constant<int, 0xC>());
-  return x;
-}
-template <class T>
-__device__ __forceinline__ T wave_total(T scanned) {
-  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scanned), 63));
-}
-
 // How the sequences are divided, from their lengths alone and so the same for every
 // workgroup: into parts of `chunk` tokens, 2^target workgroups over all the tokens, and one
 // for what is left of each. The full parts come first, sequence by sequence, then the
@@ -170,8 +146,9 @@ __device__ __forceinline__ Division divide(const AttnArgs& a) {
   float tokens = (float)d.len0;   // (rounded alike everywhere)
   for (int b = lane + 64; b < a.B; b += 64) tokens += (float)length_of(a, b);
   const float each = wave_total(wave_scan(tokens)) * (float)(a.c.heads * a.tiles) *
-                     ldexpf(1.0f, -a.target);
-  // (above `each`, so that there are no more full parts than workgroups; no length is 2^30)
+                     ldexpf(1.001f, -a.target);
+  // (above the quotient whatever the roundings, so that there are no more full parts than
+  // workgroups; no length is 2^30)
   const int c = (int)fminf(fmaxf(each + 1.0f, (float)a.least), 0x1p30f);
   d.chunk = __builtin_amdgcn_readfirstlane((c + GRAIN - 1) / GRAIN * GRAIN);
   d.full = 0;
