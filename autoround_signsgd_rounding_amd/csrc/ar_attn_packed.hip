@@ -213,7 +213,13 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
   constexpr int TILE = KT * ROW;                   // bytes of a tile of keys or values
   constexpr int LD = TILE / (NT * 16), LROWS = NT / C;   // loads a wave, rows between them
   constexpr int ND = DH / 32, NC = DH / 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][TILE];
+  // Two stages of keys and values. With an array for each, the long loop going by twos, the
+  // values' reads need not wait for the next tile's loads (16384 tokens, 64 heads of 128 over 8:
+  // 3717 us instead of 3787). With 64 channels the registers for that cost a workgroup on each CU (8 x
+  // 2048, 32 heads: 177 us instead of 173).
+  constexpr bool APART = DH == 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[(APART ? 2 : 4) * TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[APART ? 2 * TILE : 16];
 
   const int kvh = blockIdx.x % a.kv_heads, at = blockIdx.x / a.kv_heads;
   const int chunk = PARTS ? chunk_of(a) : 0;
@@ -251,7 +257,7 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
   const uint32_t vvo = (uint32_t)(lrow * a.v_stride * 2 + ((lpos ^ vswz) << 4));
   const uint16_t* kb = a.k + (int64_t)k0 * a.k_stride + kvh * DH;
   const uint16_t* vb = a.v + (int64_t)k0 * a.v_stride + kvh * DH;
-  auto stage = [&](int t0, int s) {
+  auto stage = [&](int t0, uint8_t* to) {
     const int n = min(nk - t0, KT);
     const auto bk = make_rsrc(kb + (int64_t)t0 * a.k_stride,
                               (uint32_t)(((n - 1) * a.k_stride + DH) * 2));
@@ -259,15 +265,15 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
                               (uint32_t)(((n - 1) * a.v_stride + DH) * 2));
 #pragma unroll
     for (int j = 0; j < LD; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bk, AR_LDS(&lds[s][0][(j * 4 + wave) * 1024]), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bk, AR_LDS(to + (j * 4 + wave) * 1024), 16,
                                                kvo + (uint32_t)(j * LROWS * a.k_stride * 2), 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < LD; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bv, AR_LDS(&lds[s][1][(j * 4 + wave) * 1024]), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bv, AR_LDS(to + TILE + (j * 4 + wave) * 1024), 16,
                                                vvo + (uint32_t)(j * LROWS * a.v_stride * 2), 0, 0, 0);
   };
 
-  if (kend > kfirst) stage(kfirst, 0);
+  if (kend > kfirst) stage(kfirst, lds0);
 
   const uint16_t* qp = a.q + (int64_t)(q0 + i) * a.q_stride + head * DH;
   bf16x8_t qf[NC];
@@ -356,19 +362,32 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
       }
   };
 
-  int t0 = kfirst, s = 0;
-  auto step = [&](auto masked) {
+  int t0 = kfirst;
+  auto step = [&](auto masked, uint8_t* now, uint8_t* next) {
     __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of the tile (vmcnt 0)
     __syncthreads();                      // everybody's; and the other stage has been read
-    if (t0 + KT < kend) stage(t0 + KT, s ^ 1);
-    if (!decltype(masked)::value || t0 < wend) work(masked, t0, lds[s][0], lds[s][1]);
+    if (t0 + KT < kend) stage(t0 + KT, next);
+    if (!decltype(masked)::value || t0 < wend) work(masked, t0, now, now + TILE);
     t0 += KT;
-    s ^= 1;
   };
   // tiles that every row of the workgroup sees whole, then the others
-  const int kfull = r0 / a.ratio + nk - nq + 1;
-  while (t0 + KT <= min(kfull, kend)) step(std::false_type());
-  while (t0 < kend) step(std::true_type());
+  const int full = min(r0 / a.ratio + nk - nq + 1, kend) - KT;
+  int s = 0;
+  auto of = [&](int s) { return APART ? s ? lds1 : lds0 : lds0 + s * 2 * TILE; };
+  while (t0 <= full) {
+    if constexpr (APART) {
+      step(std::false_type(), lds0, lds1);
+      if (t0 > full) {
+        s = 1;
+        break;
+      }
+      step(std::false_type(), lds1, lds0);
+    } else {
+      step(std::false_type(), of(s), of(s ^ 1));
+      s ^= 1;
+    }
+  }
+  for (; t0 < kend; s ^= 1) step(std::true_type(), of(s), of(s ^ 1));
 
   l += __shfl_xor(l, 32, 64);
   const int64_t to = (int64_t)(q0 + i) * a.heads + head;
