@@ -43,7 +43,7 @@ constexpr int GRAIN = 64;   // parts of the keys are a multiple of that
 constexpr int TARGET = 512, LEAST = 1024;
 constexpr int PER = 8;       // workgroups that join the parts of a tile (64 tokens behind 16000:
                              // 38.6 us; 4 of them 48.7)
-constexpr int MANY = 1536;   // workgroups from which on tiles are of 32 keys
+constexpr int MANY = 768;    // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
 
@@ -204,9 +204,10 @@ __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, cons
 }
 
 // KT keys a tile. 64 wait less often; 32 leave registers and LDS for a third workgroup on a
-// CU, which pays where there are more of them than run at once (16384 tokens, 64 heads of 128 over
-// 8: 3832 us instead of 3976; 1000 tokens, 32 over 8: 26.6 instead of 24.2). With 64 channels
-// four workgroups fit anyway (16384 tokens, 32 heads over 8: 1127 us instead of 1100).
+// CU, which pays where there are more of them than run at once (heads of 128; 16384 tokens, 64 over
+// 8: 3720 us instead of 3887; 4096, 32 over 8: 135 and 146; 3000: 83.1 and 80.8; 2048: 48.8 and
+// 47.8). With 64 channels four workgroups fit anyway (16384 tokens, 32 heads over 8: 1127 us
+// instead of 1100).
 template <int DH, bool PARTS, int KT>
 __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args a) {
   constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
