@@ -490,9 +490,15 @@ __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
   }
 }
 
-// The keys are divided where there are too few tiles for the GPU, so far as the host can tell
-// (256 x up to 20 tokens, 8 heads over 2: 5.7 us, divided 19.1; 150 x 8 tokens behind 3000, 32
-// over 8: 294 and 317; 64 tokens behind 16000: see above).
+// The keys are divided where there is at most a tile for each CU, and then where a sequence may
+// be so long that the time saved pays for the plan and the join: more than 1300 keys times the share
+// of TARGET that the tiles leave free. The host does not know the longest; it is taken for a
+// quarter of all keys at least. (32 heads of 128 over 8: 1500 tokens, 376 tiles, 34.9 us, divided
+// 50.3; 1200 behind 16000, 304 tiles, 261 and 294. 256 tiles: 2048 tokens, 16 heads over 4, 40.1
+// and 45.0; 4096 tokens, 8 heads, 71.3 and 64.0. 128 tiles: 4 x 100 behind 1500 27.4 and 31.1;
+// 2048 tokens, 8 heads, 38.5 and 31.3. 64 tiles: 512 behind 8000, 16 heads of 64 over 2, 79.5 and
+// 33.7.)
+constexpr int ONE_EACH = 256, PAYS = 1300;
 struct Plan {
   int64_t tiles, groups;   // tiles and workgroups at most, both times key heads
   bool parts;
@@ -502,7 +508,9 @@ Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads)
   const int64_t rows = Tq * (heads / kv_heads);
   // no fewer than the sequences': each of at most min(B, Tq) ends within a tile
   p.tiles = (rows + (B < Tq ? B : Tq) * (BM - 1)) / BM * kv_heads;
-  p.parts = p.tiles < TARGET && Tk > LEAST;
+  const int64_t tiles = (rows + BM - 1) / BM * kv_heads;   // .. at least
+  p.parts = p.tiles < TARGET && tiles <= ONE_EACH &&
+            Tk / (B < 4 ? B : 4) * (TARGET - tiles) > (int64_t)PAYS * TARGET;
   p.groups = p.tiles + (p.parts ? (TARGET + kv_heads - 1) / kv_heads * kv_heads : 0);
   return p;
 }

@@ -172,6 +172,20 @@ def test_offsets_that_lead_nowhere(qo):
     assert (whole[:32] == 7).all() and (whole[32 + T:] == 7).all()
 
 
+@pytest.mark.parametrize("qo", [[0, 9000, 100], [-5, 60, 1 << 30], [9000, 20, 5000, 10], [0, 6000, 0, 6000],
+                                [-1 << 31, (1 << 31) - 1], [6000, 6000]])
+def test_offsets_that_lead_nowhere_in_divided_calls(qo):
+    """The same where the keys are divided, sequences over each other among them."""
+    log(f"packed divided offsets {qo}")
+    T, H, D = 6000, 4, 64
+    (Q, _), (K, _), (V, _) = problem(3, [T], [T], H, 2, D)
+    whole = torch.full((T + 64, H, D), 7.0, dtype=torch.bfloat16, device=dev())
+    ar.attention_packed(Q, K, V, i32(qo), out=whole[32:32 + T])
+    ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(qo[::-1]), out=whole[32:32 + T])
+    torch.cuda.synchronize()
+    assert (whole[:32] == 7).all() and (whole[32 + T:] == 7).all()
+
+
 def test_many_sequences():
     """More sequences than a wave has lanes, most of them short or empty."""
     log("packed many sequences")
