@@ -36,11 +36,12 @@ namespace {
 
 constexpr int NT = 256, BM = 128;
 constexpr int GRAIN = 64;   // parts of the keys are a multiple of that
-// With few tiles the keys are divided: workgroups wanted (as many as run at once), keys of one at
-// least. A part costs its rows in float32, written and read, as much as 256 keys and values at
-// 128 channels. (32 heads of 128 over 8; 2048 tokens: 48.8 us, 768 or 1024 wanted 69; 64 tokens
-// behind 16000: 38.5, parts of 512 keys 49.2; 1000 tokens: 24.2 and 31.)
-constexpr int TARGET = 512, LEAST = 1024;
+// With few tiles the keys are divided: workgroups wanted, keys of one at least. A part costs its
+// rows in float32, written and read, as much as 256 keys and values at 128 channels. (8 heads of 128,
+// 4096 tokens: 55.7 us, 512 wanted 63.8, 1024 77.0; 4 heads over 1, 8192 tokens: 91.8, 113 and 123.
+// 64 tokens behind 16000, 32 heads over 8: 38.5, parts of 512 keys 49.0; 2048 tokens, 8 heads:
+// 31.6, parts of 768 keys 33.3.)
+constexpr int TARGET = 768, LEAST = 1024;
 constexpr int PER = 8;       // workgroups that join the parts of a tile (64 tokens behind 16000:
                              // 38.6 us; 4 of them 48.7)
 constexpr int MANY = 768;    // workgroups from which on tiles are of 32 keys
@@ -492,13 +493,13 @@ __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
 
 // The keys are divided where there is at most a tile for each CU, and then where a sequence may
 // be so long that the time saved pays for the plan and the join: more than 1300 keys times the share
-// of TARGET that the tiles leave free. The host does not know the longest; it is taken for a
+// of ROOM that the tiles leave free. The host does not know the longest; it is taken for a
 // quarter of all keys at least. (32 heads of 128 over 8: 1500 tokens, 376 tiles, 34.9 us, divided
 // 50.3; 1200 behind 16000, 304 tiles, 261 and 294. 256 tiles: 2048 tokens, 16 heads over 4, 40.1
 // and 45.0; 4096 tokens, 8 heads, 71.3 and 64.0. 128 tiles: 4 x 100 behind 1500 27.4 and 31.1;
 // 2048 tokens, 8 heads, 38.5 and 31.3. 64 tiles: 512 behind 8000, 16 heads of 64 over 2, 79.5 and
 // 33.7.)
-constexpr int ONE_EACH = 256, PAYS = 1300;
+constexpr int ONE_EACH = 256, ROOM = 512, PAYS = 1300;   // (512 workgroups run at once)
 struct Plan {
   int64_t tiles, groups;   // tiles and workgroups at most, both times key heads
   bool parts;
@@ -509,8 +510,8 @@ Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads)
   // no fewer than the sequences': each of at most min(B, Tq) ends within a tile
   p.tiles = (rows + (B < Tq ? B : Tq) * (BM - 1)) / BM * kv_heads;
   const int64_t tiles = (rows + BM - 1) / BM * kv_heads;   // .. at least
-  p.parts = p.tiles < TARGET && tiles <= ONE_EACH &&
-            Tk / (B < 4 ? B : 4) * (TARGET - tiles) > (int64_t)PAYS * TARGET;
+  p.parts = p.tiles < ROOM && tiles <= ONE_EACH &&
+            Tk / (B < 4 ? B : 4) * (ROOM - tiles) > (int64_t)PAYS * ROOM;
   p.groups = p.tiles + (p.parts ? (TARGET + kv_heads - 1) / kv_heads * kv_heads : 0);
   return p;
 }
