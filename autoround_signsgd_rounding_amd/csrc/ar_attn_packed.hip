@@ -20,11 +20,11 @@
 // float32.
 //
 // The matrix unit and what feeds it bound long prompts. Measured, counting the causal half:
-// 16384 tokens, 64 heads of 128 over 8: 3748 us, 1.17 PFLOP/s (a large library product: 1.23),
-// the unit busy 67% of the cycles at 1.63 GHz; 8 x 2048 tokens, 32 heads of 128: 311 us, 0.88
-// PFLOP/s, where 4096 workgroups go in 5.3 rounds and each has 17 tiles of 64 keys in the mean;
+// 16384 tokens, 64 heads of 128 over 8: 3694 us, 1.19 PFLOP/s (a large library product: 1.23),
+// the unit busy 71% of the cycles at 1.58 GHz; 8 x 2048 tokens, 32 heads of 128: 302 us, 0.91
+// PFLOP/s, where 4096 workgroups go in 5.3 rounds and each has 34 tiles of 32 keys in the mean;
 // 16384 tokens, 32 heads of 64 over 8: 1100 us, 1.0 PFLOP/s, half as much product for each
-// exponential; 37 tokens: 5 us, a launch and four tiles one after the other.
+// exponential; 37 tokens: 5 us, a launch and the first loads.
 #include <math.h>
 
 #include <type_traits>
