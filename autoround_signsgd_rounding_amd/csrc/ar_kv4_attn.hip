@@ -560,7 +560,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
       const int n0 = page_of(t + STAGES * STEP), n1 = page_of(t + STAGES * STEP + 16);
       scores(ring + i * Tl::BYTES);
       weigh(ring + i * Tl::BYTES, t, p0[i], p1[i]);
-      asm volatile("" ::: "memory");
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the tile has been read
       if (t + STAGES * STEP < last) fetch(t + STAGES * STEP, n0, n1, ring + i * Tl::BYTES);
       p0[i] = n0, p1[i] = n1;
     }
