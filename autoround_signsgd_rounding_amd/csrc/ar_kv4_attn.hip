@@ -130,8 +130,10 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
   return b < a.B ? min(max(a.lengths[b], 0), a.max_len) : 0;
 }
+constexpr int KEPT = 4;   // times 64 sequences whose lengths stay in registers
 struct Division {
-  int chunk, full, len0;   // tokens of a part, full parts in all, length of sequence `lane`
+  int chunk, full;   // tokens of a part, full parts in all
+  int len[KEPT];     // lengths of the sequences lane, lane + 64, ..
   __device__ __forceinline__ int full_of(int len) const { return (uint32_t)len / (uint32_t)chunk; }
   // a rest, or the one part of an empty sequence
   __device__ __forceinline__ int rest_of(int len) const {
@@ -139,22 +141,37 @@ struct Division {
   }
   __device__ __forceinline__ int parts_of(int len) const { return full_of(len) + rest_of(len); }
 };
+// f(base, length of sequence base + lane) for base = 0, 64, .. below `to`, while f is true.
+template <class F>
+__device__ __forceinline__ void each_64(const AttnArgs& a, const Division& d, int to, F f) {
+#pragma unroll
+  for (int i = 0; i < KEPT; ++i)
+    if (64 * i >= to || !f(64 * i, d.len[i])) return;
+  for (int base = 64 * KEPT; base < to; base += 64)
+    if (!f(base, length_of(a, base + (threadIdx.x & 63)))) return;
+}
 __device__ __forceinline__ Division divide(const AttnArgs& a) {
   const int lane = threadIdx.x & 63;
   Division d;
-  d.len0 = length_of(a, lane);
-  float tokens = (float)d.len0;   // (rounded alike everywhere)
-  for (int b = lane + 64; b < a.B; b += 64) tokens += (float)length_of(a, b);
+#pragma unroll
+  for (int i = 0; i < KEPT; ++i) d.len[i] = length_of(a, 64 * i + lane);
+  float tokens = 0.0f;   // (rounded alike everywhere)
+  each_64(a, d, a.B, [&](int, int len) {
+    tokens += (float)len;
+    return true;
+  });
   const float each = wave_total(wave_scan(tokens)) * (float)(a.c.heads * a.tiles) *
                      ldexpf(1.001f, -a.target);
   // (above the quotient whatever the roundings, so that there are no more full parts than
   // workgroups; no length is 2^30)
   const int c = (int)fminf(fmaxf(each + 1.0f, (float)a.least), 0x1p30f);
   d.chunk = __builtin_amdgcn_readfirstlane((c + GRAIN - 1) / GRAIN * GRAIN);
-  d.full = 0;
-  for (int base = 0; base < a.B; base += 64)
-    d.full += wave_total(wave_scan(
-        base + lane < a.B ? d.full_of(base ? length_of(a, base + lane) : d.len0) : 0));
+  int full = 0;
+  each_64(a, d, a.B, [&](int, int len) {
+    full += d.full_of(len);   // (0 beyond the last sequence)
+    return true;
+  });
+  d.full = wave_total(wave_scan(full));
   return d;
 }
 // Part `at` of all: sequence b's part `part`; false when there is none.
@@ -163,21 +180,22 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, const Division& d, 
   const int lane = threadIdx.x & 63;
   const bool whole = at < d.full;
   int before = whole ? 0 : d.full;
-  for (int base = 0; base < a.B; base += 64) {
-    const int mine = base ? length_of(a, base + lane) : d.len0;
+  bool found = false;
+  each_64(a, d, a.B, [&](int base, int mine) {
     const int n = base + lane < a.B ? (whole ? d.full_of(mine) : d.rest_of(mine)) : 0;
     const int sum = wave_scan(n);
     const uint64_t past = __ballot(before + sum > at);
-    if (past) {
+    found = past != 0;
+    if (found) {
       const int l = __ffsll((unsigned long long)past) - 1;
       b = base + l;
       len = __builtin_amdgcn_readlane(mine, l);
       part = whole ? at - before - __builtin_amdgcn_readlane(sum - n, l) : d.full_of(len);
-      return true;
     }
     before += wave_total(sum);
-  }
-  return false;
+    return !found;
+  });
+  return found;
 }
 
 // Four channels of a row's output from its sums relative to 2^m, and its lse.
@@ -631,12 +649,14 @@ __global__ __launch_bounds__(NT) void k_kv4_join(AttnArgs a, int R) {
   const int len = length_of(a, b), parts = d.parts_of(len);
   if (parts < 2) return;   // a single one has written its rows
   // parts of the sequences before this one
-  int full = 0, rests = d.full;
-  for (int base = 0; base < b; base += 64) {
-    const int mine = base ? length_of(a, base + lane) : d.len0;
-    full += wave_total(wave_scan(base + lane < b ? d.full_of(mine) : 0));
-    rests += wave_total(wave_scan(base + lane < b ? d.rest_of(mine) : 0));
-  }
+  int full = 0, rests = 0;
+  each_64(a, d, b, [&](int base, int mine) {
+    full += base + lane < b ? d.full_of(mine) : 0;
+    rests += base + lane < b ? d.rest_of(mine) : 0;
+    return true;
+  });
+  full = wave_total(wave_scan(full));
+  rests = d.full + wave_total(wave_scan(rests));
   const int whole = d.full_of(len);
   float mm = NO_MAX, sum = 0.0f;
   f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -691,8 +711,12 @@ Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max
   p.RT = !p.wide && rows > 16 && DH / GS < 4 && B * heads * max_len >= 3 << 17 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   const int64_t per = heads * p.tiles;
-  // (300 x up to 4000 tokens, 8 key heads: 72.3 us, divided 85.4; 150 of them: 46.5 either way)
-  p.whole = p.wide || max_len <= p.least || B * per >= int64_t(4) << p.target;
+  // Undivided, a call has neither plan nor join; what that saves is lost where few workgroups wait
+  // for a long one. (7 query heads a key head; 150 x up to 960 tokens, 4 key heads: 13.5 us,
+  // divided 19.7; 100 x 1000, 8: 28.7 and 31.6. 200 x up to 2000, 4: 23.1 and 24.3; 100 x 2000, 8:
+  // 50.1 and 53.4. 150 x up to 4000, 8: 46.2 and 44.0; 240: 67.1 and 71.3.)
+  const int64_t units = B * per;
+  p.whole = max_len <= (units > 512 ? 2048 : 1024) || units >= int64_t(4) << p.target;
   p.groups = (B + (p.whole ? 0 : ((int64_t(1) << p.target) + per - 1) / per)) * per;
   return p;
 }

@@ -282,6 +282,19 @@ def test_many_short_sequences(new):
     compare(got, q, ks, vs, new, "many")
 
 
+@pytest.mark.parametrize("B", [100, 300])
+def test_a_few_long_sequences_among_many(B):
+    """More sequences than a wave has lanes, and than it keeps lengths of, some of them divided."""
+    log(f"kv4 few long among {B}")
+    rng = np.random.default_rng(B)
+    lengths = [int(x) for x in rng.integers(0, 40, B)]
+    lengths[5], lengths[70], lengths[B - 1] = 1100, 2500, 2200
+    cache, table, ks, vs = filled(rng, lengths, 1, 64, 16, 64)
+    Q, q = bf16(1.5 * rng.normal(size=(B, 2, 4, 64)))
+    got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+    compare(got, q, ks, vs, 2, "few long")
+
+
 def test_strided_queries():
     """Queries [B, n] within a larger array, all of whose tokens lie one stride apart; what
     does not is refused."""
