@@ -56,12 +56,16 @@ struct AttnArgs {
   ArKv4 c;
   const int32_t *table, *lengths;
   int width, max_len, B, news, heads, ratio, rows, tiles;
-  int whole;               // sequences are not divided
   int target, least;       // log2 of the workgroups wanted; tokens of one at least
   float sl;                // scale·log2 e
   uint16_t* out;
   float* lse;
   float *po, *pm;          // partial sums [workgroup][row][Dh] and (m, l) of each row
+  // where the parts of a sequence went: how many there are, the full ones among them, the
+  // place of the first of these and that of the rest
+  struct Parts {
+    int all, full, first, rest;
+  } * parts;
 };
 
 // Codes as f16: a code at bit b of a half word is the subnormal code·2^(b - 24), which the
@@ -211,12 +215,14 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int a
 }
 
 // Waves a SIMD that the registers are held to. (From two on, products stay out of the
-// accumulation registers, which the softmax would have to copy from.)
+// accumulation registers, which the softmax would have to copy from. At 64 channels in groups of
+// 32 the divided form spills a register, outside its loop.)
 constexpr int occupancy(int DH, int G, int RT, int WAVES) {
   return WAVES == 8 || RT == 2 ? 2 : DH == 64 ? 4 : G == 4 ? 2 : 3;
 }
 
-template <int DH, int GS, int RT, int WAVES, int STAGES>
+// WHOLE: sequences are not divided.
+template <int DH, int GS, int RT, int WAVES, int STAGES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void k_kv4_attention(AttnArgs a) {
   constexpr int G = DH / GS, KW = GS / 32, NB = DH / 64, NO = DH / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -225,16 +231,16 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
   const int at = blockIdx.x / per, rest = blockIdx.x - at * per;
   const int h = rest / a.tiles, tile = rest - h * a.tiles;
   int b = at, len, first = 0, last;
-  bool joined = false;
-  if (a.whole) {
+  int chunk = 1 << 30;   // tokens of a part
+  if constexpr (WHOLE) {
     len = last = __builtin_amdgcn_readfirstlane(length_of(a, b));
   } else {
     const Division d = divide(a);
     int part;
     if (!find_part(a, d, at, b, part, len)) return;
-    joined = len > d.chunk;
     first = part * d.chunk;
     last = min(len, first + d.chunk);
+    chunk = d.chunk;
   }
 
   // the lane's row of each of the RT products and its queries
@@ -625,13 +631,18 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
       sum += f * sl[w][row];
       v += f * *reinterpret_cast<const f32x4_t*>(&so[w][row][c]);
     }
-    if (joined) {
+    if (!WHOLE && len > chunk) {
       const int64_t to = (int64_t)blockIdx.x * R + row;
       *reinterpret_cast<f32x4_t*>(a.po + to * DH + c) = v;
       if (c == 0) a.pm[2 * to] = mm, a.pm[2 * to + 1] = sum;
     } else {
       write_row<DH>(a, b, h, at, c, v, mm, sum);
     }
+  }
+  if (!WHOLE && rest == 0 && wave == 0) {   // (by all lanes alike)
+    const int full = len / chunk, all = full + (len == 0 || full * chunk < len);
+    if (first == full * chunk) a.parts[b].rest = at;
+    if (first == 0) a.parts[b].all = all, a.parts[b].full = full, a.parts[b].first = at;
   }
 }
 
@@ -641,36 +652,25 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 template <int DH, int GROUPS>
 __global__ __launch_bounds__(NT) void k_kv4_join(AttnArgs a, int R) {
   constexpr int LPR = DH / 4, ROWS = NT / LPR / GROUPS;   // rows a workgroup
-  const int lane = threadIdx.x & 63, each = (a.rows + ROWS - 1) / ROWS;
+  const int each = (a.rows + ROWS - 1) / ROWS;
   const int bh = blockIdx.x / each, b = bh / a.c.heads, h = bh - b * a.c.heads;
   const int row = (blockIdx.x - bh * each) * ROWS + threadIdx.x / LPR / GROUPS;
   const int g = threadIdx.x / LPR % GROUPS, c = threadIdx.x % LPR;
-  const Division d = divide(a);
-  const int len = length_of(a, b), parts = d.parts_of(len);
-  if (parts < 2) return;   // a single one has written its rows
-  // parts of the sequences before this one
-  int full = 0, rests = 0;
-  each_64(a, d, b, [&](int base, int mine) {
-    full += base + lane < b ? d.full_of(mine) : 0;
-    rests += base + lane < b ? d.rest_of(mine) : 0;
-    return true;
-  });
-  full = wave_total(wave_scan(full));
-  rests = d.full + wave_total(wave_scan(rests));
-  const int whole = d.full_of(len);
+  const AttnArgs::Parts p = a.parts[b];
+  if (p.all < 2) return;   // a single one has written its rows
   float mm = NO_MAX, sum = 0.0f;
   f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (row < a.rows) {
     const int64_t step = (int64_t)a.c.heads * a.tiles * R, from = (int64_t)h * a.tiles * R + row;
-    auto at = [&](int s) { return from + (s < whole ? full + s : rests) * step; };
-    for (int s = c; s < parts; s += LPR) mm = fmaxf(mm, a.pm[2 * at(s)]);
+    auto at = [&](int s) { return from + (s < p.full ? p.first + s : p.rest) * step; };
+    for (int s = c; s < p.all; s += LPR) mm = fmaxf(mm, a.pm[2 * at(s)]);
     mm = group_max<LPR>(mm);
 #pragma unroll 4
-    for (int s = g; s < parts; s += GROUPS) {
-      const int64_t p = at(s);
-      const float f = __builtin_amdgcn_exp2f(a.pm[2 * p] - mm);
-      sum += f * a.pm[2 * p + 1];
-      v += f * *reinterpret_cast<const f32x4_t*>(a.po + p * DH + 4 * c);
+    for (int s = g; s < p.all; s += GROUPS) {
+      const int64_t to = at(s);
+      const float f = __builtin_amdgcn_exp2f(a.pm[2 * to] - mm);
+      sum += f * a.pm[2 * to + 1];
+      v += f * *reinterpret_cast<const f32x4_t*>(a.po + to * DH + 4 * c);
     }
   }
   if constexpr (GROUPS > 1) {
@@ -721,18 +721,23 @@ Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max
   return p;
 }
 
+template <int DH, int GS, int RT>
+void launch_4(const AttnArgs& a, const Plan& p, hipStream_t st) {
+  const dim3 grid((unsigned)p.groups);
+  if (p.whole) hipLaunchKernelGGL((k_kv4_attention<DH, GS, RT, 4, 2, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((k_kv4_attention<DH, GS, RT, 4, 2, false>), grid, dim3(256), 0, st, a);
+}
 template <int DH, int GS>
 void launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
-  const dim3 grid((unsigned)p.groups);
   if constexpr (DH / GS < 4)
     if (p.RT == 2) {
-      hipLaunchKernelGGL((k_kv4_attention<DH, GS, 2, 4, 2>), grid, dim3(256), 0, st, a);
+      launch_4<DH, GS, 2>(a, p, st);
       return;
     }
   if (p.wide)
-    hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 8, 2>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 8, 2, true>), dim3((unsigned)p.groups), dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((k_kv4_attention<DH, GS, 1, 4, 2>), grid, dim3(256), 0, st, a);
+    launch_4<DH, GS, 1>(a, p, st);
 }
 template <int DH>
 void join(const AttnArgs& a, const Plan& p, hipStream_t st) {
@@ -751,11 +756,12 @@ void join(const AttnArgs& a, const Plan& p, hipStream_t st) {
 
 }  // namespace
 
-// Floats of the workspace: partial sums and (m, l) of every row of every workgroup.
+// Floats of the workspace: partial sums and (m, l) of every row of every workgroup, and where
+// the parts of each sequence went.
 int64_t ar_kv4_attention_floats(const ar_kv4_cache& c, int64_t B, int64_t news, int64_t heads,
                                 int64_t max_len) {
   const Plan p = plan_of(B, c.heads, c.head_dim, c.group_size, news * (heads / c.heads), max_len);
-  return p.whole ? 0 : p.groups * 16 * p.RT * (c.head_dim + 2);
+  return p.whole ? 0 : p.groups * 16 * p.RT * (c.head_dim + 2) + 4 * B;
 }
 
 ar_status ar_launch_kv4_attention(const ArKv4Attention& g, hipStream_t st) {
@@ -776,7 +782,6 @@ ar_status ar_launch_kv4_attention(const ArKv4Attention& g, hipStream_t st) {
   a.ratio = (int)(g.heads / c.heads);
   a.rows = (int)rows;
   a.tiles = p.tiles;
-  a.whole = p.whole;
   a.target = p.target;
   a.least = p.least;
   a.sl = (float)((double)g.scale * 1.4426950408889634);
@@ -784,6 +789,7 @@ ar_status ar_launch_kv4_attention(const ArKv4Attention& g, hipStream_t st) {
   a.lse = g.lse;
   a.po = g.ws;
   a.pm = g.ws + p.groups * 16 * p.RT * c.head_dim;
+  a.parts = reinterpret_cast<AttnArgs::Parts*>(a.pm + p.groups * 16 * p.RT * 2);
   const int DH = c.head_dim, GS = c.group_size;
   if (DH == 64 && GS == 32) launch<64, 32>(a, p, st);
   else if (DH == 64) launch<64, 64>(a, p, st);
