@@ -923,8 +923,11 @@ def _attention_outputs(q, out, want_lse, dev):
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif not _is(out, shape, torch.bfloat16, dev):
         _refuse(out, "out", shape, torch.bfloat16)
-    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
-    return out, lse
+    if not want_lse:
+        return out, None
+    *_, n, H, _ = shape
+    return out, torch.empty_strided(shape[:-1], (H, 1) if len(shape) == 3 else (n * H, H, 1),
+                                    dtype=torch.float32, device=dev)
 
 
 def attention_packed(q, k, v, offsets, *, k_offsets=None, scale=None, want_lse: bool = False,

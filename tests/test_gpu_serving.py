@@ -142,6 +142,38 @@ def test_graph(long):
             assert torch.equal(g, w)
 
 
+def test_graph_of_divided_keys():
+    """A chunk over thousands of keys in a graph, replayed with other offsets: of two sequences,
+    of one, with queries of no sequence, with no key in sight."""
+    log("serving graph divided")
+    rng = np.random.default_rng(6)
+    X, _ = qkv(rng, 6000)
+    q, k, v = parts(X)
+    q = q[:50].contiguous()
+    po, ko = i32([0, 20, 50]), i32([0, 3000, 6000])
+
+    def step():
+        return [*ar.attention_packed(q, k, v, po, k_offsets=ko, want_lse=True),
+                *ar.attention_packed(q, k, v, po, k_offsets=ko, want_lse=True, scale=0.5)]
+
+    step()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        with torch.cuda.graph(graph, stream=s):
+            captured = step()
+    torch.cuda.current_stream().wait_stream(s)
+    for p, o in (([0, 20, 50], [0, 3000, 6000]), ([0, 50, 50], [0, 6000, 6000]), ([10, 10, 40], [5, 7, 5990]),
+                 ([0, 1, 50], [0, 4000, 4000]), ([0, 20, 50], [0, 3000, 6000])):
+        po.copy_(i32(p))
+        ko.copy_(i32(o))
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip([t.clone() for t in captured], step()):
+            assert torch.equal(g[p[0]:p[2]], w[p[0]:p[2]])
+
+
 def test_streams():
     """The same calls on two streams at once, each with outputs and workspace of its own, and
     on a stream that is not the current one."""
@@ -172,6 +204,37 @@ def test_streams():
     for i in range(2):
         for o in got[i]:
             assert torch.equal(o, want[i] if o.shape == want[i].shape else prompt)
+
+
+def test_a_named_stream():
+    """Every call on a stream that it names, behind work of that stream; outputs and workspaces
+    are that stream's too."""
+    log("serving named stream")
+    rng = np.random.default_rng(5)
+    T = 3000
+    caches = [ar.kv4_cache(T // P + 1, HK, D, page_size=P) for _ in range(2)]
+    X, _ = qkv(rng, T)
+    slots, off, table, n = i32(np.arange(T)), i32([0, T]), i32(np.arange(T // P + 1)[None]), i32([T])
+
+    def chain(cache, x, **kw):
+        q, k, v = parts(x)
+        ar.kv4_write(k, v, cache, slots, **kw)
+        return [ar.attention_packed(q[-9:], k, v, i32([0, 9]), k_offsets=off, want_lse=True, **kw),
+                ar.kv4_attention(q[-1:], cache, table, n, want_lse=True, **kw),
+                ar.kv4_read(cache, slots, **kw)]
+
+    want = chain(caches[0], X)
+    s, late = torch.cuda.Stream(), torch.zeros_like(X)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            late.add_(0)
+        late.copy_(X)
+    got = chain(caches[1], late, stream=s)
+    s.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a, b)
 
 
 def test_same_bits_every_time():
