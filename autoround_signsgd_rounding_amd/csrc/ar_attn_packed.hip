@@ -172,9 +172,9 @@ __device__ __forceinline__ bool finite_bits(uint32_t pair) {
 
 // One row by the definition over the keys first .. last, by one wave: for a row whose product
 // met an infinity or a NaN of a value hidden from it (0·inf). The lane takes the channels
-// lane, lane + 64 of o.
+// lane, lane + 64 of o. False once all of o is NaN, m and l then being those of the keys so far.
 template <int DH>
-__device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, const uint16_t* k,
+__device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, const uint16_t* k,
                                           const uint16_t* v, int first, int last, float& m, float& l,
                                           float (&o)[DH / 64]) {
   const int lane = threadIdx.x & 63;
@@ -201,7 +201,12 @@ __device__ __forceinline__ void plain_row(const Args& a, const uint16_t* q, cons
       for (int d = 0; d < DH / 64; ++d)
         o[d] = fmaf(w, bf16_val(v[(int64_t)(t0 + j) * a.v_stride + lane + 64 * d]), o[d]);
     }
+    bool lost = true;
+#pragma unroll
+    for (int d = 0; d < DH / 64; ++d) lost = lost && o[d] != o[d];
+    if (__all(lost)) return false;
   }
+  return true;
 }
 
 // KT keys a tile. 64 wait less often; 32 leave registers and LDS for a third workgroup on a
@@ -440,15 +445,15 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
         redo &= redo - 1;
         const int ri = __shfl(i, r, 64), rh = __shfl(head, r, 64);
         float rm, rl, ro[DH / 64];
-        plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, kfirst,
-                      min(ri + nk - nq, kend - 1), rm, rl, ro);
+        const bool all = plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb,
+                                       kfirst, min(ri + nk - nq, kend - 1), rm, rl, ro);
         const int64_t rto = (int64_t)(q0 + ri) * a.heads + rh;
         const int64_t rpto = slot + 32 * wave + r;
 #pragma unroll
         for (int d = 0; d < DH / 64; ++d)
           if (joined) a.po[rpto * DH + lane + 64 * d] = ro[d];
           else a.out[rto * DH + lane + 64 * d] = (uint16_t)bf16_bits(ro[d] / rl);
-        if (joined && lane == 0) a.pm[2 * rpto] = rm, a.pm[2 * rpto + 1] = rl;
+        if (joined && all && lane == 0) a.pm[2 * rpto] = rm, a.pm[2 * rpto + 1] = rl;
       }
   }
 }
