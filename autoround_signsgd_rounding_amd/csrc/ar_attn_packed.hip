@@ -186,7 +186,16 @@ __device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, cons
     if (t0 + lane <= last) {
       const uint16_t* kr = k + (int64_t)(t0 + lane) * a.k_stride;
       s = 0.0f;
-      for (int d = 0; d < DH; ++d) s = fmaf(bf16_val(q[d]), bf16_val(kr[d]), s);
+#pragma unroll 4
+      for (int d = 0; d < DH; d += 8) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(q + d);
+        const u32x4_t y = *reinterpret_cast<const u32x4_t*>(kr + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
+          s = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), s);
+        }
+      }
       s *= a.sl;
     }
     const float mn = fmaxf(m, group_max<64>(s)), by = exp2f(m - mn);
@@ -195,11 +204,21 @@ __device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, cons
     l = l * by + group_sum<64>(p);
 #pragma unroll
     for (int d = 0; d < DH / 64; ++d) o[d] *= by;
-    for (int j = 0; j < min(64, last + 1 - t0); ++j) {
-      const float w = __shfl(p, j, 64);
+    const int n = min(64, last + 1 - t0);
+    for (int j0 = 0; j0 < n; j0 += 16) {   // (16 loads at a time)
+      float x[16][DH / 64];
 #pragma unroll
-      for (int d = 0; d < DH / 64; ++d)
-        o[d] = fmaf(w, bf16_val(v[(int64_t)(t0 + j) * a.v_stride + lane + 64 * d]), o[d]);
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int d = 0; d < DH / 64; ++d)
+          x[j][d] = bf16_val(v[(int64_t)(t0 + min(j0 + j, n - 1)) * a.v_stride + lane + 64 * d]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j0 + j < n) {
+          const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), j0 + j));
+#pragma unroll
+          for (int d = 0; d < DH / 64; ++d) o[d] = fmaf(w, x[j][d], o[d]);
+        }
     }
     bool lost = true;
 #pragma unroll
