@@ -416,6 +416,13 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
   for (; t0 < kend; s ^= 1) step(std::true_type(), of(s), of(s ^ 1));
 
   l += __shfl_xor(l, 32, 64);
+  // A row that sees no key is 0: its weights of 0 have met whatever the others' values hold.
+  const bool none = last < 0;
+  if (none)
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   const int64_t to = (int64_t)(q0 + i) * a.heads + head;
   const int64_t slot = ((int64_t)at * a.kv_heads + kvh) * BM, pto = slot + 32 * wave + l31;
   if (row < rows && joined) {
@@ -427,7 +434,7 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
             f32x4_t{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
     if (half == 0) a.pm[2 * pto] = m, a.pm[2 * pto + 1] = l;
   } else if (row < rows) {
-    const float inv = last < 0 ? 0.0f : 1.0f / l;   // a row that sees no key is 0
+    const float inv = none ? 0.0f : 1.0f / l;
     uint16_t* op = a.out + to * DH + 4 * half;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -436,7 +443,7 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
         *reinterpret_cast<u32x2_t*>(op + 32 * d + 8 * r) =
             u32x2_t{bf16_pair(o[d][4 * r] * inv, o[d][4 * r + 1] * inv),
                     bf16_pair(o[d][4 * r + 2] * inv, o[d][4 * r + 3] * inv)};
-    if (a.lse && half == 0) a.lse[to] = last < 0 ? -INFINITY : 0.69314718f * (m + __log2f(l));
+    if (a.lse && half == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(l));
   }
 
   // An infinity or a NaN among the values of a tile meets weights of 0 in the rows that do
@@ -447,7 +454,7 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       big = __builtin_elementwise_maximum(big, fabsf(o[d][r]));
-  const bool off = row < rows && !(big < INFINITY) && last >= 0;
+  const bool off = row < rows && !(big < INFINITY);
   uint64_t redo = __ballot(off);
   redo = (redo | (redo >> 32)) & 0xFFFFFFFFull;
   if (redo) {
@@ -478,7 +485,9 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 }
 
 // Joins the parts of a tile's rows, where there are several: Dh/4 lanes a row, four channels
-// each, the parts in order.
+// each, the parts in order. Every row there sees a key: the last of the tile more than LEAST,
+// the others at most BM fewer.
+static_assert(LEAST >= BM);
 template <int DH>
 __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
   constexpr int LPR = DH / 4, ROWS = NT / LPR;
@@ -507,11 +516,10 @@ __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
     }
     const int i = row / a.ratio;
     const int64_t to = (int64_t)(s.q0 + i) * a.heads + kvh * a.ratio + row - i * a.ratio;
-    const bool none = i + s.nk - s.nq < 0;
-    const float inv = none ? 0.0f : 1.0f / sum;
+    const float inv = 1.0f / sum;
     *reinterpret_cast<u32x2_t*>(a.out + to * DH + 4 * c) =
         u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
-    if (a.lse && c == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(sum));
+    if (a.lse && c == 0) a.lse[to] = 0.69314718f * (m + __log2f(sum));
   }
 }
 

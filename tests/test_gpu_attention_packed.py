@@ -341,3 +341,39 @@ def test_binding_checks():
     e = ar.attention_packed(Q[:0], K[:0], V[:0], i32([0, 0]), want_lse=True)
     assert e.out.shape == (0, 4, 64) and e.lse.shape == (0, 4)
     assert ar.attention_packed(Q, K, V, i32([0])).out.shape == Q.shape
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("lq,lk", [([40, 3, 200], [10, 2, 70]),
+                                   ([40, 10, 300], [12, 4000, 290])])     # (keys divided)
+def test_rows_without_a_key_beside_infinities(lq, lk, bad, D):
+    """Fewer keys than queries: the first rows see no key and are 0, whatever the values hold that
+    the rows behind them see; those are as without it, but for the channel concerned."""
+    log(f"packed rows without a key beside {bad}, {lq} {lk} x {D}")
+    H, Hk = 4, 2
+    (Q, q), (K, k), (V, v) = problem(31, lq, lk, H, Hk, D)
+    qo, ko = offsets(lq), offsets(lk)
+    for at in (0, 5, -1):                # seen by every row with a key, by some, by the last
+        for b in (0, 2):
+            X, t = V.clone(), at % lk[b]
+            X[ko[b] + t, 1, 9] = bad
+            r = ar.attention_packed(Q, K, X, i32(qo), k_offsets=i32(ko), want_lse=True)
+            got, lse = r.out.double().cpu().numpy(), r.lse.cpu().numpy()
+            none = np.zeros((sum(lq), H), bool)
+            for s in range(3):
+                none[qo[s]:qo[s] + max(0, lq[s] - lk[s])] = True
+            assert none.any() and (got[none] == 0).all() and np.isneginf(lse[none]).all()
+            first = qo[b] + lq[b] - lk[b] + t            # the first row that sees it
+            hit = got[first:qo[b + 1], H // Hk:, 9]
+            assert (np.isnan(hit) if np.isnan(bad) else hit == bad).all()
+            hit[:] = 0.0
+            for s in range(3):
+                rows, cols = slice(qo[s], qo[s + 1]), slice(ko[s], ko[s + 1])
+                o, l, size, mag = oracle_heads(q[rows], k[cols], v[cols], R.causal(lq[s], lk[s]),
+                                               D ** -0.5)
+                if s == b:
+                    o[first - qo[b]:, H // Hk:, 9] = 0.0
+                check(got[rows], o, out_bound(o, size, mag, D, lk[s], P_BITS), f"out {s}")
+                some = ~none[rows]
+                check(lse[rows][some], l[some], lse_bound(l, mag, D, lk[s])[some], f"lse {s}")
