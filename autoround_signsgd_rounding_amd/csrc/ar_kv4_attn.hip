@@ -43,6 +43,7 @@ constexpr int NT = 256;
 constexpr int GRAIN = 128;        // a workgroup's tokens are a multiple of that
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;      // m follows the maximum when that is so far above it
+constexpr float APART = 0x1p28f;   // a reference whose rounding an exponent would feel
 constexpr float W_TOP = 64.0f;    // weight of p = 1 at vs = sv: 2^15 at p = 2^RISE, vs = 2·sv
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -387,7 +388,18 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
   // tile looks once whether any reference has to follow (two long sequences, two groups: 63 us
   // instead of 76).
   constexpr int AT = G <= 2 && (DH == 64 || G * RT < 4) ? G : 1;
+  // A wave with a reference beyond APART rounds its scores before they are compared: half a step
+  // of such a reference, which the product within an fma does not share, is more than 2^x
+  // holds. They are then scaled as they are formed, qs being the power of 2 in it.
+  bool apart = false;
+  const float sl1 = __builtin_amdgcn_frexp_mantf(a.sl);
   float s[RT][8];   // of token t0 + 8·g4 + e
+  auto scale_scores = [&]() {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[t][e] = ldexpf(s[t][e] * sl1, __float_as_int(qs[t]));
+  };
   auto scores = [&](const uint8_t* tile) {
     const float* scale = reinterpret_cast<const float*>(tile + 2 * Tl::CODES);
     float ks[AT][8];
@@ -433,6 +445,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
                                      : fmaf(acc[t][r], ks[g % AT][4 * j + r], s[t][4 * j + r]);
       }
     }
+    if (apart) scale_scores();
   };
   auto weigh = [&](const uint8_t* tile, int t0, int p0, int p1) {
     u32x4_t yv[NB];
@@ -490,7 +503,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     float top[RT], vtop[AT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      top[t] = largest(s[t]) * qs[t];
+      top[t] = largest(s[t]) * (apart ? 1.0f : qs[t]);
       rises |= top[t] > m[t] + RISE;
     }
     if constexpr (AT == G) {
@@ -514,13 +527,22 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
       if constexpr (AT == G)
 #pragma unroll
         for (int g = 0; g < G; ++g) follow(g, vtop[g]);
+      bool beyond = false;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) beyond |= fabsf(m[t]) >= APART && m[t] != NO_MAX;
+      if (!apart && __any(beyond)) {
+        apart = true;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) qs[t] = __int_as_float(__builtin_amdgcn_frexp_expf(qs[t]));
+        scale_scores();
+      }
     }
     float p[RT][8];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], qs[t], -m[t]));
+        p[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], apart ? 1.0f : qs[t], -m[t]));
         l[t] += p[t][e];
       }
 #pragma unroll

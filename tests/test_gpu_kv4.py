@@ -421,3 +421,37 @@ def test_binding_checks():
     assert ar.kv4_read(cache, s[:0])[0].shape == (0, 2, 64)
     none = ar.kv4_attention(Q, cache, t[:, :0].contiguous(), n, want_lse=True)
     assert (none.out == 0).all() and torch.isneginf(none.lse).all()
+
+
+@pytest.mark.parametrize("lengths,new", [([1], 1), ([1, 70, 200], 1), ([3000, 90], 3)])
+@pytest.mark.parametrize("size", [2.0 ** 13, 2.0 ** 17, 2.0 ** 40])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 128)])
+def test_scores_beyond_2_to_28(lengths, new, size, D, group):
+    """Scores so far apart that a row takes one key, or the mean of equal ones."""
+    log(f"kv4 scores of {size}^2, {lengths} {new} x {D}")
+    rng = np.random.default_rng(62)
+    H, heads, P, B = 4, 1, 64, len(lengths)
+    per = [-(-n // P) for n in lengths]
+    cache = ar.kv4_cache(sum(per), heads, D, page_size=P, group_size=group)
+    table, ks, vs = np.full((B, max(per)), -1), [], []
+    for b, n in enumerate(lengths):
+        at = sum(per[:b])
+        table[b, :per[b]] = np.arange(at, at + per[b])
+        level = size * rng.integers(1, 200, n)[:, None, None] * np.ones((1, heads, D))
+        slots = i32(at * P + np.arange(n))
+        ar.kv4_write(bf16(level)[0], bf16(rng.normal(size=(n, heads, D)))[0], cache, slots)
+        k, v = ar.kv4_read(cache, slots, out_dtype=torch.float32)
+        ks.append(k.double().cpu().numpy())
+        vs.append(v.double().cpu().numpy())
+    sign = np.where(np.arange(B * new * H) % 3 == 0, -1.0, 1.0).reshape(B, new, H, 1)
+    Q, q = bf16(size * sign * np.ones(D))
+    got = ar.kv4_attention(Q, cache, i32(table), i32(lengths), want_lse=True)
+    out, lse = got.out.double().cpu().numpy(), got.lse.double().cpu().numpy()
+    for b, n in enumerate(lengths):
+        for h in range(H):
+            o, l, w, _ = R.rows(q[b, :, h], ks[b][:, 0], vs[b][:, 0], R.causal(new, n), D ** -0.5)
+            weight = np.stack([R.rows(q[b, i:i + 1, h], ks[b][:, 0], np.abs(vs[b][:, 0]).max(1)[:, None] / 7,
+                                      R.causal(new, n)[i:i + 1], D ** -0.5)[0][0] for i in range(new)])
+            bound = out_bound(o, w, 0.0 * l, D, n, W_BITS) + 2.0 ** -10 * weight
+            check(out[b, :, h], o, bound, f"out {b} {h}")
+            check(lse[b, :, h], l, np.abs(l) * (D + 8) * 2.0 ** -24 + 1e-3, f"lse {b} {h}")
