@@ -312,6 +312,13 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
   };
   f16x8_t qf[RT][G][KW], qz[RT][G];
   float qs[RT];        // takes a sum of products to the exponent of 2
+  int power[RT];       // that of 2 in it
+  // A wave's scores are scaled as they are formed, qs being only that power of 2, where
+  // - it is far from 1: scale times queries above 2^91 or below 2^-109;
+  // - a row's reference is beyond APART: half a step of it, which the product within an fma does
+  //   not share, is more than 2^x holds, so the scores are rounded before they are compared.
+  bool apart = false;
+  const float sl1 = __builtin_amdgcn_frexp_mantf(a.sl);
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     float x[G][KW][8];
@@ -330,9 +337,9 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     const float big = __uint_as_float(top);
     // (a row with an infinity or a NaN is NaN whatever its other channels become)
-    // (and one below 2^-120 throughout has scores of 0)
-    const int up = top == 0 || top >= 0x7F800000u ? 0 : min(12 - __builtin_amdgcn_frexp_expf(big), 100);
-    qs[t] = fmaxf(ldexpf(a.sl, 21 - up), 0x1p-126f);   // (codes are 2^-21 of themselves)
+    const int up = top == 0 || top >= 0x7F800000u ? 0 : 12 - __builtin_amdgcn_frexp_expf(big);
+    power[t] = __builtin_amdgcn_frexp_expf(a.sl) + 21 - up;   // (codes are 2^-21 of themselves)
+    apart |= abs(power[t]) > 100;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.0f;
@@ -355,6 +362,10 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
       }
     }
   }
+
+  apart = __any(apart);
+#pragma unroll
+  for (int t = 0; t < RT; ++t) qs[t] = apart ? __int_as_float(power[t]) : ldexpf(sl1, power[t]);
 
   // STAGES tiles on their way, and the pages of those that are not yet worked on
   constexpr int STEP = 32 * WAVES, LOADS = Tl::LOADS;
@@ -388,11 +399,6 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
   // tile looks once whether any reference has to follow (two long sequences, two groups: 63 us
   // instead of 76).
   constexpr int AT = G <= 2 && (DH == 64 || G * RT < 4) ? G : 1;
-  // A wave with a reference beyond APART rounds its scores before they are compared: half a step
-  // of such a reference, which the product within an fma does not share, is more than 2^x
-  // holds. They are then scaled as they are formed, qs being the power of 2 in it.
-  bool apart = false;
-  const float sl1 = __builtin_amdgcn_frexp_mantf(a.sl);
   float s[RT][8];   // of token t0 + 8·g4 + e
   auto scale_scores = [&]() {
 #pragma unroll

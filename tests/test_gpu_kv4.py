@@ -455,3 +455,64 @@ def test_scores_beyond_2_to_28(lengths, new, size, D, group):
             bound = out_bound(o, w, 0.0 * l, D, n, W_BITS) + 2.0 ** -10 * weight
             check(out[b, :, h], o, bound, f"out {b} {h}")
             check(lse[b, :, h], l, np.abs(l) * (D + 8) * 2.0 ** -24 + 1e-3, f"lse {b} {h}")
+
+
+def held_by(cache, n):
+    """The first n tokens of a cache in float64."""
+    return (x.double().cpu().numpy() for x in
+            ar.kv4_read(cache, i32(np.arange(n)), out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128)])
+@pytest.mark.parametrize("n", [150, 3000])
+@pytest.mark.parametrize("size", [2.0 ** 118, 1e37, 1.7e38])
+def test_queries_at_the_top_of_their_range(size, n, D, group):
+    """Keys of zeros leave scores of 0 whatever the queries; any other key is far from them."""
+    log(f"kv4 queries of {size}, {n} x {D}")
+    rng = np.random.default_rng(41)
+    heads, H, P = 2, 8, 64
+    pages = -(-n // P)
+    q0 = size * np.clip(rng.normal(size=(1, 1, H, D)), -1, 1)
+    Q, q = bf16(q0)
+    for key in (None, 30, n - 1):
+        cache = ar.kv4_cache(pages, heads, D, page_size=P, group_size=group)
+        x = np.zeros((n, heads, D))
+        if key is not None:     # along the first head's query: its score is the largest by far
+            x[key] = 2e-29 * np.sign(q0[0, 0, 0])
+        K, V = bf16(x)[0], bf16(rng.normal(size=(n, heads, D)))[0]
+        ar.kv4_write(K, V, cache, i32(np.arange(n)))
+        k, v = held_by(cache, n)
+        for scale in (None, 0.5, 2.0 ** 20):
+            got = ar.kv4_attention(Q, cache, i32(np.arange(pages)[None]), i32([n]), want_lse=True,
+                                   scale=scale)
+            out, lse = got.out.double().cpu().numpy()[0, 0], got.lse.cpu().numpy()[0, 0]
+            for h in range(H):
+                s = D ** -0.5 if scale is None else scale
+                o, l, w, mag = R.rows(q[0, :, h], k[:, h // 4], v[:, h // 4], R.causal(1, n), s)
+                # scores of 0 are exact; one that is not is beyond all others or below them by more
+                # than its error (2^-17 of the largest product of a channel)
+                far = s * (k[:, h // 4] @ q[0, 0, h])
+                cut = D * 2.0 ** -17 * np.abs(q[0, 0, h]).max() * s * np.abs(k[:, h // 4]).max()
+                assert key is None or abs(far[key]) > cut + 1000
+                weight = np.abs(v[:, h // 4]).max() / 7
+                bound = out_bound(o, w, np.zeros(1), D, n, W_BITS) + 2.0 ** -10 * weight
+                check(out[h], o[0], bound[0], f"out {key} {h} {scale}")
+                check(lse[h], l[0], lse_bound(l, mag, D, n)[0] + cut, f"lse {key} {h}")
+
+
+@pytest.mark.parametrize("qs,ks_", [(2.0 ** -122, 2.0 ** 120), (2.0 ** -130, 2.0 ** 121),
+                                    (2.0 ** -126, 2.0 ** 119)])
+def test_queries_at_the_bottom_of_their_range(qs, ks_):
+    """Tiny queries, subnormal ones among them, over huge keys."""
+    log(f"kv4 queries of {qs}")
+    rng = np.random.default_rng(42)
+    H, heads, D, P, n = 8, 2, 64, 32, 150
+    cache = ar.kv4_cache(8, heads, D, page_size=P, group_size=32)
+    K, V = bf16(ks_ * rng.normal(size=(n, heads, D)))[0], bf16(rng.normal(size=(n, heads, D)))[0]
+    ar.kv4_write(K, V, cache, i32(np.arange(n)))
+    k, v = held_by(cache, n)
+    Q, q = bf16(qs * rng.normal(size=(1, 1, H, D)))
+    assert np.abs(q).max() > 0
+    for scale in (None, 16.0):
+        got = ar.kv4_attention(Q, cache, i32(np.arange(8)[None]), i32([n]), want_lse=True, scale=scale)
+        compare(got, q, [k], [v], 1, f"tiny {qs}", scale=scale)
