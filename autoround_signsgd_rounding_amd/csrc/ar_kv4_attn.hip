@@ -16,11 +16,12 @@
 // holds one row's scores of eight neighbouring tokens (8·(l/16) .. + 7 of 32, by the choice
 // which token is which row of A), and these are the eight that it supplies to the second
 // product, Oᵀ = Vᵀ·Pᵀ: nothing passes between lanes.
-// The weights of that product are p·vs in f16, relative to sv, the largest vs seen but for a
-// factor of 2: half a step of 2^-11 each, an eighth of what rounding to bf16 would cost, and below
-// 2^-30 of the largest nothing counts. p = 2^(x - m) with a running reference m that follows
-// the maximum only when that has risen by more than 8 (p <= 256); the sums of p and all
-// accumulators are float32.
+// The weights of that product are p·vs in f16, times a power of 2 for each row and group that
+// keeps the largest that the row has met in f16's upper half: half a step of 2^-11 each, an eighth
+// of what rounding to bf16 would cost, and below 2^-30 of the row's largest nothing counts. What a
+// row does not see, or gives no weight, takes no part in that. p = 2^(x - m) with a running
+// reference m, a whole number so that a step of it goes into that power of 2, that follows the
+// maximum only when that has risen by more than 8; the sums of p and all accumulators are float32.
 //
 // Each wave goes through its tokens alone, 32 at a time. A tile goes straight to one of two
 // LDS stages of the wave, and the one after next is asked for as soon as it has been used; no
@@ -43,8 +44,9 @@ constexpr int NT = 256;
 constexpr int GRAIN = 128;        // a workgroup's tokens are a multiple of that
 constexpr float NO_MAX = -3.0e38f;
 constexpr float RISE = 8.0f;      // m follows the maximum when that is so far above it
-constexpr float APART = 0x1p28f;   // a reference whose rounding an exponent would feel
-constexpr float W_TOP = 64.0f;    // weight of p = 1 at vs = sv: 2^15 at p = 2^RISE, vs = 2·sv
+constexpr float APART = 0x1p24f;  // a reference whose rounding 2^x would feel
+constexpr int W_NEW = 7;          // the largest weight when its factor is set is in [2^6, 2^7),
+constexpr float W_MOST = 0x1p15f; // and at most that later
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -216,8 +218,7 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int a
 }
 
 // Waves a SIMD that the registers are held to. (From two on, products stay out of the
-// accumulation registers, which the softmax would have to copy from. At 64 channels in groups of
-// 32 the divided form spills a register, outside its loop.)
+// accumulation registers, which the softmax would have to copy from.)
 constexpr int occupancy(int DH, int G, int RT, int WAVES) {
   return WAVES == 8 || RT == 2 ? 2 : DH == 64 ? 4 : G == 4 ? 2 : 3;
 }
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
   // what the values' zero-points take off, in every element (a group's own, so that a NaN
   // stays within it)
   f32x4_t oz[RT][G];
-  float m[RT], l[RT], sv[G], wk[G];
+  float m[RT], l[RT], wk[RT][G];   // wk: powers of 2
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = NO_MAX;
@@ -390,10 +391,14 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
     for (int d = 0; d < NO; ++d) o[t][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int g = 0; g < G; ++g) oz[t][g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < G; ++g) oz[t][g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, wk[t][g] = 0x1p120f;
   }
+  // o and oz of a row and group times f
+  auto rescale = [&](int t, int g, float f) {
 #pragma unroll
-  for (int g = 0; g < G; ++g) sv[g] = 0x1p-120f, wk[g] = W_TOP * 0x1p120f;
+    for (int d = g * GS / 16; d < (g + 1) * GS / 16; ++d) o[t][d] *= f;
+    oz[t][g] *= f;
+  };
 
   // Groups whose scales are held at once: all of four would take 64 registers; with fewer a
   // tile looks once whether any reference has to follow (two long sequences, two groups: 63 us
@@ -463,79 +468,43 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
     const bool gone = (vtok >= 16 ? p1 : p0) < 0;
     const float* vscale =
         reinterpret_cast<const float*>(tile + 2 * Tl::CODES + Tl::SCALES) + vtok * G;
-    float ys[AT][8], vs[AT][8];
-    auto value_scales = [&](int g) {
-      octet_scales<G, AT>(vscale, g, ys);
+    float ys[AT][8];
+    if constexpr (AT == G) octet_scales<G, AT>(vscale, 0, ys);
+    if (tail)   // some token is hidden from some row
 #pragma unroll
-      for (int i = 0; i < AT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) vs[i][e] = ys[i][e];
-    };
-    auto hide_scales = [&]() {
-#pragma unroll
-      for (int i = 0; i < AT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) vs[i][e] = gone || t0 + vtok + e >= len ? 0.0f : vs[i][e];
-    };
-    if constexpr (AT == G) value_scales(0);
-    if (tail) {   // some token is hidden from some row
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int tok = t0 + vtok + e;
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-          s[t][e] = gone || tok >= sees[t] ? -INFINITY : s[t][e];
-      }
-      if constexpr (AT == G) hide_scales();
-    }
+          s[t][e] = gone || t0 + vtok + e >= sees[t] ? -INFINITY : s[t][e];
     auto largest = [&](const float (&x)[8]) {
       float m = x[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
       return m;
     };
-    auto follow = [&](int g, float top) {   // sv of group g
-      const float sn = fmaxf(sv[g], group_max<64>(top)), by = sv[g] / sn;
-      sv[g] = sn;
-      wk[g] = W_TOP / sn;
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int d = g * GS / 16; d < (g + 1) * GS / 16; ++d) o[t][d] *= by;
-        oz[t][g] *= by;
-      }
-    };
     bool rises = false;
-    float top[RT], vtop[AT];
+    float top[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       top[t] = largest(s[t]) * (apart ? 1.0f : qs[t]);
       rises |= top[t] > m[t] + RISE;
     }
-    if constexpr (AT == G) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        vtop[g] = largest(vs[g]);
-        rises |= vtop[g] > 2.0f * sv[g];
-      }
-    }
     if (__any(rises)) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const float mn = fmaxf(m[t], row_max(top[t])), by = __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        l[t] *= by;
-#pragma unroll
-        for (int d = 0; d < NO; ++d) o[t][d] *= by;
-#pragma unroll
-        for (int g = 0; g < G; ++g) oz[t][g] *= by;
-      }
-      if constexpr (AT == G)
-#pragma unroll
-        for (int g = 0; g < G; ++g) follow(g, vtop[g]);
       bool beyond = false;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) beyond |= fabsf(m[t]) >= APART && m[t] != NO_MAX;
+      for (int t = 0; t < RT; ++t) {
+        const float high = row_max(top[t]), mn = high > m[t] + RISE ? ceilf(high) : m[t];
+        const int by = (int)fmaxf(m[t] - mn, -1000.0f);
+        m[t] = mn;
+        beyond |= fabsf(mn) >= APART && mn != NO_MAX;
+        l[t] = ldexpf(l[t], by);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {   // the sums stay as they are, as long as wk can make up for it
+          const int k = __builtin_amdgcn_frexp_expf(wk[t][g]) - 1 - by, kn = min(k, 120);
+          wk[t][g] = ldexpf(1.0f, kn);
+          rescale(t, g, ldexpf(1.0f, kn - k));
+        }
+      }
       if (!apart && __any(beyond)) {
         apart = true;
 #pragma unroll
@@ -551,34 +520,56 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
         p[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], apart ? 1.0f : qs[t], -m[t]));
         l[t] += p[t][e];
       }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if constexpr (AT < G) {
-        value_scales(g);
-        if (tail) hide_scales();
-        vtop[0] = largest(vs[0]);
-        if (__any(vtop[0] > 2.0f * sv[g])) follow(g, vtop[0]);
-      }
-      // weights p·vs, eight tokens of the lane's row
-      f16x8_t w[RT];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vs[g % AT][e] *= wk[g];
+    // weights p·vs of the groups g .. g + AT - 1, eight tokens of the lane's row
+    float w[RT][AT][8];
+    auto weights = [&](int g) {
+      bool rises = false;
+      float top[RT][AT];
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[t][e] = (_Float16)(p[t][e] * vs[g % AT][e]);
+        for (int i = 0; i < AT; ++i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[t][i][e] = p[t][e] * ys[i][e];
+          top[t][i] = largest(w[t][i]);
+          rises |= top[t][i] * wk[t][g + i] > W_MOST;
+        }
+      if (__any(rises))
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int i = 0; i < AT; ++i) {
+            const float high = row_max(top[t][i]);
+            const int k = __builtin_amdgcn_frexp_expf(wk[t][g + i]) - 1;
+            const int kn = high * wk[t][g + i] > W_MOST ? W_NEW - __builtin_amdgcn_frexp_expf(high) : k;
+            wk[t][g + i] = ldexpf(1.0f, kn);
+            rescale(t, g + i, ldexpf(1.0f, kn - k));
+          }
+    };
+    if constexpr (AT == G) weights(0);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if constexpr (AT < G) {
+        octet_scales<G, AT>(vscale, g, ys);
+        weights(g);
+      }
+      f16x8_t wh[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wh[t][e] = (_Float16)(w[t][g % AT][e] * wk[t][g]);
       if (tail)   // hidden tokens weigh nothing, whatever they hold
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (s[t][e] == -INFINITY) w[t][e] = (_Float16)0.0f;
+            if (s[t][e] == -INFINITY) wh[t][e] = (_Float16)0.0f;
       u32x4_t z;
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[i] = zeros_of(ys[g % AT][2 * i], ys[g % AT][2 * i + 1]);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-        oz[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, z), w[t],
+        oz[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, z), wh[t],
                                                           oz[t][g], 0, 0, 0);
 #pragma unroll
       for (int q = g * GS / 32; q < (g + 1) * GS / 32; ++q) {   // 32 channels each
@@ -592,9 +583,9 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           f32x4_t* d = &o[t][2 * q];
-          d[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, lo), w[t], d[0],
+          d[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, lo), wh[t], d[0],
                                                         0, 0, 0);
-          d[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, hi), w[t], d[1],
+          d[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, hi), wh[t], d[1],
                                                         0, 0, 0);
         }
       }
@@ -633,13 +624,13 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
       for (int q = 0; q < NO / 2; ++q) {
         // (codes are 2^-24 of themselves, those of odd channels 2^-20)
-        const float k = sv[32 * q / GS] * (0x1p24f / W_TOP);
+        const int k = 25 - __builtin_amdgcn_frexp_expf(wk[t][32 * q / GS]);
         const f32x4_t z = oz[t][32 * q / GS], x = o[t][2 * q], y = o[t][2 * q + 1];
 #pragma unroll
         for (int r = 0; r < 4; r += 2)   // channels 32·q + 8·g4 + 2·r ..
           *reinterpret_cast<f32x4_t*>(&so[wave][row][32 * q + 8 * g4 + 2 * r]) =
-              f32x4_t{(x[r] - z[r]) * k, (y[r] * 0.0625f - z[r]) * k, (x[r + 1] - z[r + 1]) * k,
-                      (y[r + 1] * 0.0625f - z[r + 1]) * k};
+              f32x4_t{ldexpf(x[r] - z[r], k), ldexpf(y[r] * 0.0625f - z[r], k),
+                      ldexpf(x[r + 1] - z[r + 1], k), ldexpf(y[r + 1] * 0.0625f - z[r + 1], k)};
       }
     }
   __syncthreads();

@@ -516,3 +516,76 @@ def test_queries_at_the_bottom_of_their_range(qs, ks_):
     for scale in (None, 16.0):
         got = ar.kv4_attention(Q, cache, i32(np.arange(8)[None]), i32([n]), want_lse=True, scale=scale)
         compare(got, q, [k], [v], 1, f"tiny {qs}", scale=scale)
+
+
+def compare_seen(got, q, ks, vs, new, what):
+    """As compare, with bounds of what a row sees only: weights below 2^-30 of its own largest
+    weight times scale may vanish."""
+    B, _, H, D = q.shape
+    out, lse = got.out.double().cpu().numpy().reshape(q.shape), got.lse.cpu().numpy().reshape(B, new, H)
+    for b in range(B):
+        n, r = len(ks[b]), H // ks[b].shape[1]
+        sees = R.causal(new, n)
+        for h in range(H):
+            k, v = ks[b][:, h // r], vs[b][:, h // r]
+            o, l, size, mag = R.rows(q[b, :, h], k, v, sees, D ** -0.5)
+            cut = D * 2.0 ** -17 * np.abs(q[b, :, h]).max(1) * D ** -0.5 * np.abs(k).max() / 7
+            weight = np.stack([R.rows(q[b, i:i + 1, h], k, np.abs(v).max(1)[:, None] / 7,
+                                      sees[i:i + 1], D ** -0.5)[0][0] for i in range(new)])
+            bound = out_bound(o, size, mag, D, n, W_BITS) + size * 2 * np.expm1(cut)[:, None] + \
+                (2.0 ** -10 + n * 2.0 ** -27) * weight
+            check(out[b, :, h], o, bound, f"{what}: out {b} {h}")
+            check(lse[b, :, h], l, lse_bound(l, mag, D, n) + cut, f"{what}: lse {b} {h}")
+
+
+VALUES = [  # lengths, new, heads, key heads, head_dim, page, group, further pages of the table
+    ([90], 5, 4, 2, 64, 16, 32, 0), ([70, 33], 3, 8, 2, 128, 64, 128, 0),
+    ([2500], 4, 8, 1, 128, 64, 64, 0), ([300], 3, 4, 1, 128, 32, 32, 0),
+    ([700], 5, 14, 2, 64, 16, 32, 100), ([400, 90], 8, 8, 1, 128, 64, 128, 3100)]
+
+
+@pytest.mark.parametrize("times", [20, 35, 70, 115])
+@pytest.mark.parametrize("lengths,new,H,heads,D,P,group,more", VALUES)
+def test_large_values_that_some_rows_do_not_see(lengths, new, H, heads, D, P, group, more, times):
+    """The draft's last token has values 2^times times the others'; its earlier rows do not see it."""
+    log(f"kv4 hidden values 2^{times} {lengths} {new} {H}/{heads} x {D} group {group}")
+    rng = np.random.default_rng(times)
+    cache, table, ks, vs = filled(rng, lengths, heads, D, P, group)
+    for b, n in enumerate(lengths):
+        slot = int(table[b, (n - 1) // P]) * P + (n - 1) % P
+        K, V = bf16(keys(rng, 1, heads, D))[0], bf16(2.0 ** times * rng.normal(size=(1, heads, D)))[0]
+        ar.kv4_write(K, V, cache, i32([slot]))
+        for x, y in zip((ks, vs), ar.kv4_read(cache, i32([slot]), out_dtype=torch.float32)):
+            x[b][n - 1] = y[0].double().cpu().numpy()
+    if more:
+        table = torch.cat([table, table[:, -1:].expand(-1, more)], 1).contiguous()
+    Q, q = bf16(1.5 * rng.normal(size=(len(lengths), new, H, D)))
+    got = ar.kv4_attention(Q, cache, table, i32(lengths), want_lse=True)
+    compare_seen(got, q, ks, vs, new, "hidden")
+
+
+@pytest.mark.parametrize("n", [1, 40, 70, 2500])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_large_values_that_weigh_little(n, group):
+    """Tokens of values 2^60 whose weight is about 2^-100, in front of the others and behind
+    them; and all values near 2^118, some of which no row can do without."""
+    log(f"kv4 values that weigh little, {n} group {group}")
+    rng = np.random.default_rng(n)
+    heads, H, D, P = 1, 4, 128, 64
+    pages = -(-n // P)
+    q0 = np.zeros((1, 1, H, D))
+    q0[..., 0] = 8.0                     # scores of a key: its first channel times 8/sqrt(128)
+    Q, q = bf16(q0 + 0.01 * rng.normal(size=q0.shape))
+    for where in ([], [0], [n - 1], [0, n // 2]):
+        x, y = 0.1 * rng.normal(size=(n, heads, D)), rng.normal(size=(n, heads, D))
+        x[:, :, 0] = 0.0
+        x[where, :, 0] = -100.0          # e^-70, 2^-102
+        y[where] *= 2.0 ** 60
+        if not where:
+            y *= 2.0 ** 118
+            x[n // 3, :, 0] = 5.0
+        cache = ar.kv4_cache(pages, heads, D, page_size=P, group_size=group)
+        ar.kv4_write(bf16(x)[0], bf16(y)[0], cache, i32(np.arange(n)))
+        k, v = held_by(cache, n)
+        got = ar.kv4_attention(Q, cache, i32(np.arange(pages)[None]), i32([n]), want_lse=True)
+        compare_seen(got, q, [k], [v], 1, f"little {where}")
