@@ -19,9 +19,9 @@
 // The weights of that product are p·vs in f16, times a power of 2 for each row and group that
 // keeps the largest that the row has met in f16's upper half: half a step of 2^-11 each, an eighth
 // of what rounding to bf16 would cost, and below 2^-30 of the row's largest nothing counts. What a
-// row does not see, or gives no weight, takes no part in that. p = 2^(x - m) with a running
-// reference m, a whole number so that a step of it goes into that power of 2, that follows the
-// maximum only when that has risen by more than 8; the sums of p and all accumulators are float32.
+// row does not see, or gives no weight, takes no part in that. p = 2^(x - m) <= 1 with a running
+// reference m, a whole number so that a step of it goes into that power of 2, that is set 8 above
+// the maximum when that has passed it; the sums of p and all accumulators are float32.
 //
 // Each wave goes through its tokens alone, 32 at a time. A tile goes straight to one of two
 // LDS stages of the wave, and the one after next is asked for as soon as it has been used; no
@@ -43,7 +43,7 @@ namespace {
 constexpr int NT = 256;
 constexpr int GRAIN = 128;        // a workgroup's tokens are a multiple of that
 constexpr float NO_MAX = -3.0e38f;
-constexpr float RISE = 8.0f;      // m follows the maximum when that is so far above it
+constexpr float RISE = 8.0f;      // m lies so far above the maximum when it is set
 constexpr float APART = 0x1p24f;  // a reference whose rounding 2^x would feel
 constexpr int W_NEW = 7;          // the largest weight when its factor is set is in [2^6, 2^7),
 constexpr float W_MOST = 0x1p15f; // and at most that later
@@ -214,7 +214,8 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int a
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees no key is 0
   *reinterpret_cast<u32x2_t*>(a.out + to * DH + c) =
       u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
-  if (a.lse && c == 0) a.lse[to] = sum == 0.0f ? -INFINITY : 0.69314718f * (m + __log2f(sum));
+  if (a.lse && c == 0)
+    a.lse[to] = sum == 0.0f ? -INFINITY : 0.69314718f * (m - RISE + __log2f(ldexpf(sum, (int)RISE)));
 }
 
 // Waves a SIMD that the registers are held to. (From two on, products stay out of the
@@ -487,13 +488,13 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       top[t] = largest(s[t]) * (apart ? 1.0f : qs[t]);
-      rises |= top[t] > m[t] + RISE;
+      rises |= top[t] > m[t];
     }
     if (__any(rises)) {
       bool beyond = false;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const float high = row_max(top[t]), mn = high > m[t] + RISE ? ceilf(high) : m[t];
+        const float high = row_max(top[t]), mn = high > m[t] ? ceilf(high) + RISE : m[t];
         const int by = (int)fmaxf(m[t] - mn, -1000.0f);
         m[t] = mn;
         beyond |= fabsf(mn) >= APART && mn != NO_MAX;

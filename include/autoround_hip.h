@@ -414,7 +414,8 @@ ar_status ar_kv4_attention_workspace_size(const ar_kv4_cache* cache, int64_t B, 
    scale, are rounded to f16, and the matrix unit cuts products off: a score is off by up to
    2^-17 of a key's scale times the largest |q| for each channel, an output by 2^-13 of the
    largest weight times scale of 8 neighbouring tokens for each token, of those that the row sees;
-   what is below 2^-30 of the row's largest weight times scale may be lost. B*new_tokens = 0 is a no-op;
+   what is below 2^-30 of the row's largest weight times scale may be lost, and so may keys of less
+   than 2^-117 of the largest weight. B*new_tokens = 0 is a no-op;
    new_tokens <= 256, B*heads*new_tokens < 2^31, and B*(cache heads)*ceil(rows/16) < 2^23 for
    the new_tokens*heads/(cache heads) rows of a key head. No host synchronisation: the call can
    be captured in a HIP graph and replayed with other lengths and tables. Two calls that may

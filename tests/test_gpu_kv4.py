@@ -589,3 +589,23 @@ def test_large_values_that_weigh_little(n, group):
         k, v = held_by(cache, n)
         got = ar.kv4_attention(Q, cache, i32(np.arange(pages)[None]), i32([n]), want_lse=True)
         compare_seen(got, q, [k], [v], 1, f"little {where}")
+
+
+@pytest.mark.parametrize("n,apart", [(900, 256), (3000, 128)])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128)])
+def test_values_near_the_top(n, apart, D, group):
+    """Values of 2^119 whose weights rise from tile to tile: no sum comes near float32's end."""
+    log(f"kv4 values of 2^119, {n} x {D}")
+    heads, H, P = 2, 4, 64
+    pages = -(-n // P)
+    Q, q = bf16(np.broadcast_to(np.eye(1, D), (1, 1, H, D)))
+    t = np.arange(n)
+    x, y = np.zeros((n, heads, D)), np.full((n, heads, D), 2.0 ** 119)
+    x[:, :, 0] = (t // apart % 2 * 7.5 - (t % 7 != 0) * 12.0)[:, None]
+    y[..., 1::2] *= -1.5
+    cache = ar.kv4_cache(pages, heads, D, page_size=P, group_size=group)
+    ar.kv4_write(bf16(x)[0], bf16(y)[0], cache, i32(t))
+    k, v = held_by(cache, n)
+    scale = 0.6931471805599453
+    got = ar.kv4_attention(Q, cache, i32(np.arange(pages)[None]), i32([n]), want_lse=True, scale=scale)
+    compare(got, q, [k], [v], 1, "top", scale=scale)
