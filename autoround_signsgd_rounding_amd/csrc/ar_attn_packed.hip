@@ -14,8 +14,8 @@
 // the lane's scores 8i .. 8i + 7 are neighbouring tokens, which are the eight that it
 // supplies as the B operand of Oᵀ = Vᵀ·Pᵀ: the weights stay where they are. The A operand
 // there is V transposed, which ds_read_b64_tr_b16 gives out of V as it lies in memory.
-// p = 2^(s - m) with a running reference m that follows the maximum only when that has
-// risen by more than 8; p is rounded to bf16 for the product (2^-9 of each weight, about as
+// p = 2^(s - m) <= 1 with a running reference m, a whole number, that is set 8 above the maximum
+// when that has passed it; p is rounded to bf16 for the product (2^-8 of each weight, about as
 // much in the output as its own rounding to bf16), the sums of p and all accumulators are
 // float32.
 //
@@ -46,7 +46,7 @@ constexpr int PER = 8;       // workgroups that join the parts of a tile (64 tok
                              // 38.6 us; 4 of them 48.7)
 constexpr int MANY = 768;    // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
-constexpr float RISE = 8.0f;   // m follows the maximum when that is so far above it
+constexpr float RISE = 8.0f;   // m lies so far above the maximum when it is set
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -164,6 +164,11 @@ __device__ __forceinline__ bool find_tile(const Args& a, int at, Unit& u) {
   u.part = 0;
   u.before = 0;
   return true;
+}
+
+// ln of the sum of exponentials from the sum l relative to 2^m.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return 0.69314718f * (m - RISE + __log2f(ldexpf(l, (int)RISE)));
 }
 
 __device__ __forceinline__ bool finite_bits(uint32_t pair) {
@@ -355,8 +360,8 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[j][r]);
     top *= a.sl;
-    if (__any(top > m + RISE)) {
-      const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+    if (__any(top > m)) {
+      const float mn = fmaxf(m, ceilf(fmaxf(top, __shfl_xor(top, 32, 64))) + RISE);
       const float by = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= by;
@@ -443,7 +448,7 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
         *reinterpret_cast<u32x2_t*>(op + 32 * d + 8 * r) =
             u32x2_t{bf16_pair(o[d][4 * r] * inv, o[d][4 * r + 1] * inv),
                     bf16_pair(o[d][4 * r + 2] * inv, o[d][4 * r + 3] * inv)};
-    if (a.lse && half == 0) a.lse[to] = none ? -INFINITY : 0.69314718f * (m + __log2f(l));
+    if (a.lse && half == 0) a.lse[to] = none ? -INFINITY : row_lse(m, l);
   }
 
   // An infinity or a NaN among the values of a tile meets weights of 0 in the rows that do
@@ -519,7 +524,7 @@ __global__ __launch_bounds__(NT) void k_attention_join(Args a) {
     const float inv = 1.0f / sum;
     *reinterpret_cast<u32x2_t*>(a.out + to * DH + 4 * c) =
         u32x2_t{bf16_pair(v[0] * inv, v[1] * inv), bf16_pair(v[2] * inv, v[3] * inv)};
-    if (a.lse && c == 0) a.lse[to] = 0.69314718f * (m + __log2f(sum));
+    if (a.lse && c == 0) a.lse[to] = row_lse(m, sum);
   }
 }
 

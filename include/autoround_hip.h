@@ -351,10 +351,10 @@ ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, 
    q_offsets[B]) keep what they held. Contents of the offsets are not checked on the host:
    they are clamped to [0, Tq] and [0, Tk], and with decreasing ones rows of out are
    unspecified, but nothing outside the arrays is read or written. The weights are rounded
-   to bf16 for their product with v. Tq = 0 or B = 0 is a no-op; B <= 65536, Tq and
-   Tk < 2^30, Tq*heads < 2^30, min(B, Tq)*kv_heads < 2^22. No host synchronisation: the call can
-   be captured in a HIP graph and replayed with other offsets. Two calls that may overlap need
-   workspaces of their own. */
+   to bf16 for their product with v, and keys of less than 2^-117 of the largest weight may be
+   lost. Tq = 0 or B = 0 is a no-op; B <= 65536, Tq and Tk < 2^30, Tq*heads < 2^30,
+   min(B, Tq)*kv_heads < 2^22. No host synchronisation: the call can be captured in a HIP graph and
+   replayed with other offsets. Two calls that may overlap need workspaces of their own. */
 ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                               int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
                               int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,

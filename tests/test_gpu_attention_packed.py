@@ -377,3 +377,24 @@ def test_rows_without_a_key_beside_infinities(lq, lk, bad, D):
                 check(got[rows], o, out_bound(o, size, mag, D, lk[s], P_BITS), f"out {s}")
                 some = ~none[rows]
                 check(lse[rows][some], l[some], lse_bound(l, mag, D, lk[s])[some], f"lse {s}")
+
+
+@pytest.mark.parametrize("T", [200, 1000, 3000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_near_the_top(T, D):
+    """Values of 2^120 whose weights rise from tile to tile: no sum comes near float32's end."""
+    log(f"packed values of 2^120, {T} x {D}")
+    H, Hk = 4, 2
+    (Q, _), (K, _), (V, _) = problem(51, [T], [T], H, Hk, D)
+    # one channel of the keys holds the score, in halves of a power of two of the weight
+    Q.zero_()
+    K.zero_()
+    Q[..., 0] = 1.0
+    t = torch.arange(T, device=dev())
+    K[..., 0] = ((t // 64 % 16) * 0.5 - (t % 7 != 0) * 12.0)[:, None].to(torch.bfloat16)
+    V.fill_(2.0 ** 120)
+    V[..., 1::2] *= -1.5
+    q, k, v = (x.double().cpu().numpy() for x in (Q, K, V))
+    scale = 0.6931471805599453
+    r = ar.attention_packed(Q, K, V, i32([0, T]), want_lse=True, scale=scale)
+    verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, [0, T], [0, T], scale, "top")
