@@ -46,6 +46,7 @@ constexpr int PER = 8;       // workgroups that join the parts of a tile (64 tok
                              // 38.6 us; 4 of them 48.7)
 constexpr int MANY = 768;    // workgroups from which on tiles are of 32 keys
 constexpr float NO_MAX = -3.0e38f;
+constexpr float FAR = 0x1p24f;  // a reference whose rounding 2^x would feel
 constexpr float RISE = 8.0f;   // m lies so far above the maximum when it is set
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -176,12 +177,14 @@ __device__ __forceinline__ bool finite_bits(uint32_t pair) {
 }
 
 // One row by the definition over the keys first .. last, by one wave: for a row whose product
-// met an infinity or a NaN of a value hidden from it (0·inf). The lane takes the channels
-// lane, lane + 64 of o. False once all of o is NaN, m and l then being those of the keys so far.
+// met an infinity or a NaN of a value hidden from it (0·inf), or whose reference is beyond FAR
+// (scores are rounded here before they are compared). The lane takes the channels
+// lane, lane + 64 of o. False once all of o is NaN, if `early`, m and l then being those of the
+// keys so far.
 template <int DH>
 __device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, const uint16_t* k,
-                                          const uint16_t* v, int first, int last, float& m, float& l,
-                                          float (&o)[DH / 64]) {
+                                          const uint16_t* v, int first, int last, bool early, float& m,
+                                          float& l, float (&o)[DH / 64]) {
   const int lane = threadIdx.x & 63;
   m = NO_MAX, l = 0.0f;
 #pragma unroll
@@ -228,7 +231,7 @@ __device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, cons
     bool lost = true;
 #pragma unroll
     for (int d = 0; d < DH / 64; ++d) lost = lost && o[d] != o[d];
-    if (__all(lost)) return false;
+    if (early && __all(lost)) return false;
   }
   return true;
 }
@@ -459,33 +462,47 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       big = __builtin_elementwise_maximum(big, fabsf(o[d][r]));
+  // And so are rows with a reference beyond FAR: half a step of it, which the product within
+  // an fma does not share, is more than 2^x holds.
+  const bool far = row < rows && fabsf(m) >= FAR && m != NO_MAX;
   const bool off = row < rows && !(big < INFINITY);
-  uint64_t redo = __ballot(off);
-  redo = (redo | (redo >> 32)) & 0xFFFFFFFFull;
-  if (redo) {
+  auto of_rows = [&](bool x) {   // both halves of the wave hold the row
+    const uint64_t w = __ballot(x);
+    return (w | (w >> 32)) & 0xFFFFFFFFull;
+  };
+  const uint64_t fars = of_rows(far), offs = of_rows(off);
+  uint64_t redo = fars;
+  if (offs & ~fars) {
     bool found = false;   // (keys beyond the wave's rows, and so hidden from some of them)
     for (int t = max(wfirst + 1, kfirst) + lane; t < min(nk, (kend + KT - 1) / KT * KT); t += 64) {
       const uint16_t* vr = vb + (int64_t)t * a.v_stride;
       for (int d = 0; d < DH; d += 2)
         found |= !finite_bits(*reinterpret_cast<const uint32_t*>(vr + d));
     }
+    if (__any(found)) redo |= offs;
+  }
+  if (redo) {
     __threadfence();   // behind the stores above
-    if (__any(found))
-      while (redo) {
-        const int r = __ffsll((unsigned long long)redo) - 1;
-        redo &= redo - 1;
-        const int ri = __shfl(i, r, 64), rh = __shfl(head, r, 64);
-        float rm, rl, ro[DH / 64];
-        const bool all = plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb,
-                                       kfirst, min(ri + nk - nq, kend - 1), rm, rl, ro);
-        const int64_t rto = (int64_t)(q0 + ri) * a.heads + rh;
-        const int64_t rpto = slot + 32 * wave + r;
+    while (redo) {
+      const int r = __ffsll((unsigned long long)redo) - 1;
+      redo &= redo - 1;
+      const int ri = __shfl(i, r, 64), rh = __shfl(head, r, 64);
+      const bool sums = (fars >> r) & 1;   // m and l have to be done again too
+      float rm, rl, ro[DH / 64];
+      const bool all =
+          plain_row<DH>(a, a.q + (int64_t)(q0 + ri) * a.q_stride + rh * DH, kb, vb, kfirst,
+                        min(ri + nk - nq, kend - 1), !sums, rm, rl, ro);
+      const int64_t rto = (int64_t)(q0 + ri) * a.heads + rh;
+      const int64_t rpto = slot + 32 * wave + r;
 #pragma unroll
-        for (int d = 0; d < DH / 64; ++d)
-          if (joined) a.po[rpto * DH + lane + 64 * d] = ro[d];
-          else a.out[rto * DH + lane + 64 * d] = (uint16_t)bf16_bits(ro[d] / rl);
-        if (joined && all && lane == 0) a.pm[2 * rpto] = rm, a.pm[2 * rpto + 1] = rl;
+      for (int d = 0; d < DH / 64; ++d)
+        if (joined) a.po[rpto * DH + lane + 64 * d] = ro[d];
+        else a.out[rto * DH + lane + 64 * d] = (uint16_t)bf16_bits(ro[d] / rl);
+      if (all && lane == 0) {
+        if (joined) a.pm[2 * rpto] = rm, a.pm[2 * rpto + 1] = rl;
+        else if (sums && a.lse) a.lse[rto] = row_lse(rm, rl);
       }
+    }
   }
 }
 

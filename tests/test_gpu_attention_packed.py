@@ -398,3 +398,29 @@ def test_values_near_the_top(T, D):
     scale = 0.6931471805599453
     r = ar.attention_packed(Q, K, V, i32([0, T]), want_lse=True, scale=scale)
     verify(r.out.double().cpu().numpy(), r.lse.cpu().numpy(), q, k, v, [0, T], [0, T], scale, "top")
+
+
+@pytest.mark.parametrize("lq,lk", [([1], [1]), ([3, 70, 200], [3, 70, 200]), ([20, 9], [3000, 90])])
+@pytest.mark.parametrize("size", [2.0 ** 13, 2.0 ** 17, 2.0 ** 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_beyond_2_to_28(lq, lk, size, D):
+    """Scores so far apart that a row takes one key, or the mean of equal ones."""
+    log(f"packed scores of {size}^2, {lq} {lk} x {D}")
+    H, Hk = 4, 2
+    (Q, q), (K, k), (V, v) = problem(61, lq, lk, H, Hk, D)
+    qo, ko = offsets(lq), offsets(lk)
+    # q is size or -size throughout, or as it was; keys are size times a whole number
+    sign = torch.where(torch.arange(sum(lq), device=dev()) % 3 == 0, -1.0, 1.0)
+    Q[:, :3] = (size * sign)[:, None, None].to(torch.bfloat16)
+    level = torch.from_numpy(np.random.default_rng(7).integers(1, 200, sum(lk))).to(dev())
+    K[:] = (size * level)[:, None, None].to(torch.bfloat16)
+    q, k = Q.double().cpu().numpy(), K.double().cpu().numpy()
+    r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True)
+    got, lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+    for b in range(len(lq)):
+        rows, cols = slice(qo[b], qo[b + 1]), slice(ko[b], ko[b + 1])
+        # (scores of a row and a level are equal to the last bit: their sums go the same way)
+        o, l, size_, _ = oracle_heads(q[rows, :3], k[cols][:, [0, 0, 1]], v[cols][:, [0, 0, 1]],
+                                      R.causal(lq[b], lk[b]), D ** -0.5)
+        check(got[rows, :3], o, out_bound(o, size_, 0.0 * l, D, lk[b], P_BITS), f"out {b}")
+        check(lse[rows, :3], l, np.abs(l) * (D + 8) * 2.0 ** -24 + 1e-3, f"lse {b}")
