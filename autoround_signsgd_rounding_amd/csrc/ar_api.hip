@@ -1112,7 +1112,8 @@ ar_status check_heads(int64_t heads, int64_t kv_heads, int64_t head_dim) {
 bool stride_ok(int64_t stride, int64_t row) {
   return stride >= row && stride % 8 == 0 && stride < kMaxLd;
 }
-bool scale_ok(float s) { return finite(s) && s > 0.0f; }
+// (the kernels multiply by scale·log2 e)
+bool scale_ok(float s) { return s > 0.0f && finite((float)((double)s * 1.4426950408889634)); }
 
 // The sizes of a cache; its arrays where `arrays`.
 ar_status check_cache(const ar_kv4_cache* c, bool arrays) {

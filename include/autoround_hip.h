@@ -332,7 +332,7 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
    [tokens, heads, head_dim] with a stride in elements between tokens (a multiple of 8, at
    least heads*head_dim, below 2^22), so they may be parts of one q|k|v product. bf16 unless
    said otherwise; float32 softmax and sums; outputs bf16, contiguous. scale multiplies
-   q·k and must be positive and finite. lse (nullable): the natural logarithm of the row's
+   q·k and must be positive and, times log2(e), a finite float32. lse (nullable): the natural logarithm of the row's
    sum of exponentials, [tokens, heads] float32. A row that sees no key is 0, its lse
    minus infinity. What a row does not see may hold anything, NaN too. Index arrays need
    4-byte alignment, the others 16. */

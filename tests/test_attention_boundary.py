@@ -154,3 +154,12 @@ def test_binding_refuses_on_the_host():
             ar.kv4_cache(**{**dict(pages=4, heads=2, head_dim=128, device="cpu"), **kw})
     assert ar.kv4_cache(4, 2, 64, page_size=16, group_size=32, device="cpu").scale.shape == \
         (4, 2, 2, 16, 2)
+
+
+def test_scales_whose_logarithm_leaves_float32():
+    """scale·log2(e) is what the kernels multiply by: it has to be a float32."""
+    for s in (2.4e38, 3.4028e38):
+        assert packed(scale=s) == attention(scale=s) == INV
+    most = 2.3e38
+    assert packed(Tk=4000, ko=P, scale=most) == WS
+    assert attention(max_len=1 << 20, width=1 << 14, size=0, scale=most) == WS
