@@ -1100,7 +1100,8 @@ namespace {
 constexpr int64_t kMaxI32 = int64_t(1) << 31;
 constexpr int64_t kMaxRatio = 256;   // query heads a key head, and new tokens a sequence
 constexpr int64_t kMaxSeqs = 65536;
-constexpr int64_t kMaxTokens = int64_t(1) << 28;   // written or read in one call
+constexpr int64_t kMaxTokens = ((int64_t(1) << 24) - 1) * 16;   // written or read in one call: 16
+                                                               // a workgroup, below 2^32 threads
 constexpr int64_t kMaxGroups = int64_t(1) << 23;   // workgroups of a launch (below 2^32 threads)
 
 // heads over kv_heads, and a head's width.
@@ -1195,7 +1196,7 @@ ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int
                        void* stream) {
   AR_TRY(check_cache(cache, true));
   if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
-  if (T < 0 || T >= kMaxTokens) return AR_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens) return AR_ERR_SHAPE;
   if (T == 0) return AR_OK;
   const int64_t row = cache->heads * cache->head_dim;
   if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return AR_ERR_SHAPE;
@@ -1208,7 +1209,7 @@ ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T
                       void* k, void* v, void* stream) {
   AR_TRY(check_cache(cache, true));
   if (!dtype_ok(dt)) return AR_ERR_UNSUPPORTED;
-  if (T < 0 || T >= kMaxTokens) return AR_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens) return AR_ERR_SHAPE;
   if (T == 0) return AR_OK;
   if (!k || !v || !slots || !a16(k) || !a16(v) || !a4(slots)) return AR_ERR_INVALID_ARG;
   return ar_launch_kv4_read(*cache, slots, T, dt, k, v, static_cast<hipStream_t>(stream));

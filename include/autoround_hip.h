@@ -387,14 +387,14 @@ typedef struct {
    into slots [T] int32 on the device; tokens whose slot lies outside the cache (-1, say)
    are left out. Where two tokens of one call name the same slot, what that slot then
    holds is unspecified (every other slot is as it should be). T = 0 is a no-op;
-   T < 2^28. */
+   T <= 2^28 - 16. */
 ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int64_t k_stride,
                        const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
                        void* stream);
 
 /* The values held in slots [T] int32 (any number of times each), to k and v [T, cache heads,
    head_dim] of dtype dt, contiguous; zeros for a slot outside the cache. A bf16 output is
-   rounded once. T = 0 is a no-op; T < 2^28. */
+   rounded once. T = 0 is a no-op; T <= 2^28 - 16. */
 ar_status ar_kv4_read(const ar_kv4_cache* cache, const int32_t* slots, int64_t T, int32_t dt,
                       void* k, void* v, void* stream);
 

@@ -163,3 +163,11 @@ def test_scales_whose_logarithm_leaves_float32():
     most = 2.3e38
     assert packed(Tk=4000, ko=P, scale=most) == WS
     assert attention(max_len=1 << 20, width=1 << 14, size=0, scale=most) == WS
+
+
+@pytest.mark.parametrize("f", [write, read])
+def test_tokens_of_one_launch(f):
+    """16 tokens a workgroup of 256 threads: 2^24 workgroups are a thread more than a launch holds."""
+    most = ((1 << 24) - 1) * 16
+    assert f(T=most + 1) == f(T=(1 << 28) - 1) == SHAPE
+    assert f(T=most, k=NULL) == INV     # the size is fine
