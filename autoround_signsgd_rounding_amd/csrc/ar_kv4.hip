@@ -6,8 +6,8 @@
 //   lo = min(x, 0), hi = max(x, 0);   s = max((hi - lo)/15, 2^-100)
 //   zp = clamp(rint(-lo/s), 0, 15);   s' = s with its four lowest bits replaced by zp
 //   code = clamp(rint(x/s') + zp, 0, 15);   value s'·(code - zp)
-// s' is off s by 15·2^-23 at most, 1/70000 of the half step that a code is rounded by,
-// and the codes are those of s': one word a group holds all there is to know.
+// s' is off s by 15·2^-23 of it at most: 15 steps from zero that is 1/18600 of the half step that
+// a code is rounded by. The codes are those of s': one word a group holds all there is to know.
 // A NaN or an infinity in a group (or a range beyond float32) makes s' NaN and with it
 // the group's values; its codes are 0.
 //

@@ -421,8 +421,8 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t z = kv4_zero(scale[(ktok + 4 * j) * G + g]) * 0x00800080u;   // 128·zp, twice
-        // (of the same shape as the products that it is chained to: behind a 16x16x16 one they
-        // took half of its result too early)
+        // (of the same shape as the products that it is chained to: between one of 16x16x16 and
+        // these the compiler puts no wait, and they took half of its result too early)
         const f16x8_t zf = __builtin_bit_cast(f16x8_t, u32x4_t{z, z, z, z});
         f32x4_t acc[RT];
 #pragma unroll
