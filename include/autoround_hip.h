@@ -331,11 +331,11 @@ ar_status ar_fp8_gemm_grouped(const uint8_t* Xq, const float* xs, int64_t T, int
    be a multiple, the quotient at most 256). head_dim is 64 or 128. q, k and v are
    [tokens, heads, head_dim] with a stride in elements between tokens (a multiple of 8, at
    least heads*head_dim, below 2^22), so they may be parts of one q|k|v product. bf16 unless
-   said otherwise; float32 softmax and sums; outputs bf16, contiguous. scale multiplies
-   q·k and must be positive and, times log2(e), a finite float32. lse (nullable): the natural logarithm of the row's
-   sum of exponentials, [tokens, heads] float32. A row that sees no key is 0, its lse
-   minus infinity. What a row does not see may hold anything, NaN too. Index arrays need
-   4-byte alignment, the others 16. */
+   said otherwise; float32 softmax and sums; outputs bf16, contiguous, apart from the inputs and
+   the workspace. scale multiplies q·k and must be positive and, times log2(e), a finite
+   float32. lse (nullable): the natural logarithm of the row's sum of exponentials, [tokens,
+   heads] float32. A row that sees no key is 0, its lse minus infinity. What a row does not see
+   may hold anything, NaN too. Index arrays need 4-byte alignment, the others 16. */
 
 /* Bytes of device workspace of ar_attention_packed. */
 ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,

@@ -609,3 +609,51 @@ def test_values_near_the_top(n, apart, D, group):
     scale = 0.6931471805599453
     got = ar.kv4_attention(Q, cache, i32(np.arange(pages)[None]), i32([n]), want_lse=True, scale=scale)
     compare(got, q, [k], [v], 1, "top", scale=scale)
+
+
+KERNELS = [  # sequences, longest, tokens the table has room for, new, heads, key heads, head_dim, group
+    (3, 900, 3000, 1, 8, 2, 64, 32),        # one tile of rows, divided
+    (3, 900, 3000, 2, 8, 2, 64, 64),
+    (3, 900, 3000, 1, 8, 2, 128, 32),
+    (3, 900, 3000, 1, 8, 2, 128, 64),
+    (3, 900, 3000, 1, 8, 2, 128, 128),
+    (5, 200, 256, 1, 8, 2, 64, 32),         # undivided, four waves
+    (5, 200, 256, 2, 8, 2, 64, 64),
+    (5, 200, 256, 1, 8, 2, 128, 32),
+    (5, 200, 256, 1, 8, 2, 128, 64),
+    (5, 200, 256, 2, 8, 2, 128, 128),
+    (3, 500, 1024, 3, 8, 2, 64, 32),        # undivided, eight waves
+    (3, 500, 1024, 1, 8, 2, 64, 64),
+    (3, 500, 1024, 1, 8, 2, 128, 32),
+    (3, 500, 1024, 3, 8, 2, 128, 64),
+    (3, 500, 1024, 1, 8, 2, 128, 128),
+    (2, 900, 200000, 3, 12, 1, 64, 32),     # two tiles of rows, divided
+    (2, 900, 200000, 3, 12, 1, 64, 64),
+    (2, 900, 200000, 5, 12, 1, 128, 64),
+    (2, 900, 200000, 3, 12, 1, 128, 128),
+    (128, 300, 1024, 3, 24, 4, 64, 32),     # .. undivided
+    (128, 300, 1024, 3, 24, 4, 64, 64),
+    (128, 300, 1024, 5, 24, 4, 128, 64),
+    (128, 300, 1024, 3, 24, 4, 128, 128),
+    (160, 300, 2048, 3, 24, 4, 128, 128),   # of up to 2048 tokens
+    (64, 900, 3000, 2, 16, 4, 64, 32),      # many rows to join
+    (64, 900, 3000, 2, 16, 4, 128, 64),
+    (512, 5000, 5008, 1, 4, 4, 64, 64),     # many sequences: one far longer than the others
+    (512, 5000, 5008, 1, 4, 4, 128, 128),
+]
+
+
+@pytest.mark.parametrize("B,longest,room,new,H,heads,D,group", KERNELS)
+def test_every_kernel(B, longest, room, new, H, heads, D, group):
+    log(f"kv4 every kernel {B} x {longest} of {room} new {new} heads {H}/{heads} x {D} group {group}")
+    rng = np.random.default_rng(B + new)
+    P = 16
+    lengths = [int(x) for x in rng.integers(0, 40, B)]
+    lengths[B // 2] = longest
+    cache, table, ks, vs = filled(rng, lengths, heads, D, P, group)
+    wide = torch.full((B, room // P), -1, dtype=torch.int32, device=dev())
+    n = min(table.shape[1], room // P)
+    wide[:, :n] = table[:, :n]
+    Q, q = bf16(1.5 * rng.normal(size=(B, new, H, D)))
+    got = ar.kv4_attention(Q, cache, wide, i32(lengths), want_lse=True)
+    compare(got, q, ks, vs, new, "every kernel")
