@@ -532,7 +532,10 @@ __global__ __launch_bounds__(64 * WAVES, occupancy(DH, DH / GS, RT, WAVES)) void
         for (int i = 0; i < AT; ++i) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[t][i][e] = p[t][e] * ys[i][e];
-          top[t][i] = largest(w[t][i]);
+          float size[8];   // (a cache's owner may hold scales below 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) size[e] = fabsf(w[t][i][e]);
+          top[t][i] = largest(size);
           rises |= top[t][i] * wk[t][g + i] > W_MOST;
         }
       if (__any(rises))

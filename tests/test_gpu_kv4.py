@@ -657,3 +657,21 @@ def test_every_kernel(B, longest, room, new, H, heads, D, group):
     Q, q = bf16(1.5 * rng.normal(size=(B, new, H, D)))
     got = ar.kv4_attention(Q, cache, wide, i32(lengths), want_lse=True)
     compare(got, q, ks, vs, new, "every kernel")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_scales_of_either_sign(group):
+    """A cache that its owner filled: scales below 0, as large as they come."""
+    log(f"kv4 negative scales, group {group}")
+    rng = np.random.default_rng(71)
+    heads, H, D, P, n = 2, 4, 128, 64, 300
+    for size in (1.0, 1e30):
+        codes = rng.integers(0, 256, (5, 2, heads, P, D // 2)).astype(np.uint8)
+        scale = (rng.uniform(0.01, 0.1, (5, 2, heads, P, D // group)) *
+                 rng.choice([-1.0, 1.0], (5, 2, heads, P, D // group))).astype(F32)
+        scale[:, 1] *= F32(-size)
+        scale[:, 1, 0] = -np.abs(scale[:, 1, 0])        # below 0 throughout
+        k, v = R.held(codes, scale, np.arange(n))
+        Q, q = bf16(rng.normal(size=(1, 1, H, D)))
+        got = ar.kv4_attention(Q, on_gpu((codes, scale)), i32(np.arange(5)[None]), i32([n]), want_lse=True)
+        compare(got, q, [k], [v], 1, f"signs {size}")
