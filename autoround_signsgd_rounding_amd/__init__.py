@@ -33,6 +33,7 @@ EXPORTS = (
     "ar_block_forward", "ar_tune_block", "ar_attention", "ar_tune_step_noalloc",
     "ar_fp8_quant_act", "ar_fp8_quant_weight", "ar_rmsnorm_fp8", "ar_fp8_gemm",
     "ar_fp8_gemm_grouped", "ar_attention_packed_workspace_size", "ar_attention_packed",
+    "ar_attention_packed_f32",
     "ar_kv4_write", "ar_kv4_read", "ar_kv4_attention_workspace_size", "ar_kv4_attention",
 )
 
@@ -164,6 +165,8 @@ def _load():
         "ar_attention_packed_workspace_size": [i64] * 6 + [ctypes.POINTER(sz)],
         "ar_attention_packed": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64,
                                 fl, vp, vp, vp, sz, vp],
+        "ar_attention_packed_f32": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64,
+                                    fl, vp, vp, vp, sz, vp],
         "ar_kv4_write": [kvp, i32, vp, i64, vp, i64, vp, i64, vp],
         "ar_kv4_read": [kvp, vp, i64, i32, vp, vp, vp],
         "ar_kv4_attention_workspace_size": [kvp, i64, i64, i64, i64, ctypes.POINTER(sz)],
@@ -931,20 +934,23 @@ def _attention_outputs(q, out, want_lse, dev):
 
 
 def attention_packed(q, k, v, offsets, *, k_offsets=None, scale=None, want_lse: bool = False,
-                     out=None, workspace=None, stream=None) -> AttentionOutput:
+                     out=None, workspace=None, float32_weights: bool = False,
+                     stream=None) -> AttentionOutput:
     """Causal attention within packed sequences (ar_attention_packed): q [Tq, heads,
     head_dim], k and v [Tk, kv_heads, head_dim] bf16, whose tokens may lie apart (the
     parts of one q|k|v product); offsets [B + 1] int32 on the GPU: sequence b's tokens of q,
     and of k and v unless ``k_offsets`` gives theirs (then a query sees the keys up to its
     own distance from the end). ``scale`` is 1/sqrt(head_dim) by default. Rows of out and
     lse outside the offsets keep what ``out`` held (without ``out`` they hold nothing
-    meaningful)."""
+    meaningful). The weights are rounded to bf16 for their product with v; with
+    ``float32_weights`` (ar_attention_packed_f32) they are not, as in attention."""
     torch = _torch()
     H, Hk, D, dev = _heads_of(q, k, v)
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _elsewhere(stream, q, k, v, offsets, k_offsets, out, workspace):
             return attention_packed(q, k, v, offsets, k_offsets=k_offsets, scale=scale,
-                                    want_lse=want_lse, out=out, workspace=workspace)
+                                    want_lse=want_lse, out=out, workspace=workspace,
+                                    float32_weights=float32_weights)
     bf16 = (torch.bfloat16,)
     qs, ks = _tokens(q, "q", H, D, bf16, dev), _tokens(k, "k", Hk, D, bf16, dev)
     vs, Tq, Tk = _tokens(v, "v", Hk, D, bf16, dev), q.shape[0], k.shape[0]
@@ -963,12 +969,13 @@ def attention_packed(q, k, v, offsets, *, k_offsets=None, scale=None, want_lse: 
     if st:
         _check(st, "ar_attention_packed_workspace_size")
     ws, size, _keep = _scratch(need.value, workspace, dev)
-    st = lib.ar_attention_packed(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, H,
-                                 Hk, D, off, koff, B, D ** -0.5 if scale is None else scale,
-                                 out.data_ptr(), None if lse is None else lse.data_ptr(), ws, size,
-                                 torch._C._cuda_getCurrentRawStream(dev))
+    f = lib.ar_attention_packed_f32 if float32_weights else lib.ar_attention_packed
+    st = f(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, H, Hk, D, off, koff, B,
+           D ** -0.5 if scale is None else scale, out.data_ptr(),
+           None if lse is None else lse.data_ptr(), ws, size,
+           torch._C._cuda_getCurrentRawStream(dev))
     if st:
-        _check(st, "ar_attention_packed")
+        _check(st, f.__name__)
     return AttentionOutput(out, lse)
 
 

@@ -1163,12 +1163,13 @@ ar_status ar_attention_packed_workspace_size(int64_t B, int64_t Tq, int64_t Tk, 
   return AR_OK;
 }
 
-ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
-                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
-                              int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                              const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
-                              float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
-                              void* stream) {
+namespace {
+ar_status attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                           int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                           const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                           float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                           void* stream, bool f32_weights) {
   AR_TRY(check_packed(B, Tq, Tk, heads, kv_heads, head_dim));
   if (!k_offsets && Tq != Tk) return AR_ERR_SHAPE;
   if (!scale_ok(scale)) return AR_ERR_INVALID_ARG;
@@ -1187,8 +1188,29 @@ ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_
   return ar_launch_attention_packed(
       ArAttentionPacked{q, k, v, q_stride, k_stride, v_stride, Tq, Tk, heads, kv_heads, head_dim,
                         q_offsets, k_offsets ? k_offsets : q_offsets, B, scale, out, lse,
-                        static_cast<float*>(ws)},
+                        static_cast<float*>(ws), f32_weights},
       static_cast<hipStream_t>(stream));
+}
+}  // namespace
+
+ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                              int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                              const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                              float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream) {
+  return attention_packed(q, q_stride, k, k_stride, v, v_stride, Tq, Tk, heads, kv_heads, head_dim,
+                          q_offsets, k_offsets, B, scale, out, lse, ws, ws_bytes, stream, false);
+}
+
+ar_status ar_attention_packed_f32(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                  int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                                  int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                                  float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  return attention_packed(q, q_stride, k, k_stride, v, v_stride, Tq, Tk, heads, kv_heads, head_dim,
+                          q_offsets, k_offsets, B, scale, out, lse, ws, ws_bytes, stream, true);
 }
 
 ar_status ar_kv4_write(const ar_kv4_cache* cache, int32_t dt, const void* k, int64_t k_stride,

@@ -16,8 +16,8 @@
 // there is V transposed, which ds_read_b64_tr_b16 gives out of V as it lies in memory.
 // p = 2^(s - m) <= 1 with a running reference m, a whole number, that is set 8 above the maximum
 // when that has passed it; p is rounded to bf16 for the product (2^-8 of each weight, about as
-// much in the output as its own rounding to bf16), the sums of p and all accumulators are
-// float32.
+// much in the output as its own rounding to bf16) or, where the caller asks for float32 weights,
+// taken in three bf16 parts; the sums of p and all accumulators are float32.
 //
 // The matrix unit and what feeds it bound long prompts. Measured, counting the causal half:
 // 16384 tokens, 64 heads of 128 over 8: 3694 us, 1.19 PFLOP/s (a large library product: 1.23),
@@ -241,7 +241,10 @@ __device__ __forceinline__ bool plain_row(const Args& a, const uint16_t* q, cons
 // 8: 3720 us instead of 3887; 4096, 32 over 8: 135 and 146; 3000: 83.1 and 80.8; 2048: 48.8 and
 // 47.8). With 64 channels four workgroups fit anyway (16384 tokens, 32 heads over 8: 1127 us
 // instead of 1100).
-template <int DH, bool PARTS, int KT>
+//
+// SPLIT: parts of a weight, 1 or 3 (16384 tokens, 64 over 8: 6972 us instead of 3923; 8 x 2048, 32
+// heads: 492 and 302).
+template <int DH, bool PARTS, int KT, int SPLIT>
 __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args a) {
   constexpr int C = DH / 8, ROW = 2 * DH;          // 16-byte chunks and bytes of a row
   constexpr int TILE = KT * ROW;                   // bytes of a tile of keys or values
@@ -371,15 +374,21 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[d] *= by;
     }
-    u32x4_t p[KT / 16];
+    u32x4_t p[SPLIT][KT / 16];
 #pragma unroll
     for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], a.sl, -m));
-        const float e1 = __builtin_amdgcn_exp2f(fmaf(s[j][r + 1], a.sl, -m));
+        float e0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], a.sl, -m));
+        float e1 = __builtin_amdgcn_exp2f(fmaf(s[j][r + 1], a.sl, -m));
         l += e0 + e1;
-        p[2 * j + (r >> 3)][(r & 7) >> 1] = bf16_pair(e0, e1);
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i) {
+          const uint32_t w = bf16_pair(e0, e1);
+          p[i][2 * j + (r >> 3)][(r & 7) >> 1] = w;
+          e0 -= __uint_as_float(w << 16);   // exact
+          e1 -= __uint_as_float(w & 0xFFFF0000u);
+        }
       }
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk)
@@ -390,9 +399,11 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
         const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr)(at));
         const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr)(at + 4 * ROW));
         const auto f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f),
-                                                       __builtin_bit_cast(bf16x8_t, p[kk]), o[d],
-                                                       0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                         __builtin_bit_cast(bf16x8_t, p[i][kk]),
+                                                         o[d], 0, 0, 0);
       }
   };
 
@@ -570,19 +581,19 @@ Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t heads, int64_t kv_heads)
   return p;
 }
 
-template <int DH>
+template <int DH, int SPLIT>
 void launch(const Args& a, const Plan& p, hipStream_t st) {
   const dim3 grid((unsigned)p.groups), block(NT);
   if (!p.parts) {
     if constexpr (DH == 128)
       if (p.groups >= MANY) {
-        hipLaunchKernelGGL((k_attention_packed<DH, false, 32>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((k_attention_packed<DH, false, 32, SPLIT>), grid, block, 0, st, a);
         return;
       }
-    hipLaunchKernelGGL((k_attention_packed<DH, false, 64>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((k_attention_packed<DH, false, 64, SPLIT>), grid, block, 0, st, a);
     return;
   }
-  hipLaunchKernelGGL((k_attention_packed<DH, true, 64>), grid, block, 0, st, a);
+  hipLaunchKernelGGL((k_attention_packed<DH, true, 64, SPLIT>), grid, block, 0, st, a);
   hipLaunchKernelGGL((k_attention_join<DH>), dim3((unsigned)(p.tiles * PER)), dim3(NT), 0, st, a);
 }
 
@@ -610,7 +621,7 @@ ar_status ar_launch_attention_packed(const ArAttentionPacked& g, hipStream_t st)
   a.po = g.ws;
   a.groups = p.groups;
   a.pm = g.ws + p.groups * BM * g.head_dim;
-  if (g.head_dim == 64) launch<64>(a, p, st);
-  else launch<128>(a, p, st);
+  if (g.head_dim == 64) g.f32_weights ? launch<64, 3>(a, p, st) : launch<64, 1>(a, p, st);
+  else g.f32_weights ? launch<128, 3>(a, p, st) : launch<128, 1>(a, p, st);
   return last_status();
 }

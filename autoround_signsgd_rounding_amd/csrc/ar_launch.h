@@ -267,6 +267,7 @@ struct ArAttentionPacked {
   uint16_t* out;
   float* lse;
   float* ws;
+  bool f32_weights;   // not rounded to bf16 for their product with v
 };
 int64_t ar_attention_packed_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t heads,
                                    int64_t kv_heads, int64_t head_dim);

@@ -362,6 +362,15 @@ ar_status ar_attention_packed(const uint16_t* q, int64_t q_stride, const uint16_
                               float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                               void* stream);
 
+/* The same, same workspace, with float32 weights in their product with v (three bf16 parts), as
+   ar_attention has them, at up to twice the time. */
+ar_status ar_attention_packed_f32(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                  int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t Tq,
+                                  int64_t Tk, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
+                                  float scale, uint16_t* out, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* A cache of pages of page_size tokens (16, 32, 64, 128 or 256). Slot p*page_size + t is
    token t of page p. Per token, head and group of group_size channels (32, 64 or 128, a
    divisor of head_dim), for keys and for values, in float32, each step rounded once:

@@ -171,3 +171,17 @@ def test_tokens_of_one_launch(f):
     most = ((1 << 24) - 1) * 16
     assert f(T=most + 1) == f(T=(1 << 28) - 1) == SHAPE
     assert f(T=most, k=NULL) == INV     # the size is fine
+
+
+def test_packed_f32_validation():
+    """The form with float32 weights refuses what the other does."""
+    def f(**kw):
+        a = dict(q=P, qs=1024, k=P, ks=256, v=P, vs=256, Tq=4, Tk=4, H=8, Hk=2, D=128, qo=P, ko=NULL,
+                 B=1, scale=0.1, out=P, lse=NULL, ws=NULL, size=0)
+        a.update(kw)
+        return ar.lib.ar_attention_packed_f32(*a.values(), NULL)
+    assert f(D=96, qs=768) == UNSUP
+    assert f(H=7) == f(Tk=5) == f(qs=1016) == f(ks=252) == f(B=65537) == SHAPE
+    assert f(q=NULL) == f(v=P4) == f(out=NULL) == f(scale=0.0) == f(qo=P2) == INV
+    assert f(Tk=4000, ko=P) == WS
+    assert f(Tq=0, Tk=0) == f(B=0) == OK

@@ -424,3 +424,69 @@ def test_scores_beyond_2_to_28(lq, lk, size, D):
                                       R.causal(lq[b], lk[b]), D ** -0.5)
         check(got[rows, :3], o, out_bound(o, size_, 0.0 * l, D, lk[b], P_BITS), f"out {b}")
         check(lse[rows, :3], l, np.abs(l) * (D + 8) * 2.0 ** -24 + 1e-3, f"lse {b}")
+
+
+F32_CASES = [  # queries, keys, heads, key heads, head_dim
+    ([1], [1], 2, 1, 64), ([130, 1, 37], [130, 1, 37], 6, 2, 128), ([700], [700], 3, 1, 64),
+    ([40, 3, 100], [10, 0, 99], 4, 2, 128), ([3, 20], [5000, 2777], 8, 2, 128),     # (keys divided)
+    ([5, 17], [4000, 90], 4, 2, 64), ([600, 33, 500], [600, 33, 500], 64, 32, 128)]
+
+
+@pytest.mark.parametrize("lq,lk,H,Hk,D", F32_CASES)
+def test_float32_weights(lq, lk, H, Hk, D):
+    """Weights in three bf16 parts: 2^-24 of each, and three sums for each key."""
+    log(f"packed float32 weights {lq} {lk} heads {H}/{Hk} x {D}")
+    (Q, q), (K, k), (V, v) = problem(sum(lq) + H, lq, lk, H, Hk, D)
+    qo, ko = offsets(lq), offsets(lk)
+    r = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True, float32_weights=True)
+    got, lse = r.out.double().cpu().numpy(), r.lse.cpu().numpy()
+    plain = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), want_lse=True)
+    assert torch.equal(plain.lse, r.lse)
+    worse = plain.out.double().cpu().numpy()
+    for b in range(len(lq)):
+        rows, cols = slice(qo[b], qo[b + 1]), slice(ko[b], ko[b + 1])
+        o, l, size, mag = oracle_heads(q[rows], k[cols], v[cols], R.causal(lq[b], lk[b]), D ** -0.5)
+        check(got[rows], o, out_bound(o, size, mag, D, 2 * lk[b], 2.0 ** -24), f"f32 weights: out {b}")
+        assert (got[rows][np.isneginf(l)] == 0).all() and (np.isneginf(lse[rows]) == np.isneginf(l)).all()
+        if lk[b] >= 500:        # what rounding the output alone costs
+            error = lambda x: np.linalg.norm(x[rows] - o) / np.linalg.norm(o)       # noqa: E731
+            assert error(got) <= 2.0 ** -9 and error(got) < error(worse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    again = ar.attention_packed(Q, K, V, i32(qo), k_offsets=i32(ko), float32_weights=True, stream=s)
+    s.synchronize()
+    assert torch.equal(again.out, r.out)
+
+
+@pytest.mark.parametrize("bad", [np.nan, -np.inf])
+def test_float32_weights_and_hidden_infinities(bad):
+    """Values that a row does not see, with float32 weights as without; and scores far apart."""
+    log(f"packed float32 weights, hidden {bad}")
+    lq, H, Hk, D = [70, 130], 4, 2, 128
+    (Q, q), (K, k), (V, v) = problem(8, lq, lq, H, Hk, D)
+    V[199, 0, 0] = bad
+    Q[30:60] *= 2.0 ** 20
+    q = Q.double().cpu().numpy()
+    r = ar.attention_packed(Q, K, V, i32([0, 70, 200]), want_lse=True, float32_weights=True)
+    got = r.out.double().cpu().numpy()
+    for rows, n in ((slice(0, 30), 70), (slice(70, 199), 130)):
+        cols = slice(rows.start, rows.start + n)
+        o, _, size, mag = oracle_heads(q[cols], k[cols], v[cols], R.causal(n, n), D ** -0.5)
+        m = rows.stop - rows.start
+        check(got[rows], o[:m], out_bound(o, size, mag, D, 2 * n, 2.0 ** -24)[:m], f"{rows}")
+    assert torch.isfinite(r.out[30:60]).all() and torch.isfinite(r.lse).all()
+    assert not torch.isfinite(r.out[199, 0, 0]) and torch.isfinite(r.out[199, 0, 1:]).all()
+
+
+def test_float32_weights_equal_the_blocks_attention():
+    """ar_attention's case: the same float32 values but for their sums' order, rounded to bf16."""
+    log("packed float32 weights beside ar_attention")
+    H, D, S, B = 4, 128, 200, 3
+    (Q, _), (K, _), (V, _) = problem(6, [S] * B, [S] * B, H, H, D)
+    dims = ar.block_dims(H * D, H, 64, S, B)
+    flat = [x.reshape(S * B, H * D).contiguous() for x in (Q, K, V)]
+    want = ar.attention(*flat, dims).view(S * B, H, D).double()
+    got = ar.attention_packed(Q, K, V, i32(offsets([S] * B)), float32_weights=True).out.double()
+    # one step of bf16 apart at most, beside 1e-4 of the largest value for scores and sums
+    assert ((got - want).abs() <= 2.0 ** -7 * want.abs() + 1e-4 * V.double().abs().max()).all()
+    assert ((got - want).norm() / want.norm()).item() <= 2.0 ** -12
