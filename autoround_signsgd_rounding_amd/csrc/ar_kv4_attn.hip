@@ -30,9 +30,10 @@
 // from their lengths, on the device: every workgroup makes the same plan.
 //
 // Measured: 2 x 131072 tokens, 64 heads over 8 of 128, groups of 64 (302 MB) 63 us, 4.8 TB/s;
-// 64 x 8192, groups of 128 (570 MB) 103 us, 5.5 TB/s; 64 x up to 8192 (123 MB) 39 us, 3.2 TB/s,
+// 64 x 8192, groups of 128 (570 MB) 107 us, 5.3 TB/s; 64 x up to 8192 (123 MB) 38 us, 3.2 TB/s,
 // where plan, joins and the last workgroups' ends are a third; one sequence of 1000 tokens,
-// 32 heads, 10 us, a chain of launch, lengths, table, tiles and joins with nothing to hide it under.
+// 32 heads, 9.8 us, a chain of launch, lengths, table, tiles and joins with nothing to hide it
+// under.
 #include <math.h>
 
 #include "ar_kv4.h"
@@ -719,25 +720,27 @@ struct Plan {
 };
 Plan plan_of(int64_t B, int64_t heads, int DH, int GS, int64_t rows, int64_t max_len) {
   Plan p;
-  // 512 workgroups run at once (2 x 131072 tokens: 63.2 us; 256 wanted 80.5, 1024 70.9), of
+  // 512 workgroups run at once (2 x 131072 tokens: 62.8 us; 256 wanted 80.0, 1024 70.7), of
   // 256 tokens at least (1 x 2000: 10.3; of 512 11.8, of 128 10.0)
   p.least = 256;
   p.target = 9;
   // Up to 1024 tokens, eight waves of four tiles each are done before a join would be, unless
-  // there are many (8 x 900 tokens, 8 key heads: 9.8 us, divided 10.7; 1 x 2000: 13.7, divided
-  // 10.3; 64 x 900: 17.5 and 18.8).
+  // there are many (8 x 900 tokens, 8 key heads: 9.9 us, divided 10.7; 1 x 2000: 13.7, divided
+  // 10.3; 64 x 900: 17.4 and 18.7). (Their sequences are not divided: see `whole`.)
   p.wide = B * heads * ((rows + 15) / 16) <= 512 && max_len > 256 && max_len <= 1024;
   // Two tiles of rows halve what each token's codes cost, where there is enough of that (8 key
-  // heads, 32 rows; 8 x 8192 tokens: 29.9 us instead of 33.2; 64 x 1200: 36.0 and 43.1), and the
-  // time of a single workgroup counts where there is not (2 x 8192: 22.1 instead of 18.0;
-  // 32 x 1500: 15.8 and 15.6). Those of four groups do not fit.
+  // heads, 32 rows; 8 x 8192 tokens: 29.9 us instead of 32.6; 64 x 1200: 30.4 and 33.6), and the
+  // time of a single workgroup counts where there is not (2 x 8192: 22.0 instead of 17.7; just
+  // at the border 32 x 1500: 26.1 and 24.8). Those of four groups do not fit.
   p.RT = !p.wide && rows > 16 && DH / GS < 4 && B * heads * max_len >= 3 << 17 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   const int64_t per = heads * p.tiles;
   // Undivided, a call has neither plan nor join; what that saves is lost where few workgroups wait
-  // for a long one. (7 query heads a key head; 150 x up to 960 tokens, 4 key heads: 13.5 us,
-  // divided 19.7; 100 x 1000, 8: 28.7 and 31.6. 200 x up to 2000, 4: 23.1 and 24.3; 100 x 2000, 8:
-  // 50.1 and 53.4. 150 x up to 4000, 8: 46.2 and 44.0; 240: 67.1 and 71.3.)
+  // for a long one. (7 query heads a key head; 150 x up to 960 tokens, 4 key heads: 13.4 us,
+  // divided 17.1; 100 x 1000, 8: 28.6 and 31.7. 200 x up to 2000, 4: 23.0 either way; 100 x 2000, 8:
+  // 49.5 and 52.8. 150 x up to 4000, 8: 46.2 and 43.0; 240: 66.5 and 69.2.) The rule for very many
+  // is not borne out beyond such lengths: 255 x 1000 tokens and one of 131072, 8 key heads, take 889
+  // us, and 101 with one sequence fewer, divided.
   const int64_t units = B * per;
   p.whole = max_len <= (units > 512 ? 2048 : 1024) || units >= int64_t(4) << p.target;
   p.groups = (B + (p.whole ? 0 : ((int64_t(1) << p.target) + per - 1) / per)) * per;
@@ -765,9 +768,9 @@ void launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
 template <int DH>
 void join(const AttnArgs& a, const Plan& p, hipStream_t st) {
   constexpr int ALL = NT / (DH / 4);
-  // one group a row where there are many rows (32 x up to 8192 tokens, 64 rows: 38.9 us and
-  // 41.0 by all groups; 150 x up to 4000: 46.5 and 55.6), all of them for the many parts of
-  // few rows (2 x 30000 tokens: 24.2 us and 27.2 by one)
+  // one group a row where there are many rows (64 x 1200 tokens, 32 rows a key head: 30.4 us and
+  // 34.6 by all groups; 150 x up to 4000, 7: 43.0 and 45.4), all of them for the many parts of
+  // few rows (2 x 30000 tokens: 21.1 us and 23.8 by one)
   const int64_t units = (int64_t)a.B * a.c.heads;
   if (units * a.rows >= 2048)
     hipLaunchKernelGGL((k_kv4_join<DH, 1>), dim3((unsigned)(units * ((a.rows + ALL - 1) / ALL))),
