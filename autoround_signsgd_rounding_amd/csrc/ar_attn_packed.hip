@@ -474,8 +474,8 @@ __global__ __launch_bounds__(NT, KT == 32 ? 3 : 2) void k_attention_packed(Args 
     for (int r = 0; r < 16; ++r)
       big = __builtin_elementwise_maximum(big, fabsf(o[d][r]));
   // And so are rows with a reference beyond FAR: half a step of it, which the product within
-  // an fma does not share, is more than 2^x holds.
-  const bool far = row < rows && fabsf(m) >= FAR && m != NO_MAX;
+  // an fma does not share, is more than 2^x holds. (An infinite one has made NaN of its row.)
+  const bool far = row < rows && fabsf(m) >= FAR && m != NO_MAX && m != INFINITY;
   const bool off = row < rows && !(big < INFINITY);
   auto of_rows = [&](bool x) {   // both halves of the wave hold the row
     const uint64_t w = __ballot(x);
